@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "fp8bs.h"
@@ -65,6 +66,62 @@ fp8bs_status check_scales(const float* p, int64_t cols, int64_t ld) {
   if (p == nullptr) return FP8BS_ERR_INVALID_ARG;
   if (ld < cols) return FP8BS_ERR_INVALID_ARG;
   if (!aligned(p, 4)) return FP8BS_ERR_MISALIGNED;
+  return FP8BS_OK;
+}
+
+// Attention limits: heads, head dims of the rotation, and what a 32-bit
+// position, row or page number reaches.
+constexpr int64_t kMaxHeads = int64_t(1) << 16;
+constexpr int64_t kMaxHeadDim = 512;
+constexpr int64_t kMaxInt32 = 0x7fffffff;
+
+fp8bs_status check_rotation(int64_t rot, int64_t off, fp8bs_rope_layout layout, int64_t D) {
+  if (layout != FP8BS_ROPE_HALF && layout != FP8BS_ROPE_INTERLEAVED) return FP8BS_ERR_INVALID_ARG;
+  if (rot <= 0 || off < 0) return FP8BS_ERR_INVALID_ARG;
+  if (D % 16 != 0 || D > kMaxHeadDim || rot % 16 != 0 || off % 8 != 0 || off > D - rot)
+    return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_table(const float* cs, int64_t n_pos) {
+  if (cs == nullptr || n_pos <= 0 || n_pos > kMaxInt32) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(cs, 16)) return FP8BS_ERR_MISALIGNED;
+  return FP8BS_OK;
+}
+
+// Packed rows of a batch.
+fp8bs_status check_packing(const int32_t* q_off, int64_t B, int64_t T, int64_t max_q) {
+  if (B < 0 || T < 0 || max_q < 0) return FP8BS_ERR_INVALID_ARG;
+  if (B > kMaxInt32 || T > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && B > 0 && max_q == 0) return FP8BS_ERR_INVALID_ARG;
+  if (q_off == nullptr && T != B) return FP8BS_ERR_INVALID_ARG;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_heads(int64_t Hq, int64_t Hkv) {
+  if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return FP8BS_ERR_INVALID_ARG;
+  if (Hq > kMaxHeads || Hq / Hkv > 1024) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_cache_shape(int64_t D, int64_t page, int64_t max_pages, int64_t n_pages) {
+  if (D <= 0 || page <= 0 || max_pages <= 0 || n_pages <= 0) return FP8BS_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  // positions are 32-bit, page numbers too
+  if (max_pages > kMaxInt32 / page || n_pages > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_cache(const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int64_t ldt,
+                         int64_t max_pages, const uint8_t* kc, const float* ks, const uint8_t* vc,
+                         const float* vs) {
+  if (kv_len == nullptr || table == nullptr || kc == nullptr || ks == nullptr || vc == nullptr || vs == nullptr)
+    return FP8BS_ERR_INVALID_ARG;
+  if (ldt < max_pages) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(q_off, 4) || !aligned(kv_len, 4) || !aligned(table, 4) || !aligned(ks, 4) || !aligned(vs, 4) ||
+      !aligned(kc, 16) || !aligned(vc, 16))
+    return FP8BS_ERR_MISALIGNED;
   return FP8BS_OK;
 }
 
@@ -347,6 +404,162 @@ fp8bs_status fp8bs_grouped_gemm(const uint8_t* a, const float* sa, int64_t ldsa,
   return launched(fp8bs::launch_grouped_gemm(a, sa, ldsa, b, sb, offsets, E, M_total, d,
                                              dt == FP8BS_OUT_F32, N, K,
                                              static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_rope_table(float* cs, int64_t n_pos, int64_t rot, double base, double factor,
+                              double orig_len, double turns_lo, double turns_hi, double mscale,
+                              void* stream) {
+  if (n_pos < 0 || rot <= 0) return FP8BS_ERR_INVALID_ARG;
+  if (!(base > 0.0 && factor > 0.0 && orig_len >= 0.0) || !std::isfinite(base) || !std::isfinite(factor) ||
+      !std::isfinite(orig_len) || !std::isfinite(mscale))
+    return FP8BS_ERR_INVALID_ARG;
+  if (orig_len > 0.0 && !(turns_hi > turns_lo && std::isfinite(turns_hi) && std::isfinite(turns_lo)))
+    return FP8BS_ERR_INVALID_ARG;
+  if (rot % 16 != 0 || rot > kMaxHeadDim) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (n_pos > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (n_pos == 0) return FP8BS_OK;
+  if (cs == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(cs, 16)) return FP8BS_ERR_MISALIGNED;
+  FP8BS_TRY(check_device());
+  return launched(fp8bs::launch_rope_table(cs, n_pos, rot, base, factor, orig_len, turns_lo, turns_hi, mscale,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_rope(const void* x, int64_t ldx, void* y, int64_t ldy, const int32_t* pos, int64_t T,
+                        int64_t H, int64_t D, int64_t rot, int64_t rot_off, fp8bs_rope_layout layout,
+                        int inverse, const float* cs, int64_t n_pos, void* stream) {
+  if (T < 0 || H <= 0 || D <= 0) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_rotation(rot, rot_off, layout, D));
+  if (H > kMaxHeads) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  FP8BS_TRY(check_matrix(x, H * D, ldx, 2));
+  FP8BS_TRY(check_matrix(y, H * D, ldy, 2));
+  if (x == y && ldx != ldy) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_table(cs, n_pos));
+  if (pos == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(pos, 4)) return FP8BS_ERR_MISALIGNED;
+  FP8BS_TRY(check_device());
+  return launched(fp8bs::launch_rope(static_cast<const uint16_t*>(x), ldx, static_cast<uint16_t*>(y), ldy, pos, T,
+                                     static_cast<int>(H), static_cast<int>(D), static_cast<int>(rot),
+                                     static_cast<int>(rot_off), layout == FP8BS_ROPE_INTERLEAVED, inverse != 0, cs,
+                                     n_pos, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ldqo, int64_t Hq,
+                             const void* k, int64_t ldk, const void* v, int64_t ldv, int64_t Hkv, int64_t D,
+                             const float* cs, int64_t n_pos, int64_t rot, int64_t rot_off,
+                             fp8bs_rope_layout layout, const int32_t* q_off, const int32_t* kv_len, int64_t B,
+                             int64_t T, int64_t max_q, const int32_t* table, int64_t ldt, int64_t max_pages,
+                             int64_t page, uint8_t* kc, float* ks, uint8_t* vc, float* vs, int64_t n_pages,
+                             void* stream) {
+  if (Hkv <= 0 || (q != nullptr && Hq <= 0)) return FP8BS_ERR_INVALID_ARG;
+  if (q != nullptr && cs == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (Hkv > kMaxHeads || Hq > kMaxHeads) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (cs != nullptr) FP8BS_TRY(check_rotation(rot, rot_off, layout, D));
+  FP8BS_TRY(check_packing(q_off, B, T, max_q));
+  FP8BS_TRY(check_cache_shape(D, page, max_pages, n_pages));
+  if (T == 0 || B == 0) return FP8BS_OK;
+  FP8BS_TRY(check_matrix(k, Hkv * D, ldk, 2));
+  FP8BS_TRY(check_matrix(v, Hkv * D, ldv, 2));
+  if (q != nullptr) {
+    FP8BS_TRY(check_matrix(q, Hq * D, ldq, 2));
+    FP8BS_TRY(check_matrix(q_out, Hq * D, ldqo, 2));
+  }
+  if (cs != nullptr) FP8BS_TRY(check_table(cs, n_pos));
+  FP8BS_TRY(check_cache(q_off, kv_len, table, ldt, max_pages, kc, ks, vc, vs));
+  FP8BS_TRY(check_device());
+  fp8bs::KvAppend p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.ldq = ldq;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.ldqo = ldqo;
+  p.Hq = static_cast<int>(q != nullptr ? Hq : 0);
+  p.k = static_cast<const uint16_t*>(k);
+  p.ldk = ldk;
+  p.v = static_cast<const uint16_t*>(v);
+  p.ldv = ldv;
+  p.Hkv = static_cast<int>(Hkv);
+  p.D = static_cast<int>(D);
+  p.cs = cs;
+  p.n_pos = n_pos;
+  p.rot = static_cast<int>(cs != nullptr ? rot : 0);
+  p.rot_off = static_cast<int>(cs != nullptr ? rot_off : 0);
+  p.interleaved = layout == FP8BS_ROPE_INTERLEAVED;
+  p.q_off = q_off;
+  p.kv_len = kv_len;
+  p.B = static_cast<int>(B);
+  p.T = T;
+  p.max_q = max_q;
+  p.table = table;
+  p.ldt = ldt;
+  p.max_pages = max_pages;
+  p.page = static_cast<int>(page);
+  p.kc = kc;
+  p.ks = ks;
+  p.vc = vc;
+  p.vs = vs;
+  p.n_pages = n_pages;
+  return launched(fp8bs::launch_kv_append(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                            int64_t max_pages, int64_t page) {
+  if (check_heads(Hq, Hkv) != FP8BS_OK || check_packing(nullptr, B, B, max_q) != FP8BS_OK || T < 0 ||
+      T > kMaxInt32 || check_cache_shape(D, page, max_pages, 1) != FP8BS_OK)
+    return -1;
+  if (T == 0 || B == 0) return 0;
+  return fp8bs::attn_paged_ws(B, T, max_q, static_cast<int>(Hq), static_cast<int>(Hkv), static_cast<int>(D),
+                              max_pages, static_cast<int>(page));
+}
+
+fp8bs_status fp8bs_attn_paged(const void* q, int64_t ldq, void* out, int64_t ldo, float* lse, int64_t ldl,
+                              const int32_t* q_off, const int32_t* kv_len, int64_t B, int64_t T, int64_t max_q,
+                              int64_t Hq, int64_t Hkv, int64_t D, const int32_t* table, int64_t ldt,
+                              int64_t max_pages, int64_t page, const uint8_t* kc, const float* ks,
+                              const uint8_t* vc, const float* vs, int64_t n_pages, float scale, int causal,
+                              int64_t window, void* ws, int64_t ws_bytes, void* stream) {
+  FP8BS_TRY(check_heads(Hq, Hkv));
+  if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_packing(q_off, B, T, max_q));
+  FP8BS_TRY(check_cache_shape(D, page, max_pages, n_pages));
+  if (T == 0 || B == 0) return FP8BS_OK;
+  FP8BS_TRY(check_matrix(q, Hq * D, ldq, 2));
+  FP8BS_TRY(check_matrix(out, Hq * D, ldo, 2));
+  if (lse != nullptr) FP8BS_TRY(check_scales(lse, Hq, ldl));
+  FP8BS_TRY(check_cache(q_off, kv_len, table, ldt, max_pages, kc, ks, vc, vs));
+  const int64_t need = fp8bs_attn_paged_ws(B, T, max_q, Hq, Hkv, D, max_pages, page);
+  if (ws_bytes < need || (need > 0 && ws == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(ws, 16)) return FP8BS_ERR_MISALIGNED;
+  FP8BS_TRY(check_device());
+  fp8bs::AttnPaged p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.ldq = ldq;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  p.lse = lse;
+  p.ldl = ldl;
+  p.q_off = q_off;
+  p.kv_len = kv_len;
+  p.B = static_cast<int>(B);
+  p.T = T;
+  p.max_q = max_q;
+  p.Hq = static_cast<int>(Hq);
+  p.Hkv = static_cast<int>(Hkv);
+  p.D = static_cast<int>(D);
+  p.table = table;
+  p.ldt = ldt;
+  p.max_pages = max_pages;
+  p.page = static_cast<int>(page);
+  p.kc = kc;
+  p.ks = ks;
+  p.vc = vc;
+  p.vs = vs;
+  p.n_pages = n_pages;
+  p.scale = scale;
+  p.causal = causal != 0;
+  p.window = window;
+  p.ws = ws;
+  return launched(fp8bs::launch_attn_paged(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

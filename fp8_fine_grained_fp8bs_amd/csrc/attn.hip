@@ -1,0 +1,482 @@
+// attn.hip -- attention over the paged E4M3 cache: few rows a key/value head
+// (decoding), and the joining of partial results (gfx950).
+//
+// For few rows the call reads len * 2 D bytes of cache a key/value head and
+// does 4 D operations a byte pair and row: HBM-bound, so the kernel is built
+// around loads in flight.  A wave takes steps of 32 keys, its loads going
+// straight from the cache to registers (no LDS, no barrier in the loop), the
+// next step's in flight while this one is computed, page numbers a further
+// step ahead.
+//
+// Mathematics of a step.  S^T = K Q^T on 16x16x32 BF16 MFMAs (every E4M3 code
+// is a BF16 value, products are exact), so a lane holds scores of one query row
+// (column lane % 16).  With a value block's scale v and key block's scale k
+// (both of the lane's 8 keys' page), s' = s * (k scale log2 e) + log2 v is one
+// FMA, p' = 2^(s' - m) already carries the value scale, the denominator
+// takes p' / v (another FMA), and the values enter the second product as their
+// bare codes: O^T += V^T P'^T.  P' goes to FP16 (11 significant bits, where BF16's 8
+// would double the output's rounding error) and the codes too, exactly.
+// m is a reference, not the exact maximum: it is moved (and O, l rescaled)
+// only when a score exceeds it by 2^15; a move sets the largest p' to 2^8, so
+// FP16 neither overflows nor loses weights above 2^-33 of the largest.
+//
+// Layouts.  Key rows of the two 16-row MFMA tiles are assigned so that
+// lane group g = lane / 16 gets the scores of keys 8g .. 8g+7: those are the
+// 8 consecutive k of its P'^T operand, no exchange between lanes.  The
+// inner dims are permuted the same way on both sides so that a lane loads 16
+// contiguous key bytes.  V^T needs 8 keys of one dim in a lane: it loads 8 keys x
+// D/16 dims and transposes bytes in registers (2 v_perm_b32 a dword).
+#include <hip/hip_runtime.h>
+
+#include "attn_sched.h"
+
+namespace fp8bs {
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kNoKeys = -1e30f;       // reference of a row that has seen no key yet
+constexpr float kHeadroom = 15.0f;      // log2 of the largest p' before the reference moves
+constexpr float kTop = 8.0f;            // log2 of the largest p' after a move
+constexpr float kMinVScale = 0x1p-100f;
+
+// Eight codes (two dwords) to eight BF16 / FP16 values, exact.
+__device__ __forceinline__ bf16x8 bf16_of_codes(uint32_t a, uint32_t b) {
+  const u32x4 w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true))};
+  return __builtin_bit_cast(bf16x8, w);
+}
+__device__ __forceinline__ f16x8 f16_of_codes(uint32_t a, uint32_t b) {
+  const u32x4 w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true))};
+  return __builtin_bit_cast(f16x8, w);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), f16x2));
+}
+
+// A 4x4 byte transpose: r[i] holds byte i of a, b, c, d.
+__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t r[4]) {
+  const uint32_t x = __builtin_amdgcn_perm(b, a, 0x05010400u), y = __builtin_amdgcn_perm(b, a, 0x07030602u);
+  const uint32_t z = __builtin_amdgcn_perm(d, c, 0x05010400u), w = __builtin_amdgcn_perm(d, c, 0x07030602u);
+  r[0] = __builtin_amdgcn_perm(z, x, 0x05040100u);
+  r[1] = __builtin_amdgcn_perm(z, x, 0x07060302u);
+  r[2] = __builtin_amdgcn_perm(w, y, 0x05040100u);
+  r[3] = __builtin_amdgcn_perm(w, y, 0x07060302u);
+}
+
+// What a wave holds of one step of 32 keys.
+template <int D>
+struct Step {
+  u32x4 k[2][D / 64];          // two MFMA tiles of 16 keys, 16 bytes a lane and 64 dims
+  uint32_t v[8][D / 64];       // 8 keys, D/16 dims a lane
+  float ks, vs;                // scales of the lane's 8 keys
+};
+
+// Page numbers of a step: of the lane's key row and of its 8 keys.
+struct Pages {
+  int k, v;
+};
+
+template <int D, int NR>
+__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_rows_kernel(AttnArgs a) {
+  constexpr int R = 16 * NR, VW = D / 16, NW = D / 64;
+  __shared__ __attribute__((aligned(16))) float obuf[4][16][D + 4];
+  __shared__ float ml[4][16][2];
+  __shared__ int64_t prefix[kMaxSlots + 1];
+  __shared__ int64_t sums[4];
+  poison_lds<sizeof(obuf)>(obuf);
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = tid >> 6;
+  const int m16 = lane & 15, g = lane >> 4;
+  const int page_mask = (1 << a.pshift) - 1;
+
+  Line line;
+  int64_t cur, stop;
+  int slot, h, w;
+  if (a.workers != 0) {
+    line = make_line(a, R, prefix, sums);
+    w = xcd_order(blockIdx.x, gridDim.x);
+    if (tid == 0) a.rec[w * 8] = 0;
+    if (w >= line.workers) return;
+    cur = stretch_begin(line, w);
+    stop = stretch_begin(line, w + 1);
+    h = static_cast<int>(cur / line.per_head);
+    slot = slot_of(a, line, cur - h * line.per_head);
+  } else {
+    w = blockIdx.x;
+    h = w / a.slots;
+    slot = w - h * a.slots;
+    cur = 0;
+    stop = 1;
+  }
+
+  while (cur < stop) {
+    const Tile t = tile_of(a, slot, R);
+    int ub = 0, ue = t.units;   // the piece: units ub .. ue - 1 of the item
+    if (a.workers != 0) {
+      const int64_t first = h * line.per_head + line.prefix[slot];
+      ub = static_cast<int>(cur - first);
+      if (stop - first < ue) ue = static_cast<int>(stop - first);
+      cur = first + ue;
+    } else {
+      cur = stop;
+      if (t.units == 0) return;
+    }
+    const bool whole = ub == 0 && ue == t.units;
+
+    // queries: the B operand, row m16 of each 16-row group
+    bf16x8 qf[NR][2 * NW];
+    int rlo[NR], rhi[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = 16 * r + m16;
+      const bool there = row < t.rows;
+      const int rr = there ? row : 0;
+      row_keys(a, t, t.row0 + rr, rlo[r], rhi[r]);
+      if (!there) rhi[r] = 0;
+      const uint16_t* q = a.p.q + row_token(a, t, rr) * a.p.ldq + static_cast<int64_t>(row_head(a, t, h, rr)) * D;
+#pragma unroll
+      for (int c = 0; c < 2 * NW; ++c) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
+        qf[r][c] = __builtin_bit_cast(bf16x8, there ? x : zero);
+      }
+    }
+    // keys that every row sees need no mask
+    int64_t pf = static_cast<int64_t>(t.len) - t.n + t.row0 / a.G;
+    int64_t pl = static_cast<int64_t>(t.len) - t.n + (t.row0 + t.rows - 1) / a.G;
+    const int all_hi = a.p.causal && pf + 1 < t.len ? static_cast<int>(pf < -1 ? 0 : pf + 1) : t.len;
+    const int64_t wlo = a.p.window > 0 ? pl - a.p.window + 1 : 0;
+    const int all_lo = wlo > 0 ? static_cast<int>(wlo) : 0;
+
+    f32x4 o[NR][4 * NW];
+    float mr[NR], lr[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      mr[r] = kNoKeys;
+      lr[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4 * NW; ++i) o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    const int32_t* table = a.p.table + t.b * a.p.ldt;
+    const int last_page = static_cast<int>(a.p.max_pages) - 1;
+    const int base = (t.u0 + ub) * kUnit;
+    int steps = (ue - ub) * (kUnit / 32);
+    if (base + 32 * steps > t.hi) steps = t.hi > base ? (t.hi - base + 31) / 32 : 0;
+    auto clamp_page = [&](int id) {
+      const unsigned u = static_cast<unsigned>(id), n = static_cast<unsigned>(a.p.n_pages) - 1u;
+      return static_cast<int>(u < n ? u : n);
+    };
+    auto load_pages = [&](int s) {
+      Pages p;
+      const int t0 = base + 32 * s;
+      const int ik = (t0 + 8 * (m16 >> 2)) >> a.pshift, iv = (t0 + 8 * g) >> a.pshift;
+      p.k = table[ik < last_page ? ik : last_page];
+      p.v = table[iv < last_page ? iv : last_page];
+      return p;
+    };
+    auto load_step = [&](int s, const Pages& pg) {
+      Step<D> x;
+      const int t0 = base + 32 * s;
+      const int64_t bk = static_cast<int64_t>(clamp_page(pg.k)) * a.p.Hkv + h;
+      const int64_t bv = static_cast<int64_t>(clamp_page(pg.v)) * a.p.Hkv + h;
+      const int tk = (t0 + 8 * (m16 >> 2) + (m16 & 3)) & page_mask, tv = (t0 + 8 * g) & page_mask;
+      const uint8_t* pk = a.p.kc + ((bk << a.pshift) + tk) * D + 16 * g;
+      const uint8_t* pv = a.p.vc + ((bv << a.pshift) + tv) * D + m16 * VW;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < NW; ++c) x.k[i][c] = *reinterpret_cast<const u32x4*>(pk + 4 * i * D + 64 * c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (NW == 2) {
+          const u32x2 y = *reinterpret_cast<const u32x2*>(pv + j * D);
+          x.v[j][0] = y[0];
+          x.v[j][NW - 1] = y[1];
+        } else {
+          x.v[j][0] = *reinterpret_cast<const uint32_t*>(pv + j * D);
+        }
+      }
+      x.ks = a.p.ks[bv];
+      x.vs = a.p.vs[bv];
+      return x;
+    };
+    auto compute = [&](int s, Step<D>& x) {
+      const int t0 = base + 32 * s, mine = t0 + 8 * g;
+      const bool clear = t0 >= all_lo && t0 + 32 <= all_hi;
+      float kq = x.ks * a.scale_log2;
+      float vs = x.vs > kMinVScale ? x.vs : kMinVScale;
+      if (!clear) {
+        // keys that no row sees may hold anything: their values become zero
+        // codes, the scales of a page that lies wholly outside become harmless
+        const bool none = mine >= t.hi || mine + 8 <= t.lo;
+        kq = none ? 0.0f : kq;
+        vs = none ? 1.0f : vs;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (mine + j >= t.hi || mine + j < t.lo)
+#pragma unroll
+            for (int c = 0; c < NW; ++c) x.v[j][c] = 0u;
+      }
+      const float lv = __builtin_amdgcn_logf(vs), iv = __builtin_amdgcn_rcpf(vs);
+      f32x4 sc[NR][2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 2 * NW; ++c) {
+          const bf16x8 kf = bf16_of_codes(x.k[i][c >> 1][2 * (c & 1)], x.k[i][c >> 1][2 * (c & 1) + 1]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            sc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][c], sc[r][i], 0, 0, 0);
+        }
+      f16x8 pf16[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        float e[8];
+        float top = -__builtin_huge_valf();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e[j] = __builtin_fmaf(sc[r][j >> 2][j & 3], kq, lv);
+        if (!clear) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            e[j] = mine + j >= rlo[r] && mine + j < rhi[r] ? e[j] : -__builtin_huge_valf();
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, e[j]);
+        if (__ballot(top > mr[r] + kHeadroom) != 0) {
+          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+          const float to = top > mr[r] + kHeadroom ? top - kTop : mr[r];
+          const float f = __builtin_amdgcn_exp2f(mr[r] - to);
+          mr[r] = to;
+          lr[r] *= f;
+#pragma unroll
+          for (int i = 0; i < 4 * NW; ++i) o[r][i] *= f;
+        }
+        u32x4 pw;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          e[j] = __builtin_amdgcn_exp2f(e[j] - mr[r]);
+          lr[r] = __builtin_fmaf(e[j], iv, lr[r]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pw[j] = pack_f16x2(e[2 * j], e[2 * j + 1]);
+        pf16[r] = __builtin_bit_cast(f16x8, pw);
+      }
+#pragma unroll
+      for (int c = 0; c < NW; ++c) {
+        uint32_t lo4[4], hi4[4];
+        transpose4(x.v[0][c], x.v[1][c], x.v[2][c], x.v[3][c], lo4);
+        transpose4(x.v[4][c], x.v[5][c], x.v[6][c], x.v[7][c], hi4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const f16x8 vf = f16_of_codes(lo4[u], hi4[u]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            o[r][4 * c + u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pf16[r], o[r][4 * c + u], 0, 0, 0);
+        }
+      }
+    };
+
+    // the wave's steps: wv, wv + 4, ...
+    if (wv < steps) {
+      Pages pg = load_pages(wv);
+      Step<D> x = load_step(wv, pg);
+      if (wv + 4 < steps) pg = load_pages(wv + 4);
+      int s = wv;
+      while (true) {
+        Step<D> y;
+        if (s + 4 < steps) {
+          y = load_step(s + 4, pg);
+          if (s + 8 < steps) pg = load_pages(s + 8);
+        }
+        compute(s, x);
+        s += 4;
+        if (s >= steps) break;
+        if (s + 4 < steps) {
+          x = load_step(s + 4, pg);
+          if (s + 8 < steps) pg = load_pages(s + 8);
+        }
+        compute(s, y);
+        s += 4;
+        if (s >= steps) break;
+      }
+    }
+
+    // join the four waves: row r of the group, D/16 dims a thread
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      float l = lr[r];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      __syncthreads();
+      if (g == 0) {
+        ml[wv][m16][0] = mr[r];
+        ml[wv][m16][1] = l;
+      }
+      // lane's values: row m16, dims (4 g + i) * VW + c
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < NW; ++c)
+          *reinterpret_cast<f32x4*>(&obuf[wv][m16][(4 * g + i) * VW + 4 * c]) =
+              f32x4{o[r][4 * c][i], o[r][4 * c + 1][i], o[r][4 * c + 2][i], o[r][4 * c + 3][i]};
+      __syncthreads();
+      const int row = tid >> 4, d0 = (tid & 15) * VW;
+      float top = kNoKeys;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = __builtin_fmaxf(top, ml[k][row][0]);
+      float sum[VW], den = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = __builtin_amdgcn_exp2f(ml[k][row][0] - top);
+        den = __builtin_fmaf(f, ml[k][row][1], den);
+#pragma unroll
+        for (int i = 0; i < VW; ++i) sum[i] = __builtin_fmaf(f, obuf[k][row][d0 + i], sum[i]);
+      }
+      const int tr = 16 * r + row;
+      if (tr < t.rows) {
+        if (whole) store_out<VW>(a, row_token(a, t, tr), row_head(a, t, h, tr), D, d0, sum, top, den);
+        else store_part<VW>(a.part, R, D, 2 * static_cast<int64_t>(w) + (ub == 0 ? 1 : 0), tr, d0, sum, top, den);
+      }
+    }
+    if (a.workers != 0) {
+      if (!whole && ub == 0 && tid == 0) {
+        // this worker starts the item: it records who holds the rest
+        const int64_t end = cur - ue + t.units;
+        int32_t* rec = a.rec + w * 8;
+        rec[1] = slot;
+        rec[2] = h;
+        rec[3] = worker_of(line, end - 1) - w;
+        rec[0] = 1;
+      }
+      // the next item with units
+      do {
+        if (++slot == a.slots) {
+          slot = 0;
+          ++h;
+        }
+      } while (cur < stop && line.prefix[slot + 1] == line.prefix[slot]);
+    }
+  }
+}
+
+// Joins the partials of the item that worker blockIdx.x began: 16 rows a
+// workgroup (blockIdx.y), thread (row, D/16 dims), in the workers' order.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
+  constexpr int VW = D / 16;
+  const int w = blockIdx.x;
+  const int32_t* rec = a.rec + w * 8;
+  if (rec[0] == 0) return;
+  const int slot = rec[1], h = rec[2], more = rec[3];
+  const Tile t = tile_of(a, slot, R);
+  const int r = static_cast<int>(blockIdx.y) * 16 + (static_cast<int>(threadIdx.x) >> 4);
+  if (r >= t.rows) return;
+  const int d0 = (static_cast<int>(threadIdx.x) & 15) * VW;
+  const int64_t size = static_cast<int64_t>(R) * (D + 2);
+  float sum[VW], top = kNoKeys, den = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k <= more; ++k) {
+    const float* piece = a.part + (2 * static_cast<int64_t>(w + k) + (k == 0 ? 1 : 0)) * size;
+    const float m = piece[R * D + 2 * r], l = piece[R * D + 2 * r + 1];
+    const float to = __builtin_fmaxf(top, m);
+    const float f = __builtin_amdgcn_exp2f(top - to), g = __builtin_amdgcn_exp2f(m - to);
+    den = __builtin_fmaf(g, l, den * f);
+#pragma unroll
+    for (int i = 0; i < VW / 4; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(piece + r * D + d0 + 4 * i);
+      sum[4 * i] = __builtin_fmaf(g, x.x, sum[4 * i] * f);
+      sum[4 * i + 1] = __builtin_fmaf(g, x.y, sum[4 * i + 1] * f);
+      sum[4 * i + 2] = __builtin_fmaf(g, x.z, sum[4 * i + 2] * f);
+      sum[4 * i + 3] = __builtin_fmaf(g, x.w, sum[4 * i + 3] * f);
+    }
+    top = to;
+  }
+  store_out<VW>(a, row_token(a, t, r), row_head(a, t, h, r), D, d0, sum, top, den);
+}
+
+// Launch sizes: a function of the call's sizes alone.
+struct Plan {
+  int R;
+  int64_t slots;
+  int most;
+  int workers;   // 0: one item a workgroup
+  int min_units;
+  int64_t bytes;
+};
+
+Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
+  Plan p;
+  const int64_t G = Hq / Hkv, rows = max_q * G;
+  p.R = rows <= 16 ? 16 : 32;
+  const int64_t most = (rows + p.R - 1) / p.R;
+  const int64_t direct = B * most, searched = T * G / p.R + B;
+  p.most = direct <= searched ? static_cast<int>(most) : 0;
+  p.slots = direct <= searched ? direct : searched;
+  p.min_units = 4;
+  const int full = p.R == 16 ? 768 : 512;   // resident workgroups
+  p.workers = 0;
+  p.bytes = 0;
+  if (p.slots <= kMaxSlots) {
+    const int64_t units = (max_pages * page + kUnit - 1) / kUnit;
+    const int64_t useful = p.slots * Hkv * ((units + p.min_units - 1) / p.min_units);
+    p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
+    p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 8 * static_cast<int64_t>(p.workers)) * 4;
+  }
+  return p;
+}
+
+}  // namespace
+
+int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
+  return plan_of(B, T, max_q, Hq, Hkv, D, max_pages, page).bytes;
+}
+
+hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
+  const Plan plan = plan_of(p.B, p.T, p.max_q, p.Hq, p.Hkv, p.D, p.max_pages, p.page);
+  AttnArgs a;
+  a.p = p;
+  a.G = p.Hq / p.Hkv;
+  a.pshift = __builtin_ctz(static_cast<unsigned>(p.page));
+  a.max_len = static_cast<int>(p.max_pages * p.page);
+  a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
+  const int64_t blocks = plan.workers != 0 ? plan.workers : plan.slots * p.Hkv;
+  if (blocks > 0x7fffffff || plan.slots > 0x7fffffff) return hipErrorInvalidValue;
+  a.slots = static_cast<int>(plan.slots);
+  a.most = plan.most;
+  a.workers = plan.workers;
+  a.min_units = plan.min_units;
+  a.part = static_cast<float*>(p.ws);
+  a.rec = reinterpret_cast<int32_t*>(a.part + 2 * static_cast<int64_t>(plan.workers) * plan.R * (p.D + 2));
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+#define FP8BS_ROWS(D_, NR_) \
+  if (p.D == D_ && plan.R == 16 * NR_) hipLaunchKernelGGL((attn_rows_kernel<D_, NR_>), grid, block, 0, st, a)
+  FP8BS_ROWS(64, 1);
+  FP8BS_ROWS(64, 2);
+  FP8BS_ROWS(128, 1);
+  FP8BS_ROWS(128, 2);
+#undef FP8BS_ROWS
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || plan.workers == 0) return e;
+  const dim3 jgrid(static_cast<unsigned>(plan.workers), static_cast<unsigned>(plan.R / 16));
+  if (p.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, block, 0, st, a, plan.R);
+  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, block, 0, st, a, plan.R);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

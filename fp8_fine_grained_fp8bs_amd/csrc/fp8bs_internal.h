@@ -59,4 +59,72 @@ hipError_t launch_grouped_gemm(const uint8_t* a, const float* sa, int64_t ldsa,
                                int32_t E, int64_t M_total, void* d, bool out_f32,
                                int64_t N, int64_t K, hipStream_t st);
 
+hipError_t launch_rope_table(float* cs, int64_t n_pos, int64_t rot, double base, double factor, double orig_len,
+                             double turns_lo, double turns_hi, double mscale, hipStream_t st);
+
+hipError_t launch_rope(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy, const int32_t* pos, int64_t T,
+                       int H, int D, int rot, int rot_off, bool interleaved, bool inverse, const float* cs,
+                       int64_t n_pos, hipStream_t st);
+
+// Arguments of fp8bs_kv_append (q == nullptr: no queries; cs == nullptr: no rotation).
+struct KvAppend {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* q_out;
+  int64_t ldqo;
+  int Hq;
+  const uint16_t* k;
+  int64_t ldk;
+  const uint16_t* v;
+  int64_t ldv;
+  int Hkv, D;
+  const float* cs;
+  int64_t n_pos;
+  int rot, rot_off;
+  bool interleaved;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  int B;
+  int64_t T, max_q;
+  const int32_t* table;
+  int64_t ldt, max_pages;
+  int page;
+  uint8_t* kc;
+  float* ks;
+  uint8_t* vc;
+  float* vs;
+  int64_t n_pages;
+};
+hipError_t launch_kv_append(const KvAppend& p, hipStream_t st);
+
+// Arguments of fp8bs_attn_paged.
+struct AttnPaged {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;
+  int64_t ldl;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  int B;
+  int64_t T, max_q;
+  int Hq, Hkv, D;
+  const int32_t* table;
+  int64_t ldt, max_pages;
+  int page;
+  const uint8_t* kc;
+  const float* ks;
+  const uint8_t* vc;
+  const float* vs;
+  int64_t n_pages;
+  float scale;
+  bool causal;
+  int64_t window;
+  void* ws;
+};
+hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st);
+// Working memory of launch_attn_paged: a function of the sizes alone.
+int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page);
+
 }  // namespace fp8bs

@@ -1,0 +1,298 @@
+// kv_append.hip -- keys and values appended to a paged E4M3 cache, the
+// rotation of keys and queries on the way (gfx950).
+//
+// A block of the cache is one page of one key/value head under one FP32
+// scale.  One workgroup takes one (page, head): it reads the page's new keys
+// and values once, rotates the keys in FP32 (not rounded to BF16 in
+// between), takes both max-abs, settles both scales and writes codes and
+// scales.  No other workgroup touches the block, so a page that fills over
+// many calls needs no atomics and the result does not depend on any order:
+//   s' = max(s, fl32(amax(new) / 448)); where it grows, the codes already
+//   there are encoded again from fl32(dec(code) * s).
+// The queries' rotation runs in further workgroups of the same launch: at
+// one token a request the call is bound by its launch and its chain of
+// dependent loads (offsets, table, cache), for prompts by HBM.
+//
+// Workgroups are laid over pages without knowing lengths on the host: with n_b
+// tokens a sequence touches at most floor(n_b / page) + 2 pages, so slot
+// numbers floor(q_off[b] / page) + 2 b leave room for each, and a workgroup
+// finds its sequence by searching those numbers.  Where max_q gives a tighter
+// bound (one token a request: one page each) the slot is split directly.
+#include <hip/hip_runtime.h>
+
+#include "fp8bs_internal.h"
+#include "rope_device.h"
+
+namespace fp8bs {
+namespace {
+
+struct AppendArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  uint16_t* qo;
+  int64_t ldqo;
+  int Hq;
+  const uint16_t* k;
+  int64_t ldk;
+  const uint16_t* v;
+  int64_t ldv;
+  int Hkv;
+  const float* cs;
+  int64_t n_pos;
+  RopeShape rope;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  int B;
+  int64_t T;
+  const int32_t* table;
+  int64_t ldt;
+  int64_t max_pages;
+  int pshift;
+  uint8_t* kc;
+  float* ks;
+  uint8_t* vc;
+  float* vs;
+  int64_t n_pages;
+  int64_t slots;
+  int most;          // pages of a sequence where slots are split directly, else 0
+  int64_t page_blocks;
+};
+
+// First packed row and row count of sequence b, inside 0 .. T.
+__device__ __forceinline__ void rows_of(const int32_t* q_off, int64_t T, int b, int64_t& off, int& n) {
+  if (q_off == nullptr) {
+    off = b;
+    n = 1;
+    return;
+  }
+  int64_t a = q_off[b], e = q_off[b + 1];
+  a = a < 0 ? 0 : a > T ? T : a;
+  e = e < a ? a : e > T ? T : e;
+  off = a;
+  n = static_cast<int>(e - a);
+}
+
+// Encoder constants of a settled scale.
+__device__ __forceinline__ TileScale scale_of(float s) {
+  TileScale t;
+  t.s = s;
+  t.fast = s >= kFastScaleMin;
+  const float r = __builtin_amdgcn_rcpf(t.fast ? s : 1.0f);
+  t.rlo = r * kMarginLo;
+  t.rhi = r * kMarginHi;
+  return t;
+}
+
+__device__ __forceinline__ const float* angles(const AppendArgs& a, int64_t p) {
+  p = p < 0 ? 0 : p >= a.n_pos ? a.n_pos - 1 : p;
+  return a.cs + p * a.rope.rot;
+}
+
+// The 8 values at dim d of a key, rotated where d lies in the rotated part:
+// the unit's other vector is read too (from the cache, another thread owns it).
+__device__ __forceinline__ void load_key(const AppendArgs& a, const uint16_t* row, int64_t p, int d, float f[8]) {
+  const uint4 w = *reinterpret_cast<const uint4*>(row + d);
+  unpack8(w, f);
+  const RopeShape& r = a.rope;
+  const int o = d - r.off;
+  if (a.cs == nullptr || o < 0 || o >= r.rot) return;
+  float g[8];
+  if (r.interleaved) {
+    const int c = o >> 4;
+    const bool second = (o & 8) != 0;
+    const CosSin k = load_cossin(angles(a, p), r.rot, c);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float cc = second ? k.c[4 + i] : k.c[i], ss = second ? k.s[4 + i] : k.s[i];
+      const float x1 = f[2 * i], x2 = f[2 * i + 1];
+      f[2 * i] = x1 * cc - x2 * ss;
+      f[2 * i + 1] = x2 * cc + x1 * ss;
+    }
+  } else {
+    const int half = r.rot >> 1;
+    const bool second = o >= half;
+    unpack8(*reinterpret_cast<const uint4*>(row + (second ? d - half : d + half)), g);
+    const CosSin k = load_cossin(angles(a, p), r.rot, (second ? o - half : o) >> 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = second ? f[i] * k.c[i] + g[i] * k.s[i] : f[i] * k.c[i] - g[i] * k.s[i];
+  }
+}
+
+// Write one block's codes: `n` = there .. end - 1 are the new tokens' places,
+// 0 .. there - 1 the old ones'.
+template <int NP, int D, typename Fetch>
+__device__ __forceinline__ void store_block(uint8_t* codes, int there, int end, float s_old, float s, Fetch fetch) {
+  const TileScale ts = scale_of(s);
+  const int sub = (static_cast<int>(threadIdx.x) % (D / 8)) * 8;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = i * (2048 / D) + static_cast<int>(threadIdx.x) / (D / 8);
+    uint2* at = reinterpret_cast<uint2*>(codes + r * D + sub);
+    float f[8];
+    if (r >= there && r < end) {
+      fetch(i, f);
+    } else if (r < there && s > s_old) {
+      const uint2 c = *at;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[j] = e4m3_dec((c.x >> (8 * j)) & 0xffu) * s_old;
+        f[4 + j] = e4m3_dec((c.y >> (8 * j)) & 0xffu) * s_old;
+      }
+    } else {
+      continue;
+    }
+    *at = make_uint2(encode4(f, ts), encode4(f + 4, ts));
+  }
+}
+
+// NP: passes of 2048 values over a block (256 threads, 8 values each).
+template <int D, int NP>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
+  __shared__ float red[2][4];
+  poison_lds<sizeof(red)>(red);
+  const int tid = static_cast<int>(threadIdx.x);
+  int64_t bid = blockIdx.x;
+  if (bid >= a.page_blocks) {   // queries: one token and 256 units of 16 values a workgroup
+    bid -= a.page_blocks;
+    const int per = a.Hq * (D / 16);
+    const int strips = (per + 255) / 256;
+    const int64_t t = bid / strips;
+    const int e = static_cast<int>(bid - t * strips) * 256 + tid;
+    const int b = a.q_off == nullptr ? static_cast<int>(t)
+                                     : search64(a.B, t, [&](int i) { return static_cast<int64_t>(a.q_off[i]); });
+    int64_t off;
+    int n;
+    rows_of(a.q_off, a.T, b, off, n);
+    if (e >= per) return;
+    const int64_t p = static_cast<int64_t>(a.kv_len[b]) - n + (t - off);
+    const int h = e / (D / 16), c = e - h * (D / 16);
+    const uint16_t* x = a.q + t * a.ldq + h * D;
+    uint16_t* y = a.qo + t * a.ldqo + h * D;
+    const RopeShape& r = a.rope;
+    if (16 * c >= r.rot) {
+      const int k = 2 * (c - r.rot / 16);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        int d = 8 * (k + i);
+        if (d >= r.off) d += r.rot;
+        *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(x + d);
+      }
+      return;
+    }
+    const int ia = rope_first(r, c), ib = rope_second(r, c);
+    float f[8], g[8];
+    unpack8(*reinterpret_cast<const uint4*>(x + ia), f);
+    unpack8(*reinterpret_cast<const uint4*>(x + ib), g);
+    rotate8(f, g, load_cossin(angles(a, p), r.rot, c), r.interleaved);
+    *reinterpret_cast<uint4*>(y + ia) = pack8(f);
+    *reinterpret_cast<uint4*>(y + ib) = pack8(g);
+    return;
+  }
+  const int h = static_cast<int>(bid % a.Hkv);
+  const int64_t slot = bid / a.Hkv;
+  int b, nth;
+  if (a.most != 0) {
+    b = static_cast<int>(slot / a.most);
+    nth = static_cast<int>(slot - static_cast<int64_t>(b) * a.most);
+  } else {
+    auto key = [&](int i) {
+      const int64_t o = a.q_off == nullptr ? i : a.q_off[i];
+      return (o >> a.pshift) + 2 * static_cast<int64_t>(i);
+    };
+    b = search64(a.B, slot, key);
+    nth = static_cast<int>(slot - key(b));
+  }
+  int64_t off;
+  int n;
+  rows_of(a.q_off, a.T, b, off, n);
+  const int64_t len = a.kv_len[b], start = len - n;
+  if (n == 0 || start < 0) return;
+  const int64_t pg = (start >> a.pshift) + nth;      // the page's place in the sequence
+  const int64_t base = pg << a.pshift;
+  if (base >= len || pg >= a.max_pages) return;
+  const int64_t id = a.table[b * a.ldt + pg];
+  if (id < 0 || id >= a.n_pages) return;
+  const int there = static_cast<int>(start > base ? start - base : 0);
+  const int64_t left = len - base, page = int64_t(1) << a.pshift;
+  const int end = static_cast<int>(left < page ? left : page);
+  const int64_t blk = id * a.Hkv + h;
+  const float sk_old = there > 0 ? a.ks[blk] : 0.0f, sv_old = there > 0 ? a.vs[blk] : 0.0f;
+
+  const int sub = (tid % (D / 8)) * 8, row0 = tid / (D / 8);
+  float kf[NP][8];
+  uint4 vw[NP];
+  float mk = 0.0f, mv = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = i * (2048 / D) + row0;
+    if (r >= there && r < end) {
+      const int64_t t = off + (base + r - start);
+      load_key(a, a.k + t * a.ldk + h * D, base + r, sub, kf[i]);
+      vw[i] = *reinterpret_cast<const uint4*>(a.v + t * a.ldv + h * D + sub);
+      float f[8];
+      unpack8(vw[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mk = __builtin_fmaxf(mk, __builtin_fabsf(kf[i][j]));
+        mv = __builtin_fmaxf(mv, __builtin_fabsf(f[j]));
+      }
+    }
+  }
+  mk = wave_max(mk);
+  mv = wave_max(mv);
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = mk;
+    red[1][tid >> 6] = mv;
+  }
+  __syncthreads();
+  mk = __builtin_fmaxf(__builtin_fmaxf(red[0][0], red[0][1]), __builtin_fmaxf(red[0][2], red[0][3]));
+  mv = __builtin_fmaxf(__builtin_fmaxf(red[1][0], red[1][1]), __builtin_fmaxf(red[1][2], red[1][3]));
+  const float sk = __builtin_fmaxf(sk_old, make_tile_scale(mk).s);
+  const float sv = __builtin_fmaxf(sv_old, make_tile_scale(mv).s);
+  const int64_t at = (blk << a.pshift) * D;
+  store_block<NP, D>(a.kc + at, there, end, sk_old, sk, [&](int i, float f[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = kf[i][j];
+  });
+  store_block<NP, D>(a.vc + at, there, end, sv_old, sv, [&](int i, float f[8]) { unpack8(vw[i], f); });
+  if (tid == 0) {
+    a.ks[blk] = sk;
+    a.vs[blk] = sv;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppend& p, hipStream_t st) {
+  AppendArgs a;
+  a.q = p.q; a.ldq = p.ldq; a.qo = p.q_out; a.ldqo = p.ldqo; a.Hq = p.Hq;
+  a.k = p.k; a.ldk = p.ldk; a.v = p.v; a.ldv = p.ldv; a.Hkv = p.Hkv;
+  a.cs = p.cs; a.n_pos = p.n_pos; a.rope = RopeShape{p.rot, p.rot_off, p.interleaved};
+  a.q_off = p.q_off; a.kv_len = p.kv_len; a.B = p.B; a.T = p.T;
+  a.table = p.table; a.ldt = p.ldt; a.max_pages = p.max_pages;
+  a.pshift = __builtin_ctz(static_cast<unsigned>(p.page));
+  a.kc = p.kc; a.ks = p.ks; a.vc = p.vc; a.vs = p.vs; a.n_pages = p.n_pages;
+  const int64_t most = (p.max_q + p.page - 2) / p.page + 1;
+  const int64_t direct = most * p.B, searched = p.T / p.page + 2 * static_cast<int64_t>(p.B);
+  a.most = direct <= searched ? static_cast<int>(most) : 0;
+  a.slots = direct <= searched ? direct : searched;
+  a.page_blocks = a.slots * p.Hkv;
+  const int64_t strips = p.q != nullptr ? (static_cast<int64_t>(p.Hq) * (p.D / 16) + 255) / 256 : 0;
+  const int64_t blocks = a.page_blocks + p.T * strips;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  const int np = p.page * p.D <= 2048 ? 1 : p.page * p.D / 2048;
+#define FP8BS_APPEND(D_, NP_) \
+  if (p.D == D_ && np == NP_) hipLaunchKernelGGL((kv_append_kernel<D_, NP_>), grid, block, 0, st, a)
+  FP8BS_APPEND(64, 1);
+  FP8BS_APPEND(64, 2);
+  FP8BS_APPEND(64, 4);
+  FP8BS_APPEND(128, 1);
+  FP8BS_APPEND(128, 2);
+  FP8BS_APPEND(128, 4);
+  FP8BS_APPEND(128, 8);
+#undef FP8BS_APPEND
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

@@ -31,6 +31,8 @@ BSCALE_ROW_1x128 = 1
 SRC_FP8_1x128 = 0
 SRC_BF16 = 1
 SRC_E5M6 = 2
+ROPE_HALF = 0
+ROPE_INTERLEAVED = 1
 
 ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_act_w",
                 "fp8bs_swiglu_quant_1x128",
@@ -39,6 +41,8 @@ ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_a
                 "fp8bs_encode_e5m6", "fp8bs_decode_e5m6", "fp8bs_requant_T_128x1",
                 "fp8bs_transpose_w_128x128", "fp8bs_gemm", "fp8bs_gemm_quant_1x128", "fp8bs_gemm_bf16a",
                 "fp8bs_grouped_gemm",
+                "fp8bs_rope_table", "fp8bs_rope", "fp8bs_kv_append", "fp8bs_attn_paged",
+                "fp8bs_attn_paged_ws",
                 "fp8bs_status_string", "fp8bs_version")
 
 _lib = None
@@ -71,6 +75,7 @@ def load() -> ctypes.CDLL:
                            "`python -m fp8_fine_grained_fp8bs_amd.build` (hipcc, gfx950)")
     lib = ctypes.CDLL(_lib_path)
     P, I64, I32, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+    F, F64 = ctypes.c_float, ctypes.c_double
     sigs = {
         "fp8bs_quant_act_1x128": [P, I64, I64, I64, P, I64, P, I64, P],
         "fp8bs_swiglu_quant_1x128": [P, I64, P, I64, I64, I64, P, I64, P, I64, P, I64, P],
@@ -86,11 +91,19 @@ def load() -> ctypes.CDLL:
         "fp8bs_gemm_quant_1x128": [P, P, I64, I64, P, P, I64, I64, I, P, I64, P, I64, I64, I64, I64, P],
         "fp8bs_grouped_gemm": [P, P, I64, P, P, P, I32, I64, P, I, I64, I64, P],
         "fp8bs_gemm_bf16a": [P, I64, P, I64, P, I64, P, P, I64, I64, P, I64, I, I64, I64, I64, P],
+        "fp8bs_rope_table": [P, I64, I64, F64, F64, F64, F64, F64, F64, P],
+        "fp8bs_rope": [P, I64, P, I64, P, I64, I64, I64, I64, I64, I, I, P, I64, P],
+        "fp8bs_kv_append": [P, I64, P, I64, I64, P, I64, P, I64, I64, I64, P, I64, I64, I64, I, P, P, I64, I64,
+                            I64, P, I64, I64, I64, P, P, P, P, I64, P],
+        "fp8bs_attn_paged": [P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I64, I64, P, I64, I64, I64, P, P,
+                             P, P, I64, F, I, I64, P, I64, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    lib.fp8bs_attn_paged_ws.argtypes = [I64] * 8
+    lib.fp8bs_attn_paged_ws.restype = I64
     lib.fp8bs_status_string.argtypes = [ctypes.c_int]
     lib.fp8bs_status_string.restype = ctypes.c_char_p
     lib.fp8bs_version.argtypes = []
@@ -330,6 +343,128 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
           int(E), M_total, _ptr(d), int(dt), N, K, _stream(stream))
 
 
+def _heads(t, what):
+    """Row stride (elements) of a [T][H][D] view whose heads are contiguous in a row."""
+    if t.dim() != 3 or str(t.dtype) != "torch.bfloat16":
+        raise ValueError(f"{what}: expected a 3-D bfloat16 tensor [T][H][D], got {t.dim()}-D {t.dtype}")
+    T, H, D = t.shape
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
+        raise ValueError(f"{what}: heads must be contiguous in a row, got strides {tuple(st)}")
+    return st[0] if T > 1 else max(st[0], H * D)
+
+
+def _layout(layout):
+    if layout in ("half", ROPE_HALF):
+        return ROPE_HALF
+    if layout in ("interleaved", ROPE_INTERLEAVED):
+        return ROPE_INTERLEAVED
+    raise ValueError(f"layout: {layout!r}, expected 'half' or 'interleaved'")
+
+
+def _int32s(t, what, n):
+    if str(t.dtype) != "torch.int32" or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what}: expected {n} contiguous int32, got {t.dtype} {tuple(t.shape)}")
+
+
+def _check_angles(cs):
+    if str(cs.dtype) != "torch.float32" or cs.dim() != 2 or not cs.is_contiguous():
+        raise ValueError(f"cs: expected a contiguous float32 table [n_pos][rot], got {cs.dtype} {tuple(cs.shape)}")
+
+
+def _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T):
+    """Shapes of a paged cache and its packing; returns (B, Hkv, D, page, n_pages, ldt)."""
+    if kc.dim() != 4 or str(kc.dtype).replace("torch.", "") not in _CODES or not kc.is_contiguous():
+        raise ValueError(f"kc: expected contiguous codes [n_pages][Hkv][page][D], got {kc.dtype} {tuple(kc.shape)}")
+    if vc.shape != kc.shape or vc.dtype != kc.dtype or not vc.is_contiguous():
+        raise ValueError("vc: must have kc's shape and dtype, contiguous")
+    n_pages, Hkv, page, D = kc.shape
+    for t, what in ((ks, "ks"), (vs, "vs")):
+        if t.shape != (n_pages, Hkv) or str(t.dtype) != "torch.float32" or not t.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous float32 [{n_pages}][{Hkv}], got {t.dtype} {tuple(t.shape)}")
+    if table.dim() != 2 or str(table.dtype) != "torch.int32":
+        raise ValueError(f"table: expected int32 [B][max_pages], got {table.dtype} {tuple(table.shape)}")
+    B = table.shape[0]
+    _int32s(kv_len, "kv_len", B)
+    if q_off is not None:
+        _int32s(q_off, "q_off", B + 1)
+    elif T != B:
+        raise ValueError(f"q_off: without it every sequence has one row, but T = {T} and B = {B}")
+    return B, Hkv, D, page, n_pages, _ld(table) if B > 1 else max(table.stride(0), table.shape[1])
+
+
+def fp8bs_rope_table(cs, base, factor, orig_len, turns_lo, turns_hi, mscale, stream=None):
+    """cs f32 [n_pos][rot]: cos and sin of every position's angles."""
+    _check_angles(cs)
+    _call("fp8bs_rope_table", _ptr(cs), cs.shape[0], cs.shape[1], base, factor, orig_len, turns_lo, turns_hi,
+          mscale, _stream(stream))
+
+
+def fp8bs_rope(x, y, pos, rot_off, layout, inverse, cs, stream=None):
+    """x bf16 [T][H][D] -> y (same shape; may be x), rotated by the angles
+    cs f32 [n_pos][rot] of positions pos i32 [T]."""
+    ldx, ldy = _heads(x, "x"), _heads(y, "y")
+    T, H, D = x.shape
+    if y.shape != x.shape:
+        raise ValueError(f"y: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+    _int32s(pos, "pos", T)
+    _check_angles(cs)
+    _call("fp8bs_rope", _ptr(x), ldx, _ptr(y), ldy, _ptr(pos), T, H, D, cs.shape[1], rot_off, _layout(layout),
+          int(bool(inverse)), _ptr(cs), cs.shape[0], _stream(stream))
+
+
+def fp8bs_kv_append(q, q_out, k, v, cs, rot_off, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream=None):
+    """k, v bf16 [T][Hkv][D] into the paged cache kc, vc u8 [n_pages][Hkv][page][D],
+    ks, vs f32 [n_pages][Hkv]; q bf16 [T][Hq][D] rotated into q_out (both or neither)."""
+    ldk, ldv = _heads(k, "k"), _heads(v, "v")
+    T = k.shape[0]
+    B, Hkv, D, page, n_pages, ldt = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
+    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
+        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)}, expected {(T, Hkv, D)}")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out: both or neither")
+    Hq = ldq = ldqo = 0
+    if q is not None:
+        ldq, ldqo, Hq = _heads(q, "q"), _heads(q_out, "q_out"), q.shape[1]
+        if q.shape != (T, Hq, D) or q_out.shape != q.shape:
+            raise ValueError(f"q, q_out: shapes {tuple(q.shape)}, {tuple(q_out.shape)}, expected {(T, Hq, D)}")
+    n_pos = rot = 0
+    if cs is not None:
+        _check_angles(cs)
+        n_pos, rot = cs.shape
+    _call("fp8bs_kv_append", _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(k), ldk, _ptr(v), ldv, Hkv, D, _ptr(cs),
+          n_pos, rot, rot_off, _layout(layout), _ptr(q_off), _ptr(kv_len), B, T, max_q, _ptr(table), ldt,
+          table.shape[1], page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages, _stream(stream))
+
+
+def fp8bs_attn_paged_ws(B, T, max_q, Hq, Hkv, D, max_pages, page):
+    """Bytes of working memory fp8bs_attn_paged needs (-1: invalid sizes)."""
+    return load().fp8bs_attn_paged_ws(B, T, max_q, Hq, Hkv, D, max_pages, page)
+
+
+def fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs, scale, causal, window, ws,
+                     stream=None):
+    """q bf16 [T][Hq][D] -> out (same shape) and lse f32 [T][Hq] (or None):
+    attention over the paged cache; ws uint8 [>= fp8bs_attn_paged_ws(...)]."""
+    ldq, ldo = _heads(q, "q"), _heads(out, "out")
+    T, Hq, D = q.shape
+    B, Hkv, Dc, page, n_pages, ldt = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
+    if Dc != D or out.shape != q.shape:
+        raise ValueError(f"q, out: shapes {tuple(q.shape)}, {tuple(out.shape)}, expected heads of {Dc}")
+    ldl = 0
+    if lse is not None:
+        _check(lse, "lse", (T, Hq), ("float32",))
+        ldl = _ld(lse) if T > 1 else max(lse.stride(0), Hq)
+    ws_bytes = 0
+    if ws is not None:
+        if not ws.is_contiguous():
+            raise ValueError("ws: must be contiguous")
+        ws_bytes = ws.numel() * ws.element_size()
+    _call("fp8bs_attn_paged", _ptr(q), ldq, _ptr(out), ldo, _ptr(lse), ldl, _ptr(q_off), _ptr(kv_len), B, T, max_q,
+          Hq, Hkv, D, _ptr(table), ldt, table.shape[1], page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages,
+          scale, int(bool(causal)), window, _ptr(ws), ws_bytes, _stream(stream))
+
+
 # ---------------------------------------------------------------------------
 # allocating helpers (torch tensors on the current device)
 # ---------------------------------------------------------------------------
@@ -500,3 +635,68 @@ def grouped_gemm(a, sa, b, sb, offsets, out_f32=False, stream=None):
     d = torch.empty((M, N), dtype=torch.float32 if out_f32 else torch.bfloat16, device=a.device)
     fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, OUT_F32 if out_f32 else OUT_BF16, stream)
     return d
+
+
+def rope_table(n_pos, rot, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, turns_hi=32.0, mscale=1.0,
+               device="cuda", stream=None):
+    """Angles of positions 0 .. n_pos-1 for heads with `rot` rotated dims:
+    factor stretches positions (orig_len = 0) or, with orig_len the trained
+    length, only the slow pairs (by parts)."""
+    import torch
+    cs = torch.empty((n_pos, rot), dtype=torch.float32, device=device)
+    fp8bs_rope_table(cs, base, factor, orig_len, turns_lo, turns_hi, mscale, stream)
+    return cs
+
+
+def rope(x, pos, cs, rot_offset=0, layout="half", inverse=False, stream=None):
+    """x bf16 [T][H][D] rotated (inverse: the gradient)."""
+    import torch
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    fp8bs_rope(x, y, pos, rot_offset, layout, inverse, cs, stream)
+    return y
+
+
+def paged_cache(n_pages, heads, page, dim, device="cuda"):
+    """An empty cache: (kc, ks, vc, vs) for n_pages pages of `page` tokens."""
+    import torch
+    kc = torch.zeros((n_pages, heads, page, dim), dtype=torch.uint8, device=device)
+    ks = torch.zeros((n_pages, heads), dtype=torch.float32, device=device)
+    return kc, ks, torch.zeros_like(kc), torch.zeros_like(ks)
+
+
+def kv_append(k, v, kc, ks, vc, vs, table, kv_len, q_off, max_q, q=None, cs=None, rot_offset=0, layout="half",
+              stream=None):
+    """Appends k, v [T][Hkv][D] to the cache (keys rotated when cs is given);
+    returns the rotated queries when q is given."""
+    import torch
+    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    fp8bs_kv_append(q, q_out, k, v, cs, rot_offset, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream)
+    return q_out
+
+
+def _scratch(nbytes, device, stream):
+    """Working memory that belongs to the stream it is used on, so that it is
+    not handed out again before that stream is done with it."""
+    import torch
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(on):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
+def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None, causal=True, window=0,
+               with_lse=False, ws=None, stream=None):
+    """Attention of q bf16 [T][Hq][D] over the cache; scale None: D^-1/2.
+    The working memory is allocated unless given."""
+    import torch
+    T, Hq, D = q.shape
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+    if ws is None:
+        need = fp8bs_attn_paged_ws(table.shape[0], T, max_q, Hq, kc.shape[1], D, table.shape[1], kc.shape[2])
+        if need > 0:
+            ws = _scratch(need, q.device, stream)
+    fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs,
+                     D ** -0.5 if scale is None else scale, causal, window, ws, stream)
+    return (out, lse) if with_lse else out

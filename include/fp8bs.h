@@ -322,6 +322,138 @@ fp8bs_status fp8bs_grouped_gemm(const uint8_t *a, const float *sa, int64_t ldsa,
                                 void *d, fp8bs_out_dtype dt, int64_t N, int64_t K,
                                 void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention over a paged E4M3 cache.
+ *
+ * Between a layer's QKV projection and its output projection a serving
+ * program rotates queries and keys by their positions, appends keys and
+ * values to a cache, and attends over that cache.  The cache is held in this
+ * library's format: E4M3 codes with an FP32 scale for each block, a block
+ * being the tokens of one page for one key/value head.
+ *
+ *   kc, vc  u8  [n_pages][Hkv][page][D]   codes (dense, 16-byte aligned)
+ *   ks, vs  f32 [n_pages][Hkv]            scales (dense); a value is dec(code) * scale
+ *   table   i32 [B][ldt]                  the pages of sequence b in order; entry j
+ *                                         holds its tokens page*j .. page*j + page - 1
+ *   kv_len  i32 [B]                       tokens of sequence b in the cache, the
+ *                                         call's own tokens included (they are the last)
+ *   q_off   i32 [B+1] or NULL             packed rows of the call: sequence b owns rows
+ *                                         q_off[b] .. q_off[b+1]-1 of T, non-decreasing,
+ *                                         q_off[0] = 0, q_off[B] = T; NULL: one row each
+ *                                         (T == B)
+ * Row i of sequence b is its token at position kv_len[b] - n_b + i, n_b its
+ * rows.  max_q bounds the rows of any one sequence (the host sizes launches
+ * with it; rows past it are left unwritten).  table, kv_len and q_off are in
+ * DEVICE memory and not checked: lengths are cut to what table holds
+ * (max_pages * page), page numbers outside 0 .. n_pages-1 are never followed, so wrong
+ * contents give unspecified results but no access out of bounds.
+ * page is 16, 32, 64 or 128; D is 64 or 128.
+ * ---------------------------------------------------------------------- */
+
+typedef enum {
+    FP8BS_ROPE_HALF = 0,        /* pairs (i, i + rot/2) */
+    FP8BS_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1) */
+} fp8bs_rope_layout;
+
+/*
+ * Table of the rotary angles: cs f32 [n_pos][rot], row p = cos of the rot/2
+ * angles of position p, then their sines, both times mscale.
+ *   f_i = base^(-2 i / rot), angle = p * f_i'
+ *   orig_len == 0: f_i' = f_i / factor (positions interpolated; factor 1:
+ *                  the plain table)
+ *   orig_len > 0:  by parts: with r = orig_len f_i / (2 pi), the turns the
+ *                  pair makes over the trained context, and
+ *                  w = clamp((r - turns_lo) / (turns_hi - turns_lo), 0, 1):
+ *                  f_i' = (1 - w) f_i / factor + w f_i
+ *                  (the blend of "YaRN: Efficient Context Window Extension
+ *                  of Large Language Models", 2023)
+ * Computed in binary64 and rounded once.  n_pos >= 0 (0 is a no-op), rot a
+ * multiple of 16 up to 512, else FP8BS_ERR_UNSUPPORTED_SHAPE; base > 0,
+ * factor > 0, with orig_len > 0 also turns_hi > turns_lo, all finite, else
+ * FP8BS_ERR_INVALID_ARG.  cs 16-byte aligned.
+ */
+fp8bs_status fp8bs_rope_table(float *cs, int64_t n_pos, int64_t rot, double base, double factor,
+                              double orig_len, double turns_lo, double turns_hi, double mscale,
+                              void *stream);
+
+/*
+ * Rotary positions: dims rot_off .. rot_off + rot - 1 of every head rotated
+ * in pairs by the angles of the row's position, the others copied.
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s    (FP32, each product and each sum
+ *                                          rounded, the result rounded once)
+ * inverse != 0 turns by the negative angles: the gradient of the rotation.
+ *   x    bf16 [T][ldx]   row t holds H heads of D values
+ *   y    bf16 [T][ldy]   may be x itself (then the other dims stay), else
+ *                        must not overlap it
+ *   pos  i32 [T]         device memory; cut to 0 .. n_pos-1
+ *   cs   f32 [n_pos][rot]  of fp8bs_rope_table (dense, 16-byte aligned)
+ * T >= 0 (0 is a no-op), H > 0; D % 16 == 0, rot % 16 == 0, rot_off % 8 == 0,
+ * rot_off + rot <= D <= 512, else FP8BS_ERR_UNSUPPORTED_SHAPE.
+ */
+fp8bs_status fp8bs_rope(const void *x, int64_t ldx, void *y, int64_t ldy, const int32_t *pos, int64_t T,
+                        int64_t H, int64_t D, int64_t rot, int64_t rot_off, fp8bs_rope_layout layout,
+                        int inverse, const float *cs, int64_t n_pos, void *stream);
+
+/*
+ * Append to the cache: the call's keys (rotated to their positions in FP32)
+ * and values are quantized into their pages; the call's queries can be
+ * rotated in the same launch.
+ * A block that already held tokens keeps its scale s unless the new tokens
+ * need a larger one: s' = max(s, fl32(amax(new) / 448)).  Where s' > s its
+ * earlier codes become the nearest-even E4M3 of fl32(dec(code) * s) / s';
+ * new codes are the nearest-even E4M3 of x / s' ([p1] para 3: the tile's
+ * max-abs taken online).  A block whose first token arrives ignores what its
+ * codes and scale held.  Codes past the last token stay as they were.
+ *   q    bf16 [T][ldq] or NULL   q_out bf16 [T][ldqo]   Hq heads of D; q_out may be q
+ *   k, v bf16 [T][ldk], [T][ldv] Hkv heads of D
+ *   cs   f32 [n_pos][rot] or NULL (no rotation; q must then be NULL);
+ *        positions are cut to 0 .. n_pos-1; rot, rot_off and layout as for fp8bs_rope
+ *   q_off, kv_len, table, kc, ks, vc, vs: see above; a page is named by one
+ *        sequence of the call at most
+ * T >= 0 and B >= 0 (either 0 is a no-op), Hkv > 0.
+ */
+fp8bs_status fp8bs_kv_append(const void *q, int64_t ldq, void *q_out, int64_t ldqo, int64_t Hq,
+                             const void *k, int64_t ldk, const void *v, int64_t ldv, int64_t Hkv, int64_t D,
+                             const float *cs, int64_t n_pos, int64_t rot, int64_t rot_off,
+                             fp8bs_rope_layout layout, const int32_t *q_off, const int32_t *kv_len, int64_t B,
+                             int64_t T, int64_t max_q, const int32_t *table, int64_t ldt, int64_t max_pages,
+                             int64_t page, uint8_t *kc, float *ks, uint8_t *vc, float *vs, int64_t n_pages,
+                             void *stream);
+
+/*
+ * Attention of packed queries over the cache, from one token a sequence to
+ * whole prompts, grouped heads (Hq a multiple of Hkv; query head h reads
+ * key/value head h / (Hq / Hkv)).
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = e^(scale q.k_j)
+ * over the keys a row sees: j < kv_len; with causal != 0 j <= its position;
+ * with window > 0 j > its position - window.  A row that sees nothing gives
+ * zeros (and lse = -infinity).
+ *   q    bf16 [T][ldq]    out bf16 [T][ldo]   Hq heads of D
+ *   lse  f32 [T][ldl] or NULL  log of sum_j p_j, a value a head
+ *   scale > 0 and finite
+ *   ws   device memory of fp8bs_attn_paged_ws(...) bytes, 16-byte aligned
+ *        (may be NULL where that is 0); its contents need no preparation and are
+ *        unspecified afterwards
+ * Scores are FP32 sums of exact products; the softmax's maximum, its sum and
+ * the output sums are held in FP32; each weight is rounded to FP16 for the
+ * product with the values (codes are exact in FP16), the output once to
+ * BF16.  Results do not depend on the order in which the GPU runs: equal
+ * calls give equal bits.  Value scales below 2^-100 are taken as 2^-100.
+ * T >= 0 and B >= 0 (either 0 is a no-op), Hkv > 0, Hq % Hkv == 0,
+ * Hq / Hkv <= 1024, window >= 0.
+ */
+fp8bs_status fp8bs_attn_paged(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int64_t ldl,
+                              const int32_t *q_off, const int32_t *kv_len, int64_t B, int64_t T, int64_t max_q,
+                              int64_t Hq, int64_t Hkv, int64_t D, const int32_t *table, int64_t ldt,
+                              int64_t max_pages, int64_t page, const uint8_t *kc, const float *ks,
+                              const uint8_t *vc, const float *vs, int64_t n_pages, float scale, int causal,
+                              int64_t window, void *ws, int64_t ws_bytes, void *stream);
+
+/* Bytes of working memory that fp8bs_attn_paged needs for these sizes (0 to
+ * a few times 10^7), or -1 where a size is invalid. */
+int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
+                            int64_t max_pages, int64_t page);
+
 /* Human-readable name of a status code (static storage). */
 const char *fp8bs_status_string(fp8bs_status st);
 

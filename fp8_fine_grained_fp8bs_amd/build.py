@@ -23,8 +23,8 @@ LIB = os.path.join(PKG, "libfp8bs.so")
 # debug build for race checks: kernels fill their LDS with 0xFF before use
 POISON_LIB = os.path.join(PKG, "libfp8bs_poison.so")
 SOURCES = ["api.hip", "quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "e5m6.hip", "swiglu.hip",
-           "rope.hip", "kv_append.hip", "attn.hip"]
-LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip"]   # the sources whose kernels use LDS
+           "rope.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]
+LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]   # the sources whose kernels use LDS
 ARCH = "gfx950"
 
 

@@ -28,49 +28,10 @@
 // D/16 dims and transposes bytes in registers (2 v_perm_b32 a dword).
 #include <hip/hip_runtime.h>
 
-#include "attn_sched.h"
+#include "attn_device.h"
 
 namespace fp8bs {
 namespace {
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr float kNoKeys = -1e30f;       // reference of a row that has seen no key yet
-constexpr float kHeadroom = 15.0f;      // log2 of the largest p' before the reference moves
-constexpr float kTop = 8.0f;            // log2 of the largest p' after a move
-constexpr float kMinVScale = 0x1p-100f;
-
-// Eight codes (two dwords) to eight BF16 / FP16 values, exact.
-__device__ __forceinline__ bf16x8 bf16_of_codes(uint32_t a, uint32_t b) {
-  const u32x4 w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true))};
-  return __builtin_bit_cast(bf16x8, w);
-}
-__device__ __forceinline__ f16x8 f16_of_codes(uint32_t a, uint32_t b) {
-  const u32x4 w = {__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true))};
-  return __builtin_bit_cast(f16x8, w);
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), f16x2));
-}
-
-// A 4x4 byte transpose: r[i] holds byte i of a, b, c, d.
-__device__ __forceinline__ void transpose4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t r[4]) {
-  const uint32_t x = __builtin_amdgcn_perm(b, a, 0x05010400u), y = __builtin_amdgcn_perm(b, a, 0x07030602u);
-  const uint32_t z = __builtin_amdgcn_perm(d, c, 0x05010400u), w = __builtin_amdgcn_perm(d, c, 0x07030602u);
-  r[0] = __builtin_amdgcn_perm(z, x, 0x05040100u);
-  r[1] = __builtin_amdgcn_perm(z, x, 0x07060302u);
-  r[2] = __builtin_amdgcn_perm(w, y, 0x05040100u);
-  r[3] = __builtin_amdgcn_perm(w, y, 0x07060302u);
-}
 
 // What a wave holds of one step of 32 keys.
 template <int D>
@@ -86,50 +47,23 @@ struct Pages {
 };
 
 template <int D, int NR>
-__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
   constexpr int R = 16 * NR, VW = D / 16, NW = D / 64;
   __shared__ __attribute__((aligned(16))) float obuf[4][16][D + 4];
   __shared__ float ml[4][16][2];
-  __shared__ int64_t prefix[kMaxSlots + 1];
-  __shared__ int64_t sums[4];
+  static_assert(sizeof(obuf) >= kMaxSlots * sizeof(int), "the line's prefix sums fit");
+  __shared__ int sums[4];
   poison_lds<sizeof(obuf)>(obuf);
-  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = tid >> 6;
+  const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = uniform(tid >> 6);
   const int m16 = lane & 15, g = lane >> 4;
   const int page_mask = (1 << a.pshift) - 1;
 
-  Line line;
-  int64_t cur, stop;
-  int slot, h, w;
-  if (a.workers != 0) {
-    line = make_line(a, R, prefix, sums);
-    w = xcd_order(blockIdx.x, gridDim.x);
-    if (tid == 0) a.rec[w * 8] = 0;
-    if (w >= line.workers) return;
-    cur = stretch_begin(line, w);
-    stop = stretch_begin(line, w + 1);
-    h = static_cast<int>(cur / line.per_head);
-    slot = slot_of(a, line, cur - h * line.per_head);
-  } else {
-    w = blockIdx.x;
-    h = w / a.slots;
-    slot = w - h * a.slots;
-    cur = 0;
-    stop = 1;
-  }
-
-  while (cur < stop) {
-    const Tile t = tile_of(a, slot, R);
-    int ub = 0, ue = t.units;   // the piece: units ub .. ue - 1 of the item
-    if (a.workers != 0) {
-      const int64_t first = h * line.per_head + line.prefix[slot];
-      ub = static_cast<int>(cur - first);
-      if (stop - first < ue) ue = static_cast<int>(stop - first);
-      cur = first + ue;
-    } else {
-      cur = stop;
-      if (t.units == 0) return;
-    }
-    const bool whole = ub == 0 && ue == t.units;
+  Cursor c;
+  if (!begin_work(a, R, false, obuf, sums, c)) return;
+  while (c.cur < c.stop) {
+    take_piece(c);
+    const Tile& t = c.t;
+    const int h = c.h;
 
     // queries: the B operand, row m16 of each 16-row group
     bf16x8 qf[NR][2 * NW];
@@ -168,8 +102,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_rows_kernel(AttnArg
 
     const int32_t* table = a.p.table + t.b * a.p.ldt;
     const int last_page = static_cast<int>(a.p.max_pages) - 1;
-    const int base = (t.u0 + ub) * kUnit;
-    int steps = (ue - ub) * (kUnit / 32);
+    const int base = (t.u0 + c.ub) * kUnit;
+    int steps = (c.ue - c.ub) * (kUnit / 32);
     if (base + 32 * steps > t.hi) steps = t.hi > base ? (t.hi - base + 31) / 32 : 0;
     auto clamp_page = [&](int id) {
       const unsigned u = static_cast<unsigned>(id), n = static_cast<unsigned>(a.p.n_pages) - 1u;
@@ -194,15 +128,15 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_rows_kernel(AttnArg
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 0; c < NW; ++c) x.k[i][c] = *reinterpret_cast<const u32x4*>(pk + 4 * i * D + 64 * c);
+        for (int c = 0; c < NW; ++c) x.k[i][c] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(pk + 4 * i * D + 64 * c));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (NW == 2) {
-          const u32x2 y = *reinterpret_cast<const u32x2*>(pv + j * D);
+          const u32x2 y = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(pv + j * D));
           x.v[j][0] = y[0];
           x.v[j][NW - 1] = y[1];
         } else {
-          x.v[j][0] = *reinterpret_cast<const uint32_t*>(pv + j * D);
+          x.v[j][0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(pv + j * D));
         }
       }
       x.ks = a.p.ks[bv];
@@ -348,58 +282,56 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void attn_rows_kernel(AttnArg
       }
       const int tr = 16 * r + row;
       if (tr < t.rows) {
-        if (whole) store_out<VW>(a, row_token(a, t, tr), row_head(a, t, h, tr), D, d0, sum, top, den);
-        else store_part<VW>(a.part, R, D, 2 * static_cast<int64_t>(w) + (ub == 0 ? 1 : 0), tr, d0, sum, top, den);
+        if (c.whole) store_out<VW>(a, row_token(a, t, tr), row_head(a, t, h, tr), D, d0, sum, top, den);
+        else store_part<VW>(a.part, R, D, piece_of(c), tr, d0, sum, top, den);
       }
     }
-    if (a.workers != 0) {
-      if (!whole && ub == 0 && tid == 0) {
-        // this worker starts the item: it records who holds the rest
-        const int64_t end = cur - ue + t.units;
-        int32_t* rec = a.rec + w * 8;
-        rec[1] = slot;
-        rec[2] = h;
-        rec[3] = worker_of(line, end - 1) - w;
-        rec[0] = 1;
-      }
-      // the next item with units
-      do {
-        if (++slot == a.slots) {
-          slot = 0;
-          ++h;
-        }
-      } while (cur < stop && line.prefix[slot + 1] == line.prefix[slot]);
-    }
+    end_piece(a, R, c);
   }
 }
 
-// Joins the partials of the item that worker blockIdx.x began: 16 rows a
-// workgroup (blockIdx.y), thread (row, D/16 dims), in the workers' order.
-template <int D>
+// Joins the partials of item (or of the item that worker) blockIdx.x began.
+// A workgroup takes 16 / PG rows (blockIdx.y): a thread D/16 dims of a row and
+// every PG-th piece, all of them in flight at once; the groups' results are
+// joined through LDS in their order.  PG = 16 where a few items were shared
+// among many workers, PG = 1 where pieces are few.
+template <int D, int PG>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
-  constexpr int VW = D / 16;
-  const int w = blockIdx.x;
-  const int32_t* rec = a.rec + w * 8;
-  if (rec[0] == 0) return;
-  const int slot = rec[1], h = rec[2], more = rec[3];
-  const Tile t = tile_of(a, slot, R);
-  const int r = static_cast<int>(blockIdx.y) * 16 + (static_cast<int>(threadIdx.x) >> 4);
-  if (r >= t.rows) return;
-  const int d0 = (static_cast<int>(threadIdx.x) & 15) * VW;
+  constexpr int VW = D / 16, ROWS = 16 / PG;
+  __shared__ float part[PG][ROWS][16][VW + 2];
+  poison_lds<sizeof(part)>(part);
+  const int tid = static_cast<int>(threadIdx.x);
+  const int32_t* rec = a.rec + static_cast<int64_t>(blockIdx.x) * 4;
+  Tile t;
+  int h;
+  if (a.by_item) {   // a slot without rows has no record
+    h = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.slots));
+    t = tile_at(a, place_of<true>(a, static_cast<int>(blockIdx.x) - h * a.slots, R), R);
+    if (t.units == 0 || rec[0] == 0) return;
+  } else {
+    if (rec[0] == 0) return;
+    h = uniform(rec[2]);
+    t = tile_at(a, place_of<true>(a, uniform(rec[1]), R), R);
+  }
+  const int pieces = uniform(rec[0]), w = uniform(rec[3]);
+  const int c16 = tid & 15, lr = (tid >> 4) % ROWS, grp = (tid >> 4) / ROWS;
+  const int r = static_cast<int>(blockIdx.y) * ROWS + lr, d0 = c16 * VW;
+  if (static_cast<int>(blockIdx.y) * ROWS >= t.rows) return;
+  const int rr = r < t.rows ? r : 0;
   const int64_t size = static_cast<int64_t>(R) * (D + 2);
   float sum[VW], top = kNoKeys, den = 0.0f;
 #pragma unroll
   for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
 #pragma unroll 4
-  for (int k = 0; k <= more; ++k) {
+  for (int k = grp; k < pieces; k += PG) {
     const float* piece = a.part + (2 * static_cast<int64_t>(w + k) + (k == 0 ? 1 : 0)) * size;
-    const float m = piece[R * D + 2 * r], l = piece[R * D + 2 * r + 1];
+    const float m = piece[R * D + 2 * rr], l = piece[R * D + 2 * rr + 1];
     const float to = __builtin_fmaxf(top, m);
     const float f = __builtin_amdgcn_exp2f(top - to), g = __builtin_amdgcn_exp2f(m - to);
     den = __builtin_fmaf(g, l, den * f);
 #pragma unroll
     for (int i = 0; i < VW / 4; ++i) {
-      const float4 x = *reinterpret_cast<const float4*>(piece + r * D + d0 + 4 * i);
+      const float4 x = *reinterpret_cast<const float4*>(piece + rr * D + d0 + 4 * i);
       sum[4 * i] = __builtin_fmaf(g, x.x, sum[4 * i] * f);
       sum[4 * i + 1] = __builtin_fmaf(g, x.y, sum[4 * i + 1] * f);
       sum[4 * i + 2] = __builtin_fmaf(g, x.z, sum[4 * i + 2] * f);
@@ -407,7 +339,27 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
     }
     top = to;
   }
-  store_out<VW>(a, row_token(a, t, r), row_head(a, t, h, r), D, d0, sum, top, den);
+  if (PG > 1) {
+    float* at = part[grp][lr][c16];
+#pragma unroll
+    for (int i = 0; i < VW; ++i) at[i] = sum[i];
+    at[VW] = top;
+    at[VW + 1] = den;
+    __syncthreads();
+    if (grp != 0) return;
+    for (int k = 0; k < PG; ++k) top = __builtin_fmaxf(top, part[k][lr][c16][VW]);
+    den = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
+    for (int k = 0; k < PG; ++k) {
+      const float* from = part[k][lr][c16];
+      const float f = __builtin_amdgcn_exp2f(from[VW] - top);
+      den = __builtin_fmaf(f, from[VW + 1], den);
+#pragma unroll
+      for (int i = 0; i < VW; ++i) sum[i] = __builtin_fmaf(f, from[i], sum[i]);
+    }
+  }
+  if (r < t.rows) store_out<VW>(a, row_token(a, t, r), row_head(a, t, h, r), D, d0, sum, top, den);
 }
 
 // Launch sizes: a function of the call's sizes alone.
@@ -417,26 +369,34 @@ struct Plan {
   int most;
   int workers;   // 0: one item a workgroup
   int min_units;
+  bool by_item;
   int64_t bytes;
 };
+
+constexpr int64_t kMaxInt = 0x7fffffff;
 
 Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
   Plan p;
   const int64_t G = Hq / Hkv, rows = max_q * G;
-  p.R = rows <= 16 ? 16 : 32;
+  p.R = rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
   const int64_t most = (rows + p.R - 1) / p.R;
-  const int64_t direct = B * most, searched = T * G / p.R + B;
+  const int64_t direct = most > kMaxInt / B ? kMaxInt : B * most, searched = T * G / p.R + B;
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  const int full = p.R == 16 ? 768 : 512;   // resident workgroups
+  const int full = 512;   // resident workgroups: two a compute unit
+  const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
+  const int64_t items = p.slots * Hkv;
+  // whole items where there are enough of them to fill the GPU several times
+  // over (and where the line cannot hold them)
+  const bool many = p.R == 128 && items >= 4 * full;
   p.workers = 0;
   p.bytes = 0;
-  if (p.slots <= kMaxSlots) {
-    const int64_t units = (max_pages * page + kUnit - 1) / kUnit;
-    const int64_t useful = p.slots * Hkv * ((units + p.min_units - 1) / p.min_units);
+  p.by_item = items <= full;
+  if (p.slots <= kMaxSlots && !many && items <= kMaxInt / units) {
+    const int64_t useful = items * ((units + p.min_units - 1) / p.min_units);
     p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
-    p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 8 * static_cast<int64_t>(p.workers)) * 4;
+    p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 4 * full) * 4;
   }
   return p;
 }
@@ -455,12 +415,13 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
   a.pshift = __builtin_ctz(static_cast<unsigned>(p.page));
   a.max_len = static_cast<int>(p.max_pages * p.page);
   a.scale_log2 = static_cast<float>(static_cast<double>(p.scale) * 1.4426950408889634);
-  const int64_t blocks = plan.workers != 0 ? plan.workers : plan.slots * p.Hkv;
+  const int64_t blocks = plan.workers != 0 ? plan.workers : (plan.slots * p.Hkv + 7) / 8 * 8;
   if (blocks > 0x7fffffff || plan.slots > 0x7fffffff) return hipErrorInvalidValue;
   a.slots = static_cast<int>(plan.slots);
   a.most = plan.most;
   a.workers = plan.workers;
   a.min_units = plan.min_units;
+  a.by_item = plan.by_item;
   a.part = static_cast<float*>(p.ws);
   a.rec = reinterpret_cast<int32_t*>(a.part + 2 * static_cast<int64_t>(plan.workers) * plan.R * (p.D + 2));
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
@@ -471,11 +432,18 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
   FP8BS_ROWS(128, 1);
   FP8BS_ROWS(128, 2);
 #undef FP8BS_ROWS
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = plan.R == 128 ? launch_attn_prompt(a, static_cast<unsigned>(blocks), st) : hipGetLastError();
   if (e != hipSuccess || plan.workers == 0) return e;
-  const dim3 jgrid(static_cast<unsigned>(plan.workers), static_cast<unsigned>(plan.R / 16));
-  if (p.D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), jgrid, block, 0, st, a, plan.R);
-  else hipLaunchKernelGGL((attn_join_kernel<128>), jgrid, block, 0, st, a, plan.R);
+  const int64_t items = plan.slots * p.Hkv, joins = plan.by_item ? items : plan.workers;
+  // pieces an item on average decide how a workgroup's threads are split
+  const bool deep = items * 8 <= plan.workers;
+  const dim3 jgrid(static_cast<unsigned>(joins), static_cast<unsigned>(deep ? plan.R : plan.R / 16));
+#define FP8BS_JOIN(D_, PG_) hipLaunchKernelGGL((attn_join_kernel<D_, PG_>), jgrid, block, 0, st, a, plan.R)
+  if (p.D == 64 && deep) FP8BS_JOIN(64, 16);
+  else if (p.D == 64) FP8BS_JOIN(64, 1);
+  else if (deep) FP8BS_JOIN(128, 16);
+  else FP8BS_JOIN(128, 1);
+#undef FP8BS_JOIN
   return hipGetLastError();
 }
 

@@ -32,30 +32,49 @@ struct AttnArgs {
   int most;           // tiles a sequence where slots are split directly, else 0
   int workers;        // 0: one item a workgroup, whole
   int min_units;      // least stretch of a worker
+  bool by_item;       // records are numbered by item, else by worker
   float* part;        // partials: [2 workers][R][D + 2]
-  int32_t* rec;       // records: [workers][8]
+  int32_t* rec;       // records: [items or workers][4]
 };
 
+// The many-rows kernel on `blocks` workgroups (a multiple of 8).
+hipError_t launch_attn_prompt(const AttnArgs& a, unsigned blocks, hipStream_t st);
+
+// A value that every lane of the wave has, kept in a scalar register (a load
+// gives the compiler no way to know).
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// A tile's place, and what the device memory says of its sequence.
+struct Place {
+  int b, rt;      // sequence, tile of the sequence
+  int off, n;     // first packed row, rows of tokens
+  int len;        // tokens in the cache
+};
 struct Tile {
   int b;
-  int n;        // rows of tokens: the call's tokens of the sequence
-  int64_t off;  // first packed row
+  int n;          // the call's tokens of the sequence
+  int off;        // first packed row
   int row0, rows;
   int len;
-  int lo, hi;   // keys seen by any row
+  int lo, hi;     // keys seen by any row
   int u0, units;
 };
 
-__device__ __forceinline__ Tile tile_of(const AttnArgs& a, int slot, int R) {
-  Tile t;
-  int rt;
-  if (a.most != 0) {
-    t.b = slot / a.most;
-    rt = slot - t.b * a.most;
+// SAME: every lane asks for the same slot.
+template <bool SAME>
+__device__ __forceinline__ Place place_of(const AttnArgs& a, int slot, int R) {
+  auto same = [](int x) { return SAME ? uniform(x) : x; };
+  Place p;
+  if (a.most == 1) {
+    p.b = slot;
+    p.rt = 0;
+  } else if (a.most != 0) {
+    p.b = static_cast<int>(static_cast<unsigned>(slot) / static_cast<unsigned>(a.most));
+    p.rt = slot - p.b * a.most;
   } else {
     // tiles of b <= floor(n_b G / R) + 1: numbered from floor(q_off[b] G / R) + b
     auto key = [&](int i) {
-      const int64_t o = a.p.q_off == nullptr ? i : a.p.q_off[i];
+      const int64_t o = a.p.q_off == nullptr ? i : same(a.p.q_off[i]);
       return o * a.G / R + i;
     };
     int lo = 0, hi = a.p.B - 1;
@@ -64,43 +83,54 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs& a, int slot, int R) {
       if (key(mid) <= slot) lo = mid;
       else hi = mid - 1;
     }
-    t.b = lo;
-    rt = static_cast<int>(slot - key(lo));
+    p.b = lo;
+    p.rt = static_cast<int>(slot - key(lo));
   }
-  int64_t o = t.b, e = t.b + 1;
+  int o = p.b, e = p.b + 1, len = a.p.kv_len[p.b];
   if (a.p.q_off != nullptr) {
-    o = a.p.q_off[t.b];
-    e = a.p.q_off[t.b + 1];
-    o = o < 0 ? 0 : o > a.p.T ? a.p.T : o;
-    e = e < o ? o : e > a.p.T ? a.p.T : e;
+    o = a.p.q_off[p.b];
+    e = a.p.q_off[p.b + 1];
   }
-  t.off = o;
-  t.n = static_cast<int>(e - o);
-  const int64_t all = static_cast<int64_t>(t.n) * a.G, first = static_cast<int64_t>(rt) * R;
-  if (rt < 0 || first >= all) {
+  const int T = static_cast<int>(a.p.T);
+  o = same(o);
+  e = same(e);
+  len = same(len);
+  p.off = o < 0 ? 0 : o > T ? T : o;
+  e = e < p.off ? p.off : e > T ? T : e;
+  p.n = e - p.off;
+  p.len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
+  return p;
+}
+
+__device__ __forceinline__ Tile tile_at(const AttnArgs& a, const Place& p, int R) {
+  Tile t;
+  t.b = p.b;
+  t.off = p.off;
+  t.n = p.n;
+  const int64_t all = static_cast<int64_t>(p.n) * a.G, first = static_cast<int64_t>(p.rt) * R;
+  if (p.rt < 0 || first >= all) {
     t.row0 = t.rows = t.len = t.lo = t.hi = t.u0 = t.units = 0;
     return t;
   }
   t.row0 = static_cast<int>(first);
   t.rows = static_cast<int>(all - first < R ? all - first : R);
-  int len = a.p.kv_len[t.b];
-  len = len < 0 ? 0 : len > a.max_len ? a.max_len : len;
-  t.len = len;
-  const int64_t p0 = static_cast<int64_t>(len) - t.n + t.row0 / a.G;
-  const int64_t p1 = static_cast<int64_t>(len) - t.n + (t.row0 + t.rows - 1) / a.G;
-  const int64_t hi = a.p.causal && p1 + 1 < len ? p1 + 1 : len;
+  t.len = p.len;
+  const unsigned G = static_cast<unsigned>(a.G);
+  const int64_t p0 = static_cast<int64_t>(p.len) - p.n + static_cast<unsigned>(t.row0) / G;
+  const int64_t p1 = static_cast<int64_t>(p.len) - p.n + static_cast<unsigned>(t.row0 + t.rows - 1) / G;
+  const int64_t hi = a.p.causal && p1 + 1 < p.len ? p1 + 1 : p.len;
   const int64_t lo = a.p.window > 0 && p0 - a.p.window + 1 > 0 ? p0 - a.p.window + 1 : 0;
   const bool some = hi > lo;
   t.lo = some ? static_cast<int>(lo) : 0;
   t.hi = some ? static_cast<int>(hi) : 0;
   t.u0 = t.lo / kUnit;
-  t.units = some ? (t.hi + kUnit - 1) / kUnit - t.u0 : 1;   // rows that see nothing still get their zeros
+  t.units = some ? (t.hi - 1) / kUnit + 1 - t.u0 : 1;   // rows that see nothing still get their zeros
   return t;
 }
 
 // Keys that one row sees.
 __device__ __forceinline__ void row_keys(const AttnArgs& a, const Tile& t, int row, int& lo, int& hi) {
-  const int64_t p = static_cast<int64_t>(t.len) - t.n + row / a.G;
+  const int64_t p = static_cast<int64_t>(t.len) - t.n + static_cast<unsigned>(row) / static_cast<unsigned>(a.G);
   const int64_t h = a.p.causal && p + 1 < t.len ? p + 1 : t.len;
   const int64_t l = a.p.window > 0 && p - a.p.window + 1 > 0 ? p - a.p.window + 1 : 0;
   hi = h < 0 ? 0 : static_cast<int>(h);
@@ -111,72 +141,164 @@ __device__ __forceinline__ void row_keys(const AttnArgs& a, const Tile& t, int r
 // XCD's L2 are consecutive.  n is a multiple of 8.
 __device__ __forceinline__ int xcd_order(int bid, int n) { return (bid & 7) * (n >> 3) + (bid >> 3); }
 
-// The line of units: prefix sums over one head's slots.
-struct Line {
-  int64_t* prefix;   // LDS [slots + 1]
-  int64_t per_head;
-  int64_t total;
-  int workers;       // workers with a stretch
+// Inclusive sum over the lanes up to this one (DPP row shifts, then the two
+// row broadcasts).
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);   // row_shr:1
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+
+// A worker's way along the line.  The first `longer` workers have q + 1
+// units, the others q.  All of it fits 32 bits (the host sees to that).
+struct Cursor {
+  int q, longer;
+  int w;              // worker, or item where items are whole
+  int slot, h;        // the item
+  int cur, stop;      // what is left of the stretch
+  int first;          // the item's first unit
+  Tile t;             // the item's tile
+  int ub, ue;         // the piece: units ub .. ue - 1 of the item
+  bool whole;
 };
 
-// Fills the line; every thread of a 256-thread workgroup calls it.
-__device__ __forceinline__ Line make_line(const AttnArgs& a, int R, int64_t* prefix, int64_t* wave_sums) {
+__device__ __forceinline__ int stretch_begin(const Cursor& c, int w) { return w * c.q + (w < c.longer ? w : c.longer); }
+// The worker whose stretch holds unit x.
+__device__ __forceinline__ int worker_of(const Cursor& c, int x) {
+  const int head = c.longer * (c.q + 1);
+  return x < head ? static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(c.q + 1))
+                  : c.longer + static_cast<int>(static_cast<unsigned>(x - head) / static_cast<unsigned>(c.q));
+}
+
+// Shares a line of per_head units a head; false where this worker has none.
+__device__ __forceinline__ bool share_line(const AttnArgs& a, int per_head, Cursor& c, int& in_head) {
+  const unsigned total = static_cast<unsigned>(per_head) * static_cast<unsigned>(a.p.Hkv);
+  const unsigned useful = (total + static_cast<unsigned>(a.min_units) - 1u) / static_cast<unsigned>(a.min_units);
+  const unsigned workers = useful < static_cast<unsigned>(a.workers) ? useful : static_cast<unsigned>(a.workers);
+  if (static_cast<unsigned>(c.w) >= workers) return false;
+  c.q = static_cast<int>(total / workers);
+  c.longer = static_cast<int>(total - static_cast<unsigned>(c.q) * workers);
+  c.cur = stretch_begin(c, c.w);
+  c.stop = stretch_begin(c, c.w + 1);
+  c.h = static_cast<int>(static_cast<unsigned>(c.cur) / static_cast<unsigned>(per_head));
+  in_head = c.cur - c.h * per_head;
+  return true;
+}
+
+// Finds the worker's first item; false where it has none.  lds: at least
+// kMaxSlots words, free again on return.  backwards: whole items are dealt
+// from the last tile (a causal prompt's longest) on.
+__device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwards, void* lds, int* sums, Cursor& c) {
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63;
+  c.w = xcd_order(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  if (a.workers == 0) {
+    c.h = static_cast<int>(static_cast<unsigned>(c.w) / static_cast<unsigned>(a.slots));
+    c.slot = c.w - c.h * a.slots;
+    if (backwards) c.slot = a.slots - 1 - c.slot;
+    if (c.h >= a.p.Hkv) return false;
+    c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
+    c.cur = c.first = 0;
+    c.stop = c.t.units;
+    return c.t.units != 0;
+  }
+  if (!a.by_item && tid == 0) a.rec[c.w * 4] = 0;
+  int in_head;
+  if (a.slots <= 64) {   // a lane a slot, every wave for itself
+    Place p{0, -1, 0, 0, 0};
+    if (lane < a.slots) p = place_of<false>(a, lane, R);
+    const int units = tile_at(a, p, R).units, upto = wave_scan(units);
+    const int per_head = __builtin_amdgcn_readlane(upto, 63);
+    if (!share_line(a, per_head, c, in_head)) return false;
+    c.slot = __popcll(__ballot(upto <= in_head));   // slots that end before: empty ones are passed over
+    const Place s{__builtin_amdgcn_readlane(p.b, c.slot), __builtin_amdgcn_readlane(p.rt, c.slot),
+                  __builtin_amdgcn_readlane(p.off, c.slot), __builtin_amdgcn_readlane(p.n, c.slot),
+                  __builtin_amdgcn_readlane(p.len, c.slot)};
+    c.t = tile_at(a, s, R);
+    c.first = c.cur - in_head + __builtin_amdgcn_readlane(upto, c.slot) - c.t.units;
+    return true;
+  }
+  // prefix sums of every slot in LDS
+  int* prefix = static_cast<int*>(lds);
   const int each = (a.slots + 255) >> 8;
-  int64_t mine = 0;
+  int mine = 0;
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
-    const int u = s < a.slots ? tile_of(a, s, R).units : 0;
-    if (s < a.slots) prefix[s] = mine;
-    mine += u;
+    if (s < a.slots) {
+      prefix[s] = mine;
+      mine += tile_at(a, place_of<false>(a, s, R), R).units;
+    }
   }
-  int64_t run = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(run, d);
-    if (lane >= d) run += o;
-  }
-  if (lane == 63) wave_sums[tid >> 6] = run;
+  const int upto = wave_scan(mine);
+  if (lane == 63) sums[tid >> 6] = upto;
   __syncthreads();
-  int64_t before = run - mine, all = 0;
+  int before = upto - mine, all = 0;
   for (int w = 0; w < 4; ++w) {
-    if (w < (tid >> 6)) before += wave_sums[w];
-    all += wave_sums[w];
+    if (w < (tid >> 6)) before += sums[w];
+    all += sums[w];
   }
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
     if (s < a.slots) prefix[s] += before;
   }
-  if (tid == 0) prefix[a.slots] = all;
   __syncthreads();
-  Line l;
-  l.prefix = prefix;
-  l.per_head = all;
-  l.total = all * a.p.Hkv;
-  const int64_t useful = (l.total + a.min_units - 1) / a.min_units;
-  l.workers = static_cast<int>(useful < a.workers ? useful : a.workers);
-  return l;
-}
-__device__ __forceinline__ int64_t stretch_begin(const Line& l, int w) { return w * l.total / l.workers; }
-// The worker whose stretch holds unit x.
-__device__ __forceinline__ int worker_of(const Line& l, int64_t x) {
-  return static_cast<int>(((x + 1) * l.workers - 1) / l.total);
-}
-// The slot whose units hold place x of a head's line.
-__device__ __forceinline__ int slot_of(const AttnArgs& a, const Line& l, int64_t x) {
-  int lo = 0, hi = a.slots - 1;   // last slot with prefix <= x (empty slots share their successor's prefix)
+  const bool some = share_line(a, uniform(all), c, in_head);
+  if (!some) return false;
+  int lo = 0, hi = a.slots - 1;   // the last slot that begins at or before it (an empty one shares its successor's place)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (l.prefix[mid] <= x) lo = mid;
+    if (prefix[mid] <= in_head) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  c.slot = uniform(lo);
+  c.first = c.cur - in_head + uniform(prefix[lo]);
+  c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
+  __syncthreads();
+  return true;
+}
+
+__device__ __forceinline__ void take_piece(Cursor& c) {
+  c.ub = c.cur - c.first;
+  const int end = c.stop - c.first;
+  c.ue = end < c.t.units ? end : c.t.units;
+  c.cur = c.first + c.ue;
+  c.whole = c.ub == 0 && c.ue == c.t.units;
+}
+
+// Where the piece's partial belongs: a worker leaves two at most, of the item
+// it ends in the middle of and of the one it begins in the middle of.
+__device__ __forceinline__ int64_t piece_of(const Cursor& c) { return 2 * static_cast<int64_t>(c.w) + (c.ub == 0 ? 1 : 0); }
+
+// Records an item that others finish and goes on to the next one.
+__device__ __forceinline__ void end_piece(const AttnArgs& a, int R, Cursor& c) {
+  if (a.workers == 0) return;
+  if (c.ub == 0 && (a.by_item || !c.whole) && threadIdx.x == 0) {
+    int32_t* rec = a.rec + 4 * (a.by_item ? c.h * a.slots + c.slot : c.w);
+    rec[0] = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;   // pieces
+    rec[1] = c.slot;
+    rec[2] = c.h;
+    rec[3] = c.w;
+  }
+  if (c.cur >= c.stop) return;
+  c.first += c.t.units;
+  do {
+    if (++c.slot == a.slots) {
+      c.slot = 0;
+      ++c.h;
+    }
+    c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
+  } while (c.t.units == 0);
 }
 
 // Where a tile row's query and output live.
-__device__ __forceinline__ int64_t row_token(const AttnArgs& a, const Tile& t, int r) { return t.off + (t.row0 + r) / a.G; }
+__device__ __forceinline__ int64_t row_token(const AttnArgs& a, const Tile& t, int r) {
+  return t.off + static_cast<int64_t>(static_cast<unsigned>(t.row0 + r) / static_cast<unsigned>(a.G));
+}
 __device__ __forceinline__ int row_head(const AttnArgs& a, const Tile& t, int h, int r) {
-  return h * a.G + (t.row0 + r) % a.G;
+  return h * a.G + static_cast<int>(static_cast<unsigned>(t.row0 + r) % static_cast<unsigned>(a.G));
 }
 
 // One finished row's 1/16th (VW = D / 16 values from dim d0) to the output.

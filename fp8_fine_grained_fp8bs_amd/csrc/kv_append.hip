@@ -96,21 +96,20 @@ __device__ __forceinline__ void load_key(const AppendArgs& a, const uint16_t* ro
   const RopeShape& r = a.rope;
   const int o = d - r.off;
   if (a.cs == nullptr || o < 0 || o >= r.rot) return;
-  float g[8];
-  if (r.interleaved) {
-    const int c = o >> 4;
-    const bool second = (o & 8) != 0;
-    const CosSin k = load_cossin(angles(a, p), r.rot, c);
+  if (r.interleaved) {   // the vector's four pairs are its own
+    const float* row_cs = angles(a, p) + (o >> 1);
+    const float4 cc = *reinterpret_cast<const float4*>(row_cs), ss = *reinterpret_cast<const float4*>(row_cs + (r.rot >> 1));
+    const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float cc = second ? k.c[4 + i] : k.c[i], ss = second ? k.s[4 + i] : k.s[i];
       const float x1 = f[2 * i], x2 = f[2 * i + 1];
-      f[2 * i] = x1 * cc - x2 * ss;
-      f[2 * i + 1] = x2 * cc + x1 * ss;
+      f[2 * i] = x1 * c4[i] - x2 * s4[i];
+      f[2 * i + 1] = x2 * c4[i] + x1 * s4[i];
     }
   } else {
     const int half = r.rot >> 1;
     const bool second = o >= half;
+    float g[8];
     unpack8(*reinterpret_cast<const uint4*>(row + (second ? d - half : d + half)), g);
     const CosSin k = load_cossin(angles(a, p), r.rot, (second ? o - half : o) >> 3);
 #pragma unroll
@@ -118,74 +117,40 @@ __device__ __forceinline__ void load_key(const AppendArgs& a, const uint16_t* ro
   }
 }
 
-// Write one block's codes: `n` = there .. end - 1 are the new tokens' places,
-// 0 .. there - 1 the old ones'.
-template <int NP, int D, typename Fetch>
-__device__ __forceinline__ void store_block(uint8_t* codes, int there, int end, float s_old, float s, Fetch fetch) {
-  const TileScale ts = scale_of(s);
+// Encodes the `there` tokens a block already holds for its larger scale.
+template <int D>
+__device__ __forceinline__ void rescale_old(uint8_t* codes, int there, float s_old, const TileScale& ts) {
   const int sub = (static_cast<int>(threadIdx.x) % (D / 8)) * 8;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = i * (2048 / D) + static_cast<int>(threadIdx.x) / (D / 8);
+  for (int r = static_cast<int>(threadIdx.x) / (D / 8); r < there; r += 2048 / D) {
     uint2* at = reinterpret_cast<uint2*>(codes + r * D + sub);
+    const uint2 c = *at;
     float f[8];
-    if (r >= there && r < end) {
-      fetch(i, f);
-    } else if (r < there && s > s_old) {
-      const uint2 c = *at;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[j] = e4m3_dec((c.x >> (8 * j)) & 0xffu) * s_old;
-        f[4 + j] = e4m3_dec((c.y >> (8 * j)) & 0xffu) * s_old;
-      }
-    } else {
-      continue;
+    for (int j = 0; j < 4; ++j) {
+      f[j] = e4m3_dec((c.x >> (8 * j)) & 0xffu) * s_old;
+      f[4 + j] = e4m3_dec((c.y >> (8 * j)) & 0xffu) * s_old;
     }
     *at = make_uint2(encode4(f, ts), encode4(f + 4, ts));
   }
 }
 
-// NP: passes of 2048 values over a block (256 threads, 8 values each).
+// NP: passes of 2048 values over a block's new tokens (256 threads, 8 values each).
 template <int D, int NP>
 __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
   __shared__ float red[2][4];
   poison_lds<sizeof(red)>(red);
   const int tid = static_cast<int>(threadIdx.x);
   int64_t bid = blockIdx.x;
-  if (bid >= a.page_blocks) {   // queries: one token and 256 units of 16 values a workgroup
-    bid -= a.page_blocks;
-    const int per = a.Hq * (D / 16);
-    const int strips = (per + 255) / 256;
-    const int64_t t = bid / strips;
-    const int e = static_cast<int>(bid - t * strips) * 256 + tid;
+  if (bid >= a.page_blocks) {   // queries: a wave a token, its lanes over units of 16 values
+    const int64_t t = (bid - a.page_blocks) * 4 + (tid >> 6);
+    if (t >= a.T) return;
     const int b = a.q_off == nullptr ? static_cast<int>(t)
                                      : search64(a.B, t, [&](int i) { return static_cast<int64_t>(a.q_off[i]); });
     int64_t off;
     int n;
     rows_of(a.q_off, a.T, b, off, n);
-    if (e >= per) return;
     const int64_t p = static_cast<int64_t>(a.kv_len[b]) - n + (t - off);
-    const int h = e / (D / 16), c = e - h * (D / 16);
-    const uint16_t* x = a.q + t * a.ldq + h * D;
-    uint16_t* y = a.qo + t * a.ldqo + h * D;
-    const RopeShape& r = a.rope;
-    if (16 * c >= r.rot) {
-      const int k = 2 * (c - r.rot / 16);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int d = 8 * (k + i);
-        if (d >= r.off) d += r.rot;
-        *reinterpret_cast<uint4*>(y + d) = *reinterpret_cast<const uint4*>(x + d);
-      }
-      return;
-    }
-    const int ia = rope_first(r, c), ib = rope_second(r, c);
-    float f[8], g[8];
-    unpack8(*reinterpret_cast<const uint4*>(x + ia), f);
-    unpack8(*reinterpret_cast<const uint4*>(x + ib), g);
-    rotate8(f, g, load_cossin(angles(a, p), r.rot, c), r.interleaved);
-    *reinterpret_cast<uint4*>(y + ia) = pack8(f);
-    *reinterpret_cast<uint4*>(y + ib) = pack8(g);
+    rotate_row<D / 16>(a.q + t * a.ldq, a.qo + t * a.ldqo, a.Hq, D, a.rope, 1.0f, angles(a, p));
     return;
   }
   const int h = static_cast<int>(bid % a.Hkv);
@@ -218,17 +183,17 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
   const int64_t blk = id * a.Hkv + h;
   const float sk_old = there > 0 ? a.ks[blk] : 0.0f, sv_old = there > 0 ? a.vs[blk] : 0.0f;
 
-  const int sub = (tid % (D / 8)) * 8, row0 = tid / (D / 8);
+  const int sub = (tid % (D / 8)) * 8, row0 = there + tid / (D / 8);
   float kf[NP][8];
   uint4 vw[NP];
   float mk = 0.0f, mv = 0.0f;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = i * (2048 / D) + row0;
-    if (r >= there && r < end) {
+    if (r < end) {
       const int64_t t = off + (base + r - start);
       load_key(a, a.k + t * a.ldk + h * D, base + r, sub, kf[i]);
-      vw[i] = *reinterpret_cast<const uint4*>(a.v + t * a.ldv + h * D + sub);
+      vw[i] = load16_nt(a.v + t * a.ldv + h * D + sub);
       float f[8];
       unpack8(vw[i], f);
 #pragma unroll
@@ -249,12 +214,21 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
   mv = __builtin_fmaxf(__builtin_fmaxf(red[1][0], red[1][1]), __builtin_fmaxf(red[1][2], red[1][3]));
   const float sk = __builtin_fmaxf(sk_old, make_tile_scale(mk).s);
   const float sv = __builtin_fmaxf(sv_old, make_tile_scale(mv).s);
-  const int64_t at = (blk << a.pshift) * D;
-  store_block<NP, D>(a.kc + at, there, end, sk_old, sk, [&](int i, float f[8]) {
+  const TileScale tk = scale_of(sk), tv = scale_of(sv);
+  uint8_t* kc = a.kc + (blk << a.pshift) * D;
+  uint8_t* vc = a.vc + (blk << a.pshift) * D;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = kf[i][j];
-  });
-  store_block<NP, D>(a.vc + at, there, end, sv_old, sv, [&](int i, float f[8]) { unpack8(vw[i], f); });
+  for (int i = 0; i < NP; ++i) {
+    const int r = i * (2048 / D) + row0;
+    if (r < end) {
+      float f[8];
+      unpack8(vw[i], f);
+      *reinterpret_cast<uint2*>(kc + r * D + sub) = make_uint2(encode4(kf[i], tk), encode4(kf[i] + 4, tk));
+      *reinterpret_cast<uint2*>(vc + r * D + sub) = make_uint2(encode4(f, tv), encode4(f + 4, tv));
+    }
+  }
+  if (sk > sk_old) rescale_old<D>(kc, there, sk_old, tk);
+  if (sv > sv_old) rescale_old<D>(vc, there, sv_old, tv);
   if (tid == 0) {
     a.ks[blk] = sk;
     a.vs[blk] = sv;
@@ -277,11 +251,12 @@ hipError_t launch_kv_append(const KvAppend& p, hipStream_t st) {
   a.most = direct <= searched ? static_cast<int>(most) : 0;
   a.slots = direct <= searched ? direct : searched;
   a.page_blocks = a.slots * p.Hkv;
-  const int64_t strips = p.q != nullptr ? (static_cast<int64_t>(p.Hq) * (p.D / 16) + 255) / 256 : 0;
-  const int64_t blocks = a.page_blocks + p.T * strips;
+  const int64_t blocks = a.page_blocks + (p.q != nullptr ? (p.T + 3) / 4 : 0);
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
-  const int np = p.page * p.D <= 2048 ? 1 : p.page * p.D / 2048;
+  // passes over the tokens that one call can add to a page
+  const int64_t adds = p.max_q < p.page ? p.max_q : p.page;
+  const int need = static_cast<int>((adds * p.D + 2047) / 2048), np = need <= 2 ? need : need <= 4 ? 4 : 8;
 #define FP8BS_APPEND(D_, NP_) \
   if (p.D == D_ && np == NP_) hipLaunchKernelGGL((kv_append_kernel<D_, NP_>), grid, block, 0, st, a)
   FP8BS_APPEND(64, 1);

@@ -37,45 +37,21 @@ __global__ __launch_bounds__(256) void rope_table_kernel(float* __restrict__ cs,
   cs[p * 2 * half + half + i] = static_cast<float>(s * mscale);
 }
 
-// One thread a unit of 16 values: a rotated unit (two vectors of 8), or two
-// vectors of the head's other dims to copy.
-__global__ __launch_bounds__(256) void rope_kernel(const uint16_t* __restrict__ x, int64_t ldx,
-                                                   uint16_t* __restrict__ y, int64_t ldy,
+// A wave a token and strip of heads.
+template <int UNITS>
+__global__ __launch_bounds__(256) void rope_kernel(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy,
                                                    const int32_t* __restrict__ pos, int64_t T, int H, int D,
                                                    RopeShape r, float sign, const float* __restrict__ cs,
-                                                   int64_t n_pos, int units) {
-  const int per = H * units;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t t = e / per;
+                                                   int64_t n_pos, int units, int strip) {
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int strips = (H + strip - 1) / strip;
+  const int64_t t = e / strips;
   if (t >= T) return;
-  const int rest = static_cast<int>(e - t * per);
-  const int h = rest / units, c = rest - h * units;
-  const uint16_t* xh = x + t * ldx + h * D;
-  uint16_t* yh = y + t * ldy + h * D;
-  if (8 * c * 2 >= r.rot) {   // copied dims: vectors 2k, 2k+1 of those around the rotated part
-    const int k = 2 * (c - r.rot / 16);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int d = 8 * (k + i);
-      if (d >= r.off) d += r.rot;
-      *reinterpret_cast<uint4*>(yh + d) = *reinterpret_cast<const uint4*>(xh + d);
-    }
-    return;
-  }
-  const int ia = rope_first(r, c), ib = rope_second(r, c);
-  const uint4 va = *reinterpret_cast<const uint4*>(xh + ia);
-  const uint4 vb = *reinterpret_cast<const uint4*>(xh + ib);
+  const int h0 = static_cast<int>(e - t * strips) * strip, heads = H - h0 < strip ? H - h0 : strip;
   int64_t p = pos[t];
   p = p < 0 ? 0 : p >= n_pos ? n_pos - 1 : p;
-  CosSin k = load_cossin(cs + p * r.rot, r.rot, c);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) k.s[i] *= sign;
-  float a[8], b[8];
-  unpack8(va, a);
-  unpack8(vb, b);
-  rotate8(a, b, k, r.interleaved);
-  *reinterpret_cast<uint4*>(yh + ia) = pack8(a);
-  *reinterpret_cast<uint4*>(yh + ib) = pack8(b);
+  rotate_row<UNITS>(x + t * ldx + static_cast<int64_t>(h0) * D, y + t * ldy + static_cast<int64_t>(h0) * D, heads, D, r,
+                    sign, cs + p * r.rot, units);
 }
 
 }  // namespace
@@ -95,11 +71,21 @@ hipError_t launch_rope(const uint16_t* x, int64_t ldx, uint16_t* y, int64_t ldy,
                        int64_t n_pos, hipStream_t st) {
   // in place the other dims stay where they are
   const int units = (x == y ? rot : D) / 16;
-  const int64_t blocks = (T * H * units + 255) / 256;
+  // a wave takes all heads of a token, unless there are too few tokens to fill
+  // the GPU: then as many heads as its lanes hold at once
+  const int at_once = units >= 64 ? 1 : 64 / units;
+  const int strip = T >= 4096 ? H : at_once;
+  const int64_t waves = T * ((H + strip - 1) / strip), blocks = (waves + 3) / 4;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const RopeShape r{rot, rot_off, interleaved};
-  hipLaunchKernelGGL(rope_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, x, ldx, y, ldy, pos, T, H,
-                     D, r, inverse ? -1.0f : 1.0f, cs, n_pos, units);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+#define FP8BS_ROPE(U) \
+  hipLaunchKernelGGL((rope_kernel<U>), grid, block, 0, st, x, ldx, y, ldy, pos, T, H, D, r, inverse ? -1.0f : 1.0f, cs, \
+                     n_pos, units, strip)
+  if (units == 8) FP8BS_ROPE(8);
+  else if (units == 4) FP8BS_ROPE(4);
+  else FP8BS_ROPE(0);
+#undef FP8BS_ROPE
   return hipGetLastError();
 }
 

@@ -72,6 +72,63 @@ __device__ __forceinline__ void rotate8(float a[8], float b[8], const CosSin& k,
   }
 }
 
+// One row's H heads of D values from x to y (may be the same), by one wave:
+// lanes over units of 16 values, rotated units first, then the head's other
+// dims to copy (units = D / 16, or rot / 16 where they stay in place).  Where
+// the units of a head divide the wave (UNITS, or 0) a lane keeps its unit from
+// head to head and its angles in registers.
+template <int UNITS>
+__device__ __forceinline__ void rotate_row(const uint16_t* x, uint16_t* y, int H, int D, const RopeShape& r, float sign,
+                                           const float* cs_row, int units_any = 0) {
+  const int lane = static_cast<int>(threadIdx.x) & 63, units = UNITS ? UNITS : units_any;
+  int h = lane / units, c = lane - h * units;
+  CosSin k;
+  if (UNITS && 16 * c < r.rot) {
+    k = load_cossin(cs_row, r.rot, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k.s[i] *= sign;
+  }
+  int ia, ib;
+  auto place = [&]() {
+    if (16 * c < r.rot) {
+      ia = rope_first(r, c);
+      ib = rope_second(r, c);
+    } else {   // vectors 2j, 2j + 1 of those around the rotated part
+      ia = 16 * (c - r.rot / 16);
+      ib = ia + 8;
+      ia += ia >= r.off ? r.rot : 0;
+      ib += ib >= r.off ? r.rot : 0;
+    }
+  };
+  if (UNITS) place();
+#pragma unroll 4
+  for (int e = lane; e < H * units; e += 64) {
+    if (UNITS) {
+      h = e / units;
+    } else {
+      h = e / units;
+      c = e - h * units;
+      place();
+    }
+    uint4 va = load16_nt(x + h * D + ia), vb = load16_nt(x + h * D + ib);
+    if (16 * c < r.rot) {
+      if (!UNITS) {
+        k = load_cossin(cs_row, r.rot, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k.s[i] *= sign;
+      }
+      float a[8], b[8];
+      unpack8(va, a);
+      unpack8(vb, b);
+      rotate8(a, b, k, r.interleaved);
+      va = pack8(a);
+      vb = pack8(b);
+    }
+    *reinterpret_cast<uint4*>(y + h * D + ia) = va;
+    *reinterpret_cast<uint4*>(y + h * D + ib) = vb;
+  }
+}
+
 // Largest b in 0 .. B-1 with key(b) <= t, for a non-decreasing key with
 // key(0) <= t: 64 probes at a time, one to a lane of the wave, so 64
 // sequences cost one load, 4096 two.  Every lane of the wave must call it.

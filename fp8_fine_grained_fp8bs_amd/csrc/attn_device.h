@@ -14,6 +14,7 @@ constexpr float kNoKeys = -1e30f;       // reference of a row that has seen no k
 constexpr float kHeadroom = 15.0f;      // log2 of the largest p' before the reference moves
 constexpr float kTop = 8.0f;            // log2 of the largest p' after a move
 constexpr float kMinVScale = 0x1p-100f;
+constexpr float kMinKScale = 0x1p-120f; // of a key block's factor, so that it keeps a masked score's -infinity
 
 // Eight codes (two dwords) to eight BF16 / FP16 values, exact.
 __device__ __forceinline__ bf16x8 bf16_of_codes(uint32_t a, uint32_t b) {

@@ -20,6 +20,8 @@
 // 4h + 0..3.  A lane pair (l, l + 32) holds a row: one exchange a moved reference.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace fp8bs {
@@ -28,6 +30,10 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kRows = 128;
+#ifndef AHEAD
+#define AHEAD 4
+#endif
+constexpr int kAhead = AHEAD;   // LDS reads in flight before their products
 
 // 16-byte chunk c of an LDS row, moved so that lanes reading the same chunk
 // of 16 neighbouring rows, and the decoding writes, spread over the banks.
@@ -40,6 +46,7 @@ template <int D>
 struct Raw {           // a thread's share of a tile on its way
   u32x4 k[D / 64];     // 16 D/64 codes of key tid / 4
   uint32_t v[D / 16];  // D/16 keys by 4 dims
+  float ks, vs;        // first wave: scales of the 16 keys from 16 (lane % 4)
 };
 
 template <int D>
@@ -97,11 +104,13 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     const int last_page = static_cast<int>(a.p.max_pages) - 1;
     const int base = (t.u0 + c.ub) * kUnit;
     const int tiles = t.hi > base ? c.ue - c.ub : 0;
-    auto block_of = [&](int key) {   // the cache block of a key, never out of range
-      int i = key >> a.pshift;
-      i = i < last_page ? i : last_page;
-      const unsigned id = static_cast<unsigned>(table[i]), n = static_cast<unsigned>(a.p.n_pages) - 1u;
-      return static_cast<int64_t>(id < n ? id : n) * a.p.Hkv + h;
+    auto page_at = [&](int key) {   // the table's entry for a key's page, never past the table
+      const int i = key >> a.pshift;
+      return table[i < last_page ? i : last_page];
+    };
+    auto block_of = [&](int id) {   // never out of range
+      const unsigned u = static_cast<unsigned>(id), n = static_cast<unsigned>(a.p.n_pages) - 1u;
+      return static_cast<int64_t>(u < n ? u : n) * a.p.Hkv + h;
     };
     // a thread's keys: one for the key tile; for the value tile those whose
     // products a lane half takes together
@@ -109,16 +118,28 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     constexpr int DQ = D / 4;                 // groups of 4 dims
     const int dq = tid % DQ, vg = tid / DQ;   // D = 128: 8 groups of 8 keys; D = 64: 16 of 4
     const int vkey = D == 128 ? 16 * (vg >> 1) + 4 * (vg & 1) : 16 * (vg >> 2) + 4 * (vg & 1) + 8 * ((vg >> 1) & 1);
-    auto load_tile = [&](int i) {
+    struct Pages {
+      int k, v, s;
+    };
+    auto load_pages = [&](int i) {
+      const int t0 = base + kUnit * i;
+      return Pages{page_at(t0 + kkey), page_at(t0 + vkey), page_at(t0 + 16 * (lane & 3))};
+    };
+    auto load_tile = [&](int i, const Pages& pg) {
       Raw<D> x;
       const int t0 = base + kUnit * i;
       const int tk = t0 + kkey, tv = t0 + vkey;
-      const uint8_t* pk = a.p.kc + ((block_of(tk) << a.pshift) + (tk & page_mask)) * D + kdim;
-      const uint8_t* pv = a.p.vc + ((block_of(tv) << a.pshift) + (tv & page_mask)) * D + 4 * dq;
+      const uint8_t* pk = a.p.kc + ((block_of(pg.k) << a.pshift) + (tk & page_mask)) * D + kdim;
+      const uint8_t* pv = a.p.vc + ((block_of(pg.v) << a.pshift) + (tv & page_mask)) * D + 4 * dq;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) x.k[c] = *reinterpret_cast<const u32x4*>(pk + 16 * c);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + (j < 4 ? j : j + 4) * D);
+      if (wv == 0) {
+        const int64_t blk = block_of(pg.s);
+        x.ks = a.p.ks[blk];
+        x.vs = a.p.vs[blk];
+      }
       return x;
     };
     auto stage = [&](int i, Raw<D>& x) {
@@ -132,6 +153,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
           *reinterpret_cast<bf16x8*>(kb + 8 * swizzle<C>(kkey, kdim / 8 + 2 * c + e)) =
               bf16_of_codes(x.k[c][2 * e], x.k[c][2 * e + 1]);
       if (t0 < t.lo || t0 + kUnit > t.hi) {   // keys that no row sees may hold anything
+        asm volatile("");                     // a branch: two tiles an item come here
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           const int key = t0 + vkey + (j < 4 ? j : j + 4);
@@ -157,29 +179,42 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       if (tid < 4) {
         const int key = t0 + 16 * tid;
         const bool none = key >= t.hi || key + 16 <= t.lo;
-        const int64_t blk = block_of(key);
-        const float ks = a.p.ks[blk], vs = a.p.vs[blk];
-        const float v = none ? 1.0f : vs > kMinVScale ? vs : kMinVScale;
-        scales[buf][tid][0] = none ? 0.0f : ks * a.scale_log2;
+        const float kq = x.ks * a.scale_log2, v = none ? 1.0f : x.vs > kMinVScale ? x.vs : kMinVScale;
+        scales[buf][tid][0] = none ? 1.0f : kq > kMinKScale ? kq : kMinKScale;
         scales[buf][tid][1] = __builtin_amdgcn_logf(v);
         scales[buf][tid][2] = __builtin_amdgcn_rcpf(v);
       }
     };
-    auto compute = [&](int i) {
+    // MASK: some row of the wave does not see all keys of the tile
+    auto compute = [&](int i, auto mask) {
+      constexpr bool MASK = decltype(mask)::value;
       const int buf = i & 1, t0 = base + kUnit * i;
-      if (!live || t0 >= whi_last || t0 + kUnit <= wlo_first) return;   // nothing here for this wave
-      const bool clear = t0 >= wlo_last && t0 + kUnit <= whi_first;
       f32x16 sc[2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int j = 0; j < 16; ++j) sc[x][j] = 0.0f;
-        const int key = 32 * x + n32;
+      // operands are read from LDS kAhead products before they are used
+      {
+        bf16x8 kf[2 * NS];
+        auto read = [&](int e) {
+          const int key = 32 * (e & 1) + n32;
+          kf[e] = *reinterpret_cast<const bf16x8*>(kbuf[buf] + key * D + 8 * swizzle<D / 8>(key, 2 * (e >> 1) + h2));
+        };
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const bf16x8 kf = *reinterpret_cast<const bf16x8*>(kbuf[buf] + key * D + 8 * swizzle<D / 8>(key, 2 * s + h2));
-          sc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[s], sc[x], 0, 0, 0);
+        for (int e = 0; e < kAhead; ++e) read(e);
+#pragma unroll
+        for (int e = 0; e < 2 * NS; ++e) {
+          if (e + kAhead < 2 * NS) read(e + kAhead);
+          sc[e & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[e], qf[e >> 1], sc[e & 1], 0, 0, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+        for (int e = 0; e < 2 * NS - kAhead; ++e) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       }
       float kq[4], lv[4], iv[4];
 #pragma unroll
@@ -188,26 +223,27 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         lv[y] = scales[buf][y][1];
         iv[y] = scales[buf][y][2];
       }
-      if (!clear) {
+      if (MASK) {
+        const int from = rlo - t0 - 4 * h2, to = rhi - t0 - 4 * h2;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const int key = t0 + 32 * x + 8 * (j >> 2) + 4 * h2 + (j & 3);
-            sc[x][j] = key >= rlo && key < rhi ? sc[x][j] : -__builtin_huge_valf();
+            const int key = 32 * x + 8 * (j >> 2) + (j & 3);
+            sc[x][j] = key >= from && key < to ? sc[x][j] : -__builtin_huge_valf();
           }
       }
-      float top = -__builtin_huge_valf();
+      float top = mr;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
-        float m = sc[y >> 1][8 * (y & 1)];
+        const f32x16& z = sc[y >> 1];
+        const int j = 8 * (y & 1);
+        float m = z[j];
 #pragma unroll
-        for (int j = 1; j < 8; ++j) m = __builtin_fmaxf(m, sc[y >> 1][8 * (y & 1) + j]);
-        // a masked group stays at -infinity, also under a zero scale
-        m = m == -__builtin_huge_valf() ? m : __builtin_fmaf(m, kq[y], lv[y]);
-        top = __builtin_fmaxf(top, m);
+        for (int k = 1; k < 8; ++k) m = __builtin_fmaxf(m, z[j + k]);
+        top = __builtin_fmaxf(top, __builtin_fmaf(m, kq[y], lv[y]));
       }
-      if (__ballot(top > mr + kHeadroom) != 0) {
+      if (__builtin_expect(__ballot(top > mr + kHeadroom) != 0, 0)) {
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         const float to = top > mr + kHeadroom ? top - kTop : mr;
         const float f = __builtin_amdgcn_exp2f(mr - to);
@@ -224,14 +260,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         const float c = lv[y] - mr;
         float e[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s = sc[y >> 1][8 * (y & 1) + j];
-          e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s, kq[y], c));
-        }
-        if (!clear) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) e[j] = sc[y >> 1][8 * (y & 1) + j] == -__builtin_huge_valf() ? 0.0f : e[j];
-        }
+        for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[y >> 1][8 * (y & 1) + j], kq[y], c));
         u32x4 pw;
 #pragma unroll
         for (int j = 0; j < 8; ++j) lr = __builtin_fmaf(e[j], iv[y], lr);
@@ -239,30 +268,65 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         for (int j = 0; j < 4; ++j) pw[j] = pack_f16x2(e[2 * j], e[2 * j + 1]);
         pf[y] = __builtin_bit_cast(f16x8, pw);
       }
+      {
+        f16x8 vf[4 * ND];
+        auto read = [&](int e) {
+          const int d = 32 * (e % ND) + n32;
+          vf[e] = *reinterpret_cast<const f16x8*>(vbuf[buf] + d * kUnit + 8 * swizzle<8>(d, 2 * (e / ND) + h2));
+        };
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+        for (int e = 0; e < kAhead; ++e) read(e);
 #pragma unroll
-        for (int u = 0; u < ND; ++u) {
-          const int d = 32 * u + n32;
-          const f16x8 vf = *reinterpret_cast<const f16x8*>(vbuf[buf] + d * kUnit + 8 * swizzle<8>(d, 2 * s + h2));
-          o[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[s], o[u], 0, 0, 0);
+        for (int e = 0; e < 4 * ND; ++e) {
+          if (e + kAhead < 4 * ND) read(e + kAhead);
+          o[e % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[e], pf[e / ND], o[e % ND], 0, 0, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 1);
+#pragma unroll
+        for (int e = 0; e < 4 * ND - kAhead; ++e) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 1);
+      }
     };
 
     if (tiles > 0) {
-      Raw<D> x = load_tile(0);
+      // the wave's way through the tiles: none of its rows sees the first and
+      // last ones, all rows see all of the middle ones; masks between
+      auto tile_floor = [&](int key) { const int x = (key - base) >> 6; return x < 0 ? 0 : x > tiles ? tiles : x; };
+      int b0 = tile_floor(wlo_first), b3 = tile_floor(whi_last + kUnit - 1);
+      if (!live || b3 < b0) b0 = b3 = tiles;
+      int b1 = tile_floor(wlo_last + kUnit - 1), b2 = tile_floor(whi_first);
+      b1 = b1 < b0 ? b0 : b1 > b3 ? b3 : b1;
+      b2 = b2 < b1 ? b1 : b2 > b3 ? b3 : b2;
+      // on their way: the next tile's codes, and the page numbers of the one after
+      Pages pg = load_pages(0), next = load_pages(tiles > 1 ? 1 : 0);
+      Raw<D> x = load_tile(0, pg);
+      pg = load_pages(tiles > 2 ? 2 : 0);
       __syncthreads();   // the piece before is done with the buffers
       stage(0, x);
-      if (tiles > 1) x = load_tile(1);
+      x = load_tile(tiles > 1 ? 1 : 0, next);
       __syncthreads();
-      for (int i = 0; i < tiles; ++i) {
-        if (i + 1 < tiles) {
-          stage(i + 1, x);
-          if (i + 2 < tiles) x = load_tile(i + 2);
+      auto run = [&](int from, int to, auto kind) {
+        for (int i = from; i < to; ++i) {
+          if (i + 1 < tiles) {
+            stage(i + 1, x);
+            if (i + 2 < tiles) {
+              x = load_tile(i + 2, pg);
+              if (i + 3 < tiles) pg = load_pages(i + 3);
+            }
+          }
+          if constexpr (decltype(kind)::value == 1) compute(i, std::true_type{});
+          if constexpr (decltype(kind)::value == 2) compute(i, std::false_type{});
+          __syncthreads();
         }
-        compute(i);
-        __syncthreads();
-      }
+      };
+      run(0, b0, std::integral_constant<int, 0>{});
+      run(b0, b1, std::integral_constant<int, 1>{});
+      run(b1, b2, std::integral_constant<int, 2>{});
+      run(b2, b3, std::integral_constant<int, 1>{});
+      run(b3, tiles, std::integral_constant<int, 0>{});
     }
 
     // lane pair (l, l + 32) holds row n32: dims 32 u + 8 k + 4 h2 + 0..3

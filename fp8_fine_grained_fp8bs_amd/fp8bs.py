@@ -12,6 +12,7 @@ loading fails loudly otherwise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +48,8 @@ ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_a
 
 _lib = None
 _lib_path = LIB_PATH
+_functions = {}      # the loaded library's entry points by name
+_dtype_names = {}
 
 
 def use_library(path: str) -> str:
@@ -56,6 +59,8 @@ def use_library(path: str) -> str:
     global _lib, _lib_path
     prev = _lib_path
     _lib_path, _lib = path, None
+    _functions.clear()
+    _ws_bytes.cache_clear()
     return prev
 
 
@@ -140,13 +145,21 @@ def _ld(t):
 _CODES = ("uint8", "float8_e4m3fn")
 
 
+def _dtype(t):
+    """Name of a tensor's dtype (str() of a dtype costs more than a call's other checks)."""
+    name = _dtype_names.get(t.dtype)
+    if name is None:
+        name = _dtype_names[t.dtype] = str(t.dtype).replace("torch.", "")
+    return name
+
+
 def _check(t, what, shape, dtypes, contiguous=False):
     """Refuse a tensor whose shape or dtype does not fit what the kernels
     will read or write (a short output would be written past its end).
     shape entries: an int (exact), (">=", n) (at least n) or None (any)."""
     if t is None:
         raise ValueError(f"{what}: missing tensor")
-    if str(t.dtype).replace("torch.", "") not in dtypes:
+    if _dtype(t) not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != len(shape):
         raise ValueError(f"{what}: {t.dim()}-D tensor, expected {len(shape)}-D")
@@ -173,13 +186,16 @@ def _stream(stream):
     if stream is None:
         import torch
         return torch.cuda.current_stream().cuda_stream
-    if isinstance(stream, int):
+    if type(stream) is int:
         return stream
     return stream.cuda_stream
 
 
 def _call(name, *args):
-    st = getattr(load(), name)(*args)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(load(), name)
+    st = fn(*args)
     if st != OK:
         raise Fp8bsError(st, name)
 
@@ -344,14 +360,15 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
 
 
 def _heads(t, what):
-    """Row stride (elements) of a [T][H][D] view whose heads are contiguous in a row."""
-    if t.dim() != 3 or str(t.dtype) != "torch.bfloat16":
-        raise ValueError(f"{what}: expected a 3-D bfloat16 tensor [T][H][D], got {t.dim()}-D {t.dtype}")
-    T, H, D = t.shape
-    st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != D):
-        raise ValueError(f"{what}: heads must be contiguous in a row, got strides {tuple(st)}")
-    return st[0] if T > 1 else max(st[0], H * D)
+    """Row stride (elements) of a [T][H][D] view whose heads are contiguous in a row, and its shape."""
+    shape = t.shape
+    if len(shape) != 3 or _dtype(t) != "bfloat16":
+        raise ValueError(f"{what}: expected a 3-D bfloat16 tensor [T][H][D], got {len(shape)}-D {t.dtype}")
+    T, H, D = shape
+    row, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
+        raise ValueError(f"{what}: heads must be contiguous in a row, got strides {(row, head, one)}")
+    return (row if T > 1 else max(row, H * D)), shape
 
 
 def _layout(layout):
@@ -363,34 +380,44 @@ def _layout(layout):
 
 
 def _int32s(t, what, n):
-    if str(t.dtype) != "torch.int32" or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or _dtype(t) != "int32" or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous int32, got {t.dtype} {tuple(t.shape)}")
 
 
 def _check_angles(cs):
-    if str(cs.dtype) != "torch.float32" or cs.dim() != 2 or not cs.is_contiguous():
+    """(n_pos, rot) of a table of angles."""
+    if _dtype(cs) != "float32" or cs.dim() != 2 or not cs.is_contiguous():
         raise ValueError(f"cs: expected a contiguous float32 table [n_pos][rot], got {cs.dtype} {tuple(cs.shape)}")
+    return cs.shape
 
 
 def _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T):
-    """Shapes of a paged cache and its packing; returns (B, Hkv, D, page, n_pages, ldt)."""
-    if kc.dim() != 4 or str(kc.dtype).replace("torch.", "") not in _CODES or not kc.is_contiguous():
-        raise ValueError(f"kc: expected contiguous codes [n_pages][Hkv][page][D], got {kc.dtype} {tuple(kc.shape)}")
-    if vc.shape != kc.shape or vc.dtype != kc.dtype or not vc.is_contiguous():
+    """Shapes of a paged cache and its packing; returns
+    (B, Hkv, D, page, n_pages, ldt, max_pages)."""
+    shape, name = kc.shape, _dtype(kc)
+    if len(shape) != 4 or name not in _CODES or not kc.is_contiguous():
+        raise ValueError(f"kc: expected contiguous codes [n_pages][Hkv][page][D], got {kc.dtype} {tuple(shape)}")
+    if vc.shape != shape or _dtype(vc) != name or not vc.is_contiguous():
         raise ValueError("vc: must have kc's shape and dtype, contiguous")
-    n_pages, Hkv, page, D = kc.shape
-    for t, what in ((ks, "ks"), (vs, "vs")):
-        if t.shape != (n_pages, Hkv) or str(t.dtype) != "torch.float32" or not t.is_contiguous():
-            raise ValueError(f"{what}: expected contiguous float32 [{n_pages}][{Hkv}], got {t.dtype} {tuple(t.shape)}")
-    if table.dim() != 2 or str(table.dtype) != "torch.int32":
-        raise ValueError(f"table: expected int32 [B][max_pages], got {table.dtype} {tuple(table.shape)}")
-    B = table.shape[0]
+    n_pages, Hkv, page, D = shape
+    blocks = (n_pages, Hkv)
+    if ks.shape != blocks or _dtype(ks) != "float32" or not ks.is_contiguous():
+        raise ValueError(f"ks: expected contiguous float32 {blocks}, got {ks.dtype} {tuple(ks.shape)}")
+    if vs.shape != blocks or _dtype(vs) != "float32" or not vs.is_contiguous():
+        raise ValueError(f"vs: expected contiguous float32 {blocks}, got {vs.dtype} {tuple(vs.shape)}")
+    listed = table.shape
+    if len(listed) != 2 or _dtype(table) != "int32":
+        raise ValueError(f"table: expected int32 [B][max_pages], got {table.dtype} {tuple(listed)}")
+    B, max_pages = listed
+    ldt, one = table.stride()
+    if one != 1 and max_pages > 1:
+        raise ValueError(f"table: rows must be contiguous, got strides {(ldt, one)}")
     _int32s(kv_len, "kv_len", B)
     if q_off is not None:
         _int32s(q_off, "q_off", B + 1)
     elif T != B:
         raise ValueError(f"q_off: without it every sequence has one row, but T = {T} and B = {B}")
-    return B, Hkv, D, page, n_pages, _ld(table) if B > 1 else max(table.stride(0), table.shape[1])
+    return B, Hkv, D, page, n_pages, (ldt if B > 1 else max(ldt, max_pages)), max_pages
 
 
 def fp8bs_rope_table(cs, base, factor, orig_len, turns_lo, turns_hi, mscale, stream=None):
@@ -403,66 +430,73 @@ def fp8bs_rope_table(cs, base, factor, orig_len, turns_lo, turns_hi, mscale, str
 def fp8bs_rope(x, y, pos, rot_off, layout, inverse, cs, stream=None):
     """x bf16 [T][H][D] -> y (same shape; may be x), rotated by the angles
     cs f32 [n_pos][rot] of positions pos i32 [T]."""
-    ldx, ldy = _heads(x, "x"), _heads(y, "y")
-    T, H, D = x.shape
-    if y.shape != x.shape:
-        raise ValueError(f"y: shape {tuple(y.shape)}, expected {tuple(x.shape)}")
+    ldx, shape = _heads(x, "x")
+    ldy, shape_y = _heads(y, "y")
+    T, H, D = shape
+    if shape_y != shape:
+        raise ValueError(f"y: shape {tuple(shape_y)}, expected {tuple(shape)}")
     _int32s(pos, "pos", T)
-    _check_angles(cs)
-    _call("fp8bs_rope", _ptr(x), ldx, _ptr(y), ldy, _ptr(pos), T, H, D, cs.shape[1], rot_off, _layout(layout),
-          int(bool(inverse)), _ptr(cs), cs.shape[0], _stream(stream))
+    n_pos, rot = _check_angles(cs)
+    _call("fp8bs_rope", _ptr(x), ldx, _ptr(y), ldy, _ptr(pos), T, H, D, rot, rot_off, _layout(layout),
+          1 if inverse else 0, _ptr(cs), n_pos, _stream(stream))
 
 
 def fp8bs_kv_append(q, q_out, k, v, cs, rot_off, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream=None):
     """k, v bf16 [T][Hkv][D] into the paged cache kc, vc u8 [n_pages][Hkv][page][D],
     ks, vs f32 [n_pages][Hkv]; q bf16 [T][Hq][D] rotated into q_out (both or neither)."""
-    ldk, ldv = _heads(k, "k"), _heads(v, "v")
-    T = k.shape[0]
-    B, Hkv, D, page, n_pages, ldt = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D):
-        raise ValueError(f"k, v: shapes {tuple(k.shape)}, {tuple(v.shape)}, expected {(T, Hkv, D)}")
+    ldk, shape = _heads(k, "k")
+    ldv, shape_v = _heads(v, "v")
+    T = shape[0]
+    B, Hkv, D, page, n_pages, ldt, max_pages = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
+    if shape != (T, Hkv, D) or shape_v != shape:
+        raise ValueError(f"k, v: shapes {tuple(shape)}, {tuple(shape_v)}, expected {(T, Hkv, D)}")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out: both or neither")
-    Hq = ldq = ldqo = 0
+    Hq = ldq = ldqo = n_pos = rot = 0
     if q is not None:
-        ldq, ldqo, Hq = _heads(q, "q"), _heads(q_out, "q_out"), q.shape[1]
-        if q.shape != (T, Hq, D) or q_out.shape != q.shape:
-            raise ValueError(f"q, q_out: shapes {tuple(q.shape)}, {tuple(q_out.shape)}, expected {(T, Hq, D)}")
-    n_pos = rot = 0
+        ldq, shape_q = _heads(q, "q")
+        ldqo, shape_o = _heads(q_out, "q_out")
+        Hq = shape_q[1]
+        if shape_q != (T, Hq, D) or shape_o != shape_q:
+            raise ValueError(f"q, q_out: shapes {tuple(shape_q)}, {tuple(shape_o)}, expected {(T, Hq, D)}")
     if cs is not None:
-        _check_angles(cs)
-        n_pos, rot = cs.shape
+        n_pos, rot = _check_angles(cs)
     _call("fp8bs_kv_append", _ptr(q), ldq, _ptr(q_out), ldqo, Hq, _ptr(k), ldk, _ptr(v), ldv, Hkv, D, _ptr(cs),
           n_pos, rot, rot_off, _layout(layout), _ptr(q_off), _ptr(kv_len), B, T, max_q, _ptr(table), ldt,
-          table.shape[1], page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages, _stream(stream))
+          max_pages, page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages, _stream(stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(*sizes):
+    return load().fp8bs_attn_paged_ws(*sizes)
 
 
 def fp8bs_attn_paged_ws(B, T, max_q, Hq, Hkv, D, max_pages, page):
     """Bytes of working memory fp8bs_attn_paged needs (-1: invalid sizes)."""
-    return load().fp8bs_attn_paged_ws(B, T, max_q, Hq, Hkv, D, max_pages, page)
+    return _ws_bytes(B, T, max_q, Hq, Hkv, D, max_pages, page)
 
 
 def fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs, scale, causal, window, ws,
                      stream=None):
     """q bf16 [T][Hq][D] -> out (same shape) and lse f32 [T][Hq] (or None):
     attention over the paged cache; ws uint8 [>= fp8bs_attn_paged_ws(...)]."""
-    ldq, ldo = _heads(q, "q"), _heads(out, "out")
-    T, Hq, D = q.shape
-    B, Hkv, Dc, page, n_pages, ldt = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
-    if Dc != D or out.shape != q.shape:
-        raise ValueError(f"q, out: shapes {tuple(q.shape)}, {tuple(out.shape)}, expected heads of {Dc}")
-    ldl = 0
+    ldq, shape = _heads(q, "q")
+    ldo, shape_o = _heads(out, "out")
+    T, Hq, D = shape
+    B, Hkv, Dc, page, n_pages, ldt, max_pages = _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T)
+    if Dc != D or shape_o != shape:
+        raise ValueError(f"q, out: shapes {tuple(shape)}, {tuple(shape_o)}, expected heads of {Dc}")
+    ldl = ws_bytes = 0
     if lse is not None:
         _check(lse, "lse", (T, Hq), ("float32",))
         ldl = _ld(lse) if T > 1 else max(lse.stride(0), Hq)
-    ws_bytes = 0
     if ws is not None:
         if not ws.is_contiguous():
             raise ValueError("ws: must be contiguous")
         ws_bytes = ws.numel() * ws.element_size()
     _call("fp8bs_attn_paged", _ptr(q), ldq, _ptr(out), ldo, _ptr(lse), ldl, _ptr(q_off), _ptr(kv_len), B, T, max_q,
-          Hq, Hkv, D, _ptr(table), ldt, table.shape[1], page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages,
-          scale, int(bool(causal)), window, _ptr(ws), ws_bytes, _stream(stream))
+          Hq, Hkv, D, _ptr(table), ldt, max_pages, page, _ptr(kc), _ptr(ks), _ptr(vc), _ptr(vs), n_pages,
+          scale, 1 if causal else 0, window, _ptr(ws), ws_bytes, _stream(stream))
 
 
 # ---------------------------------------------------------------------------
@@ -650,8 +684,7 @@ def rope_table(n_pos, rot, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, t
 
 def rope(x, pos, cs, rot_offset=0, layout="half", inverse=False, stream=None):
     """x bf16 [T][H][D] rotated (inverse: the gradient)."""
-    import torch
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x.new_empty(x.shape)
     fp8bs_rope(x, y, pos, rot_offset, layout, inverse, cs, stream)
     return y
 
@@ -668,18 +701,15 @@ def kv_append(k, v, kc, ks, vc, vs, table, kv_len, q_off, max_q, q=None, cs=None
               stream=None):
     """Appends k, v [T][Hkv][D] to the cache (keys rotated when cs is given);
     returns the rotated queries when q is given."""
-    import torch
-    q_out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    q_out = None if q is None else q.new_empty(q.shape)
     fp8bs_kv_append(q, q_out, k, v, cs, rot_offset, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream)
     return q_out
 
 
 def _scratch(nbytes, device, stream):
-    """Working memory that belongs to the stream it is used on, so that it is
-    not handed out again before that stream is done with it."""
+    """Working memory that belongs to the given stream, so that it is not
+    handed out again before that stream is done with it."""
     import torch
-    if stream is None:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
     on = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(on):
         return torch.empty((nbytes,), dtype=torch.uint8, device=device)
@@ -689,14 +719,15 @@ def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None
                with_lse=False, ws=None, stream=None):
     """Attention of q bf16 [T][Hq][D] over the cache; scale None: D^-1/2.
     The working memory is allocated unless given."""
-    import torch
     T, Hq, D = q.shape
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+    out = q.new_empty(q.shape)
+    lse = ks.new_empty((T, Hq)) if with_lse else None
     if ws is None:
-        need = fp8bs_attn_paged_ws(table.shape[0], T, max_q, Hq, kc.shape[1], D, table.shape[1], kc.shape[2])
+        B, max_pages = table.shape
+        _, Hkv, page, _ = kc.shape
+        need = _ws_bytes(B, T, max_q, Hq, Hkv, D, max_pages, page)
         if need > 0:
-            ws = _scratch(need, q.device, stream)
+            ws = ks.new_empty(need // 4) if stream is None else _scratch(need, q.device, stream)
     fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs,
                      D ** -0.5 if scale is None else scale, causal, window, ws, stream)
     return (out, lse) if with_lse else out

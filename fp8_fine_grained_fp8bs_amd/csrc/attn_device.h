@@ -12,6 +12,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kNoKeys = -1e30f;       // reference of a row that has seen no key yet
 constexpr float kHeadroom = 15.0f;      // log2 of the largest p' before the reference moves
+constexpr float kMostWeight = 0x1p15f;  // the same, as a sum of weights
 constexpr float kTop = 8.0f;            // log2 of the largest p' after a move
 constexpr float kMinVScale = 0x1p-100f;
 constexpr float kMinKScale = 0x1p-120f; // of a key block's factor, so that it keeps a masked score's -infinity

@@ -30,10 +30,6 @@ namespace {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kRows = 128;
-#ifndef AHEAD
-#define AHEAD 4
-#endif
-constexpr int kAhead = AHEAD;   // LDS reads in flight before their products
 
 // 16-byte chunk c of an LDS row, moved so that lanes reading the same chunk
 // of 16 neighbouring rows, and the decoding writes, spread over the banks.
@@ -46,11 +42,16 @@ template <int D>
 struct Raw {           // a thread's share of a tile on its way
   u32x4 k[D / 64];     // 16 D/64 codes of key tid / 4
   uint32_t v[D / 16];  // D/16 keys by 4 dims
-  float ks, vs;        // first wave: scales of the 16 keys from 16 (lane % 4)
+  float ks, vs;        // the tile's scales, or in the first wave those of keys 16 (lane % 4)
 };
 
-template <int D>
+// PAGE64: a page holds whole tiles (64 or 128 tokens), so a tile has one block,
+// one pair of scales, and its addresses are scalar; else a tile's sixteens of
+// keys each have their own.
+template <int D, bool PAGE64>
 __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
+  constexpr int NG = PAGE64 ? 1 : 4;      // scale groups of a tile
+  constexpr int kAhead = PAGE64 ? 4 : 2;  // LDS reads in flight before their products (four spill with four groups)
   constexpr int NS = D / 16;   // MFMA steps over the inner dim
   constexpr int ND = D / 32;   // 32-dim tiles of the output
   __shared__ __attribute__((aligned(16))) uint16_t kbuf[2][kUnit * D];
@@ -123,25 +124,44 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
     };
     auto load_pages = [&](int i) {
       const int t0 = base + kUnit * i;
+      if (PAGE64) {
+        const int id = page_at(t0);   // made scalar where it is used: that waits for the load
+        return Pages{id, id, id};
+      }
       return Pages{page_at(t0 + kkey), page_at(t0 + vkey), page_at(t0 + 16 * (lane & 3))};
     };
     auto load_tile = [&](int i, const Pages& pg) {
       Raw<D> x;
       const int t0 = base + kUnit * i;
-      const int tk = t0 + kkey, tv = t0 + vkey;
-      const uint8_t* pk = a.p.kc + ((block_of(pg.k) << a.pshift) + (tk & page_mask)) * D + kdim;
-      const uint8_t* pv = a.p.vc + ((block_of(pg.v) << a.pshift) + (tv & page_mask)) * D + 4 * dq;
+      const uint8_t *pk, *pv;
+      if (PAGE64) {
+        const int64_t blk = block_of(uniform(pg.k)), at = ((blk << a.pshift) + (t0 & page_mask)) * D;
+        pk = a.p.kc + at + static_cast<unsigned>(kkey * D + kdim);
+        pv = a.p.vc + at + static_cast<unsigned>(vkey * D + 4 * dq);
+      } else {
+        pk = a.p.kc + ((block_of(pg.k) << a.pshift) + ((t0 + kkey) & page_mask)) * D + kdim;
+        pv = a.p.vc + ((block_of(pg.v) << a.pshift) + ((t0 + vkey) & page_mask)) * D + 4 * dq;
+      }
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) x.k[c] = *reinterpret_cast<const u32x4*>(pk + 16 * c);
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + (j < 4 ? j : j + 4) * D);
-      if (wv == 0) {
-        const int64_t blk = block_of(pg.s);
+      if (PAGE64 || wv == 0) {
+        const int64_t blk = block_of(PAGE64 ? uniform(pg.k) : pg.s);
         x.ks = a.p.ks[blk];
         x.vs = a.p.vs[blk];
       }
       return x;
     };
+    // factors of a block: of its scores, log2 and inverse of its value scale;
+    // `none`: keys that no row sees, whose scales may hold anything
+    auto set_factors = [&](float ks, float vs, bool none, float& kq, float& lv, float& iv) {
+      const float f = ks * a.scale_log2, v = none ? 1.0f : vs > kMinVScale ? vs : kMinVScale;
+      kq = none ? 1.0f : f > kMinKScale ? f : kMinKScale;
+      lv = __builtin_amdgcn_logf(v);
+      iv = __builtin_amdgcn_rcpf(v);
+    };
+    float next_kq = 0.0f, next_lv = 0.0f, next_iv = 0.0f;
     auto stage = [&](int i, Raw<D>& x) {
       const int buf = i & 1, t0 = base + kUnit * i;
       uint16_t* kb = kbuf[buf] + kkey * D;
@@ -153,9 +173,9 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
           *reinterpret_cast<bf16x8*>(kb + 8 * swizzle<C>(kkey, kdim / 8 + 2 * c + e)) =
               bf16_of_codes(x.k[c][2 * e], x.k[c][2 * e + 1]);
       if (t0 < t.lo || t0 + kUnit > t.hi) {   // keys that no row sees may hold anything
-        asm volatile("");                     // a branch: two tiles an item come here
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
+          asm volatile("" : "+v"(x.v[j]));    // a branch: two tiles an item come here
           const int key = t0 + vkey + (j < 4 ? j : j + 4);
           if (key < t.lo || key >= t.hi) x.v[j] = 0u;
         }
@@ -176,17 +196,16 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
                                     4 * ((vg >> 1) & 1)) = u32x2{y[0], y[1]};
         }
       }
-      if (tid < 4) {
+      if (PAGE64) {   // the tile's factors wait in registers for their turn
+        set_factors(x.ks, x.vs, false, next_kq, next_lv, next_iv);
+      } else if (tid < 4) {
         const int key = t0 + 16 * tid;
-        const bool none = key >= t.hi || key + 16 <= t.lo;
-        const float kq = x.ks * a.scale_log2, v = none ? 1.0f : x.vs > kMinVScale ? x.vs : kMinVScale;
-        scales[buf][tid][0] = none ? 1.0f : kq > kMinKScale ? kq : kMinKScale;
-        scales[buf][tid][1] = __builtin_amdgcn_logf(v);
-        scales[buf][tid][2] = __builtin_amdgcn_rcpf(v);
+        set_factors(x.ks, x.vs, key >= t.hi || key + 16 <= t.lo, scales[buf][tid][0], scales[buf][tid][1],
+                    scales[buf][tid][2]);
       }
     };
     // MASK: some row of the wave does not see all keys of the tile
-    auto compute = [&](int i, auto mask) {
+    auto compute = [&](int i, auto mask, float kq1, float lv1, float iv1) {
       constexpr bool MASK = decltype(mask)::value;
       const int buf = i & 1, t0 = base + kUnit * i;
       f32x16 sc[2];
@@ -216,12 +235,18 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         }
         __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       }
-      float kq[4], lv[4], iv[4];
+      float kq[NG], lv[NG], iv[NG];
+      if (PAGE64) {
+        kq[0] = kq1;
+        lv[0] = lv1;
+        iv[0] = iv1;
+      } else {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        kq[y] = scales[buf][y][0];
-        lv[y] = scales[buf][y][1];
-        iv[y] = scales[buf][y][2];
+        for (int y = 0; y < NG; ++y) {
+          kq[y] = scales[buf][y][0];
+          lv[y] = scales[buf][y][1];
+          iv[y] = scales[buf][y][2];
+        }
       }
       if (MASK) {
         const int from = rlo - t0 - 4 * h2, to = rhi - t0 - 4 * h2;
@@ -233,19 +258,45 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
             sc[x][j] = key >= from && key < to ? sc[x][j] : -__builtin_huge_valf();
           }
       }
-      float top = mr;
+      // weights under the reference as it stands; their sum shows whether it
+      // still holds (no weight above 2^15), which spares the maximum
+      f16x8 pf[4];
+      float sum[NG];
+      auto weigh = [&]() {
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const f32x16& z = sc[y >> 1];
-        const int j = 8 * (y & 1);
-        float m = z[j];
+        for (int y = 0; y < 4; ++y) {
+          const int gr = PAGE64 ? 0 : y;
+          const float c = lv[gr] - mr;
+          float e[8];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) m = __builtin_fmaxf(m, z[j + k]);
-        top = __builtin_fmaxf(top, __builtin_fmaf(m, kq[y], lv[y]));
-      }
-      if (__builtin_expect(__ballot(top > mr + kHeadroom) != 0, 0)) {
+          for (int j = 0; j < 8; ++j)
+            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[y >> 1][8 * (y & 1) + j], kq[gr], c));
+          u32x4 pw;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pw[j] = pack_f16x2(e[2 * j], e[2 * j + 1]);
+          pf[y] = __builtin_bit_cast(f16x8, pw);
+          const float s8 = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+          if (PAGE64 && y > 0) sum[0] += s8;
+          else sum[gr] = s8;
+        }
+      };
+      weigh();
+      float all = sum[0];
+#pragma unroll
+      for (int y = 1; y < NG; ++y) all += sum[y];
+      if (__builtin_expect(__ballot(all > kMostWeight) != 0, 0)) {
+        float top = -__builtin_huge_valf();
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int gr = PAGE64 ? 0 : y;
+          float m = sc[y >> 1][8 * (y & 1)];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) m = __builtin_fmaxf(m, sc[y >> 1][8 * (y & 1) + j]);
+          top = __builtin_fmaxf(top, __builtin_fmaf(m, kq[gr], lv[gr]));
+        }
+        all = __builtin_fmaxf(all, __shfl_xor(all, 32));   // both halves of a row move together
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        const float to = top > mr + kHeadroom ? top - kTop : mr;
+        const float to = all > kMostWeight ? top - kTop : mr;
         const float f = __builtin_amdgcn_exp2f(mr - to);
         mr = to;
         lr *= f;
@@ -253,21 +304,10 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         for (int u = 0; u < ND; ++u)
 #pragma unroll
           for (int j = 0; j < 16; ++j) o[u][j] *= f;
+        weigh();
       }
-      f16x8 pf[4];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const float c = lv[y] - mr;
-        float e[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[y >> 1][8 * (y & 1) + j], kq[y], c));
-        u32x4 pw;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) lr = __builtin_fmaf(e[j], iv[y], lr);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pw[j] = pack_f16x2(e[2 * j], e[2 * j + 1]);
-        pf[y] = __builtin_bit_cast(f16x8, pw);
-      }
+      for (int y = 0; y < NG; ++y) lr = __builtin_fmaf(sum[y], iv[y], lr);
       {
         f16x8 vf[4 * ND];
         auto read = [&](int e) {
@@ -310,6 +350,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       __syncthreads();
       auto run = [&](int from, int to, auto kind) {
         for (int i = from; i < to; ++i) {
+          const float kq = next_kq, lv = next_lv, iv = next_iv;
           if (i + 1 < tiles) {
             stage(i + 1, x);
             if (i + 2 < tiles) {
@@ -317,8 +358,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
               if (i + 3 < tiles) pg = load_pages(i + 3);
             }
           }
-          if constexpr (decltype(kind)::value == 1) compute(i, std::true_type{});
-          if constexpr (decltype(kind)::value == 2) compute(i, std::false_type{});
+          if constexpr (decltype(kind)::value == 1) compute(i, std::true_type{}, kq, lv, iv);
+          if constexpr (decltype(kind)::value == 2) compute(i, std::false_type{}, kq, lv, iv);
           __syncthreads();
         }
       };
@@ -368,8 +409,12 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
 }  // namespace
 
 hipError_t launch_attn_prompt(const AttnArgs& a, unsigned blocks, hipStream_t st) {
-  if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64>), dim3(blocks), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((attn_prompt_kernel<128>), dim3(blocks), dim3(256), 0, st, a);
+  const dim3 grid(blocks), block(256);
+  const bool page64 = a.p.page >= kUnit;
+  if (a.p.D == 64 && page64) hipLaunchKernelGGL((attn_prompt_kernel<64, true>), grid, block, 0, st, a);
+  else if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64, false>), grid, block, 0, st, a);
+  else if (page64) hipLaunchKernelGGL((attn_prompt_kernel<128, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((attn_prompt_kernel<128, false>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

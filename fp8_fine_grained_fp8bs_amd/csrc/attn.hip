@@ -378,18 +378,18 @@ constexpr int64_t kMaxInt = 0x7fffffff;
 Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
   Plan p;
   const int64_t G = Hq / Hkv, rows = max_q * G;
-  p.R = rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
+  p.R = rows <= 16 ? 16 : rows <= 64 ? 32 : kManyRows;
   const int64_t most = (rows + p.R - 1) / p.R;
   const int64_t direct = most > kMaxInt / B ? kMaxInt : B * most, searched = T * G / p.R + B;
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  const int full = 512;   // resident workgroups: two a compute unit
+  const int full = p.R == kManyRows ? 256 : 512;   // resident workgroups: one or two a compute unit
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t items = p.slots * Hkv;
   // whole items where there are enough of them to fill the GPU several times
   // over (and where the line cannot hold them)
-  const bool many = p.R == 128 && items >= 4 * full;
+  const bool many = p.R == kManyRows && items >= 4 * full;
   p.workers = 0;
   p.bytes = 0;
   p.by_item = items <= full;
@@ -432,7 +432,7 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
   FP8BS_ROWS(128, 1);
   FP8BS_ROWS(128, 2);
 #undef FP8BS_ROWS
-  const hipError_t e = plan.R == 128 ? launch_attn_prompt(a, static_cast<unsigned>(blocks), st) : hipGetLastError();
+  const hipError_t e = plan.R == kManyRows ? launch_attn_prompt(a, static_cast<unsigned>(blocks), st) : hipGetLastError();
   if (e != hipSuccess || plan.workers == 0) return e;
   const int64_t items = plan.slots * p.Hkv, joins = plan.by_item ? items : plan.workers;
   // pieces an item on average decide how a workgroup's threads are split

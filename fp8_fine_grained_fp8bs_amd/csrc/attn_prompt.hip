@@ -2,14 +2,25 @@
 // key/value head (prompts and their pieces), on gfx950.
 //
 // 4 D operations a row and key against 2 D / R bytes of cache: bound by the
-// matrix units at R = 128 rows a tile, with the softmax's vector work beside
-// them.  A workgroup of four waves takes 128 rows, a wave 32 of them; the cache
-// goes by in tiles of 64 keys, read once a workgroup, decoded once (keys to
-// BF16, values to FP16, both exact) and shared through LDS.  Two LDS buffers:
-// while a tile is computed the next one is decoded into the other buffer and
-// the one after is on its way from memory in registers, so a tile costs one
-// barrier.  Two workgroups live on a compute unit; their waves share the SIMDs
-// without a common barrier, so one's softmax runs under the other's MFMAs.
+// matrix units at R = 256 rows a tile, with as much vector work (softmax, decoding)
+// to be hidden under them.  A workgroup of eight waves takes 256 rows, a wave 32 of them;
+// the cache goes by in tiles of KT keys, read once a workgroup, decoded once
+// (keys to BF16, values to FP16, both exact) and shared through LDS.
+//
+// A compute unit holds one workgroup, a SIMD two of its waves: one of the first group
+// (waves 0..3), one of the second.  The groups alternate: while one multiplies
+// (the product of the last tile's weights with its values, then of the queries with
+// the next tile's keys), the other does its softmax and its share of the
+// decoding, and a barrier ends each turn.  So the matrix units run in every turn
+// and the vector units beside them; left to themselves two waves did both in
+// step and took the sum of the two times (measured: 618 us against a
+// matrix and LDS time of 400 at 8192 x 8192 keys, 32 heads of 128).
+//
+// turn 2i      first group multiplies (tile i-1 values, tile i keys), second group: softmax of tile i-1
+// turn 2i + 1  first group: softmax of tile i, second group multiplies (tile i-1 values, tile i keys)
+// Decoding of a tile has to be done two turns before its keys are read by the first
+// group, so the first group decodes its half of tile i + 1 beside the softmax of tile i,
+// the second group of tile i + 2.  Keys then need two LDS buffers, values three.
 //
 // Mathematics and number formats are those of the few-rows kernel: S^T = K Q^T
 // (32x32x16 BF16 MFMAs), p' = 2^(s k c + log2 v - m) with the value scale v
@@ -20,8 +31,6 @@
 // 4h + 0..3.  A lane pair (l, l + 32) holds a row: one exchange a moved reference.
 #include <hip/hip_runtime.h>
 
-#include <type_traits>
-
 #include "attn_device.h"
 
 namespace fp8bs {
@@ -29,7 +38,11 @@ namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kRows = 128;
+constexpr int kAhead = 4;   // LDS reads in flight before their products
+
+// Instructions stay on their side of this: matrix and other work is laid out
+// in the order in which it is written.
+#define FP8BS_PIN() __builtin_amdgcn_sched_barrier(0)
 
 // 16-byte chunk c of an LDS row, moved so that lanes reading the same chunk
 // of 16 neighbouring rows, and the decoding writes, spread over the banks.
@@ -38,51 +51,67 @@ __device__ __forceinline__ int swizzle(int row, int c) {
   return CHUNKS == 16 ? c ^ (row & 15) : c ^ ((row >> 1) & 7) ^ ((row >> 4) & 1);
 }
 
-template <int D>
-struct Raw {           // a thread's share of a tile on its way
-  u32x4 k[D / 64];     // 16 D/64 codes of key tid / 4
-  uint32_t v[D / 16];  // D/16 keys by 4 dims
-  float ks, vs;        // the tile's scales, or in the first wave those of keys 16 (lane % 4)
+// A group of keys that share a block: the factor of its scores, log2 and
+// inverse of its value scale, its page.
+struct __attribute__((aligned(16))) Group {
+  float kq, lv, iv;
+  int page;
 };
+constexpr int kInfo = 512;
 
-// PAGE64: a page holds whole tiles (64 or 128 tokens), so a tile has one block,
-// one pair of scales, and its addresses are scalar; else a tile's sixteens of
-// keys each have their own.
-template <int D, bool PAGE64>
-__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
-  constexpr int NG = PAGE64 ? 1 : 4;      // scale groups of a tile
-  constexpr int kAhead = PAGE64 ? 4 : 2;  // LDS reads in flight before their products (four spill with four groups)
-  constexpr int NS = D / 16;   // MFMA steps over the inner dim
-  constexpr int ND = D / 32;   // 32-dim tiles of the output
-  __shared__ __attribute__((aligned(16))) uint16_t kbuf[2][kUnit * D];
-  __shared__ __attribute__((aligned(16))) uint16_t vbuf[2][D * kUnit];
-  __shared__ float scales[2][4][4];   // key scale, log2 and inverse of the value scale, of 16 keys
+// GROUP: keys that surely share a page, hence a pair of scales: 64 where a page holds as
+// many, else 16.
+template <int D, int GROUP>
+__global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
+  constexpr int KT = 8192 / D;            // keys of a tile: 8 KB of codes each side
+  constexpr int NS = D / 16, NX = KT / 32;   // MFMA steps over the inner dim, 32-key tiles
+  constexpr int ND = D / 32, NY = KT / 16;   // 32-dim tiles of the output, 16-key steps
+  constexpr int NG = KT / GROUP;          // scale groups of a tile
+  constexpr int VC = KT / 8;              // 16-byte chunks of a value row
+  __shared__ __attribute__((aligned(16))) uint16_t kbuf[2][KT * D];
+  __shared__ __attribute__((aligned(16))) uint16_t vbuf[3][D * KT];
+  // factors and page of the piece's groups, kInfo at a time: read in the loop
+  // by one LDS access each, where memory would cost a chain of three loads
+  __shared__ Group info[kInfo];
   __shared__ int sums[4];
   static_assert(sizeof(kbuf) >= kMaxSlots * sizeof(int), "the line's prefix sums fit");
   poison_lds<sizeof(kbuf)>(kbuf);
   poison_lds<sizeof(vbuf)>(vbuf);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = uniform(tid >> 6);
   const int n32 = lane & 31, h2 = lane >> 5;
+  const bool second = wv >= 4;
   const int page_mask = (1 << a.pshift) - 1;
 
   Cursor c;
-  if (!begin_work(a, kRows, true, kbuf, sums, c)) return;
+  if (!begin_work(a, kManyRows, true, kbuf, sums, c)) return;
   while (c.cur < c.stop) {
     take_piece(c);
     const Tile& t = c.t;
     const int h = c.h;
 
+    // the piece's keys
+    const int base = (t.u0 + c.ub) * kUnit;
+    const int end = base + (c.ue - c.ub) * kUnit;
+    const int plo = t.lo > base ? t.lo : base, phi = t.hi < end ? t.hi : end;
+    const int tiles = phi > base ? (phi - base + KT - 1) / KT : 0;
     // this wave's rows; a lane's own row is column n32
     const int wrow = 32 * wv, row = wrow + n32;
     const bool live = wrow < t.rows, there = row < t.rows;
     const int last = t.rows - 1 < wrow + 31 ? t.rows - 1 : wrow + 31;
     int rlo = 0, rhi = 0;
     if (there) row_keys(a, t, t.row0 + row, rlo, rhi);
-    int wlo_first = 0, whi_first = 0, wlo_last = 0, whi_last = 0;   // of the wave's first and last row
+    rhi = rhi < phi ? rhi : phi;
+    // tiles b1 .. b2 - 1 hold only keys that all rows of the wave see
+    int lo_last = 0, hi_first = 0;
     if (live) {
-      row_keys(a, t, t.row0 + wrow, wlo_first, whi_first);
-      row_keys(a, t, t.row0 + last, wlo_last, whi_last);
+      int x;
+      row_keys(a, t, t.row0 + wrow, x, hi_first);
+      row_keys(a, t, t.row0 + last, lo_last, x);
     }
+    hi_first = hi_first < phi ? hi_first : phi;
+    const int b1 = uniform(lo_last > base ? (lo_last - base + KT - 1) / KT : 0);
+    const int b2 = uniform(hi_first > base ? (hi_first - base) / KT : 0);
+
     bf16x8 qf[NS];
     {
       const int rr = there ? row : 0;
@@ -103,155 +132,134 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
 
     const int32_t* table = a.p.table + t.b * a.p.ldt;
     const int last_page = static_cast<int>(a.p.max_pages) - 1;
-    const int base = (t.u0 + c.ub) * kUnit;
-    const int tiles = t.hi > base ? c.ue - c.ub : 0;
-    auto page_at = [&](int key) {   // the table's entry for a key's page, never past the table
-      const int i = key >> a.pshift;
-      return table[i < last_page ? i : last_page];
+    // Group e of the piece.  Scales of groups that no row sees may hold anything.
+    auto fill_info = [&](int e) {
+      const int key = base + GROUP * e, i = key >> a.pshift;
+      const unsigned u = static_cast<unsigned>(table[i < last_page ? i : last_page]);
+      const unsigned n = static_cast<unsigned>(a.p.n_pages) - 1u;
+      Group g;
+      g.page = static_cast<int>(u < n ? u : n);   // never out of range
+      const int64_t blk = static_cast<int64_t>(g.page) * a.p.Hkv + h;
+      const bool none = key >= phi || key + GROUP <= plo;
+      const float f = a.p.ks[blk] * a.scale_log2, vs = a.p.vs[blk];
+      const float v = none ? 1.0f : vs > kMinVScale ? vs : kMinVScale;
+      g.kq = none ? 1.0f : f > kMinKScale ? f : kMinKScale;
+      g.lv = __builtin_amdgcn_logf(v);
+      g.iv = __builtin_amdgcn_rcpf(v);
+      info[e % kInfo] = g;
     };
-    auto block_of = [&](int id) {   // never out of range
-      const unsigned u = static_cast<unsigned>(id), n = static_cast<unsigned>(a.p.n_pages) - 1u;
-      return static_cast<int64_t>(u < n ? u : n) * a.p.Hkv + h;
+    // Decoding: a thread takes 16 codes of one key, and four values of four
+    // keys.  A wave's keys lie in one sixteen, so in one page.
+    const int kkey = tid / (D / 16), kdim = (tid % (D / 16)) * 16;
+    constexpr int DQ = D / 4;
+    const int dq = tid % DQ, vg = tid / DQ;
+    // values' keys in the order that the weights come in: step, lane half, fours
+    const int vkey = 16 * (vg >> 2) + 8 * (vg & 1) + 4 * ((vg >> 1) & 1);
+    struct Raw {
+      u32x4 k;
+      uint32_t v[4];
     };
-    // a thread's keys: one for the key tile; for the value tile those whose
-    // products a lane half takes together
-    const int kkey = tid >> 2, kdim = (tid & 3) * (D / 4);
-    constexpr int DQ = D / 4;                 // groups of 4 dims
-    const int dq = tid % DQ, vg = tid / DQ;   // D = 128: 8 groups of 8 keys; D = 64: 16 of 4
-    const int vkey = D == 128 ? 16 * (vg >> 1) + 4 * (vg & 1) : 16 * (vg >> 2) + 4 * (vg & 1) + 8 * ((vg >> 1) & 1);
-    struct Pages {
-      int k, v, s;
-    };
-    auto load_pages = [&](int i) {
-      const int t0 = base + kUnit * i;
-      if (PAGE64) {
-        const int id = page_at(t0);   // made scalar where it is used: that waits for the load
-        return Pages{id, id, id};
-      }
-      return Pages{page_at(t0 + kkey), page_at(t0 + vkey), page_at(t0 + 16 * (lane & 3))};
-    };
-    auto load_tile = [&](int i, const Pages& pg) {
-      Raw<D> x;
-      const int t0 = base + kUnit * i;
-      const uint8_t *pk, *pv;
-      if (PAGE64) {
-        const int64_t blk = block_of(uniform(pg.k)), at = ((blk << a.pshift) + (t0 & page_mask)) * D;
-        pk = a.p.kc + at + static_cast<unsigned>(kkey * D + kdim);
-        pv = a.p.vc + at + static_cast<unsigned>(vkey * D + 4 * dq);
-      } else {
-        pk = a.p.kc + ((block_of(pg.k) << a.pshift) + ((t0 + kkey) & page_mask)) * D + kdim;
-        pv = a.p.vc + ((block_of(pg.v) << a.pshift) + ((t0 + vkey) & page_mask)) * D + 4 * dq;
-      }
+    auto load_tile = [&](int i) {
+      Raw x;
+      const int page = uniform(info[((KT * i + (wv * (KT / 8) & ~15)) / GROUP) % kInfo].page);
+      const int64_t at = (static_cast<int64_t>(page) * a.p.Hkv + h) << a.pshift;
+      const int t0 = base + KT * i, tk = (t0 + kkey) & page_mask, tv = (t0 + vkey) & page_mask;
+      x.k = *reinterpret_cast<const u32x4*>(a.p.kc + at * D + static_cast<unsigned>(tk * D + kdim));
+      const uint8_t* pv = a.p.vc + at * D + static_cast<unsigned>(tv * D + 4 * dq);
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) x.k[c] = *reinterpret_cast<const u32x4*>(pk + 16 * c);
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + (j < 4 ? j : j + 4) * D);
-      if (PAGE64 || wv == 0) {
-        const int64_t blk = block_of(PAGE64 ? uniform(pg.k) : pg.s);
-        x.ks = a.p.ks[blk];
-        x.vs = a.p.vs[blk];
-      }
+      for (int j = 0; j < 4; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + j * D);
       return x;
     };
-    // factors of a block: of its scores, log2 and inverse of its value scale;
-    // `none`: keys that no row sees, whose scales may hold anything
-    auto set_factors = [&](float ks, float vs, bool none, float& kq, float& lv, float& iv) {
-      const float f = ks * a.scale_log2, v = none ? 1.0f : vs > kMinVScale ? vs : kMinVScale;
-      kq = none ? 1.0f : f > kMinKScale ? f : kMinKScale;
-      lv = __builtin_amdgcn_logf(v);
-      iv = __builtin_amdgcn_rcpf(v);
-    };
-    float next_kq = 0.0f, next_lv = 0.0f, next_iv = 0.0f;
-    auto stage = [&](int i, Raw<D>& x) {
-      const int buf = i & 1, t0 = base + kUnit * i;
-      uint16_t* kb = kbuf[buf] + kkey * D;
-      constexpr int C = D / 8;
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<bf16x8*>(kb + 8 * swizzle<C>(kkey, kdim / 8 + 2 * c + e)) =
-              bf16_of_codes(x.k[c][2 * e], x.k[c][2 * e + 1]);
-      if (t0 < t.lo || t0 + kUnit > t.hi) {   // keys that no row sees may hold anything
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          asm volatile("" : "+v"(x.v[j]));    // a branch: two tiles an item come here
-          const int key = t0 + vkey + (j < 4 ? j : j + 4);
-          if (key < t.lo || key >= t.hi) x.v[j] = 0u;
-        }
-      }
-      uint32_t lo4[4], hi4[4];
-      transpose4(x.v[0], x.v[1], x.v[2], x.v[3], lo4);
-      if (D == 128) transpose4(x.v[D / 16 - 4], x.v[D / 16 - 3], x.v[D / 16 - 2], x.v[D / 16 - 1], hi4);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int d = 4 * dq + u;
-        if (D == 128) {
-          *reinterpret_cast<f16x8*>(vbuf[buf] + d * kUnit + 8 * swizzle<8>(d, vg)) = f16_of_codes(lo4[u], hi4[u]);
-        } else {
-          const f16x8 x8 = f16_of_codes(lo4[u], 0u);
-          const u32x4 y = __builtin_bit_cast(u32x4, x8);
-          // chunk (16-key step, half), its first or second four keys
-          *reinterpret_cast<u32x2*>(vbuf[buf] + d * kUnit + 8 * swizzle<8>(d, 2 * (vg >> 2) + (vg & 1)) +
-                                    4 * ((vg >> 1) & 1)) = u32x2{y[0], y[1]};
-        }
-      }
-      if (PAGE64) {   // the tile's factors wait in registers for their turn
-        set_factors(x.ks, x.vs, false, next_kq, next_lv, next_iv);
-      } else if (tid < 4) {
-        const int key = t0 + 16 * tid;
-        set_factors(x.ks, x.vs, key >= t.hi || key + 16 <= t.lo, scales[buf][tid][0], scales[buf][tid][1],
-                    scales[buf][tid][2]);
+    // Decoding of tile i in parts 0 .. 7: the key's 16 codes, the values' bytes
+    // turned, then four dims of four keys.
+    uint32_t turned[4];
+    auto stage = [&](int i, const Raw& x, int part) {
+      if (part < 2) {
+        *reinterpret_cast<bf16x8*>(kbuf[i & 1] + kkey * D + 8 * swizzle<D / 8>(kkey, kdim / 8 + part)) =
+            bf16_of_codes(x.k[2 * part], x.k[2 * part + 1]);
+      } else if (part == 3) {
+        transpose4(x.v[0], x.v[1], x.v[2], x.v[3], turned);
+      } else if (part >= 4) {
+        const int d = 4 * dq + part - 4;
+        const u32x4 y = __builtin_bit_cast(u32x4, f16_of_codes(turned[part - 4], 0u));
+        *reinterpret_cast<u32x2*>(vbuf[i % 3] + d * KT + 8 * swizzle<VC>(d, vg >> 1) + 4 * (vg & 1)) = u32x2{y[0], y[1]};
       }
     };
-    // MASK: some row of the wave does not see all keys of the tile
-    auto compute = [&](int i, auto mask, float kq1, float lv1, float iv1) {
-      constexpr bool MASK = decltype(mask)::value;
-      const int buf = i & 1, t0 = base + kUnit * i;
-      f32x16 sc[2];
+    // values of keys that no row sees may hold anything: they become zeros
+    auto clear_values = [&](int i, Raw& x) {
+      const int t0 = base + KT * i;
+      if (t0 < plo || t0 + KT > phi) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sc[x][j] = 0.0f;
-      // operands are read from LDS kAhead products before they are used
-      {
-        bf16x8 kf[2 * NS];
-        auto read = [&](int e) {
-          const int key = 32 * (e & 1) + n32;
-          kf[e] = *reinterpret_cast<const bf16x8*>(kbuf[buf] + key * D + 8 * swizzle<D / 8>(key, 2 * (e >> 1) + h2));
-        };
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) read(e);
-#pragma unroll
-        for (int e = 0; e < 2 * NS; ++e) {
-          if (e + kAhead < 2 * NS) read(e + kAhead);
-          sc[e & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[e], qf[e >> 1], sc[e & 1], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          asm volatile("" : "+v"(x.v[j]));   // a branch: two tiles an item come here
+          const int key = t0 + vkey + j;
+          if (key < plo || key >= phi) x.v[j] = 0u;
         }
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
-#pragma unroll
-        for (int e = 0; e < 2 * NS - kAhead; ++e) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
       }
+    };
+
+    auto clip = [&](int i) { return i < tiles ? i : tiles - 1; };
+    f32x16 sc[NX];
+    f16x8 pf[NY];
+    Raw x;
+    // Scores of tile i; between the products the values of tile i + 1 are decoded
+    // and the loads after them issued.
+    auto keys = [&](int i) {
+      constexpr int N = NX * NS;
+      const uint16_t* kb = kbuf[i & 1];
+      bf16x8 kf[N];
+      auto read = [&](int e) {
+        const int key = 32 * (e % NX) + n32;
+        kf[e] = *reinterpret_cast<const bf16x8*>(kb + key * D + 8 * swizzle<D / 8>(key, 2 * (e / NX) + h2));
+      };
+#pragma unroll
+      for (int q = 0; q < NX; ++q)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sc[q][j] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) read(e);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (e + kAhead < N) read(e + kAhead);
+        sc[e % NX] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[e], qf[e / NX], sc[e % NX], 0, 0, 0);
+        if (e % 3 == 2 && e < 12) stage(i + 1, x, 4 + e / 3);
+        if (e == 12) x = load_tile(clip(i + 2));
+        FP8BS_PIN();
+      }
+    };
+    // Output of tile i - 1; between the products the keys of tile i + 1 are decoded.
+    auto values = [&](int i) {
+      constexpr int N = NY * ND;
+      const uint16_t* vb = vbuf[(i + 2) % 3];
+      f16x8 vf[N];
+      auto read = [&](int e) {
+        const int d = 32 * (e % ND) + n32;
+        vf[e] = *reinterpret_cast<const f16x8*>(vb + d * KT + 8 * swizzle<VC>(d, 2 * (e / ND) + h2));
+      };
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) read(e);
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        if (e + kAhead < N) read(e + kAhead);
+        o[e % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[e], pf[e / ND], o[e % ND], 0, 0, 0);
+        if (e % 4 == 3) stage(i + 1, x, e / 4);
+        FP8BS_PIN();
+      }
+    };
+    auto softmax = [&](int i) {
+      const int t0 = base + KT * i;
       float kq[NG], lv[NG], iv[NG];
-      if (PAGE64) {
-        kq[0] = kq1;
-        lv[0] = lv1;
-        iv[0] = iv1;
-      } else {
 #pragma unroll
-        for (int y = 0; y < NG; ++y) {
-          kq[y] = scales[buf][y][0];
-          lv[y] = scales[buf][y][1];
-          iv[y] = scales[buf][y][2];
-        }
+      for (int y = 0; y < NG; ++y) {
+        const Group g = info[(NG * i + y) % kInfo];
+        kq[y] = g.kq;
+        lv[y] = g.lv;
+        iv[y] = g.iv;
       }
-      if (MASK) {
+      if (i < b1 || i >= b2) {
         const int from = rlo - t0 - 4 * h2, to = rhi - t0 - 4 * h2;
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int x = 0; x < NX; ++x)
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int key = 32 * x + 8 * (j >> 2) + (j & 3);
@@ -260,24 +268,23 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       }
       // weights under the reference as it stands; their sum shows whether it
       // still holds (no weight above 2^15), which spares the maximum
-      f16x8 pf[4];
       float sum[NG];
       auto weigh = [&]() {
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int gr = PAGE64 ? 0 : y;
-          const float c = lv[gr] - mr;
+        for (int y = 0; y < NY; ++y) {
+          const int gr = 16 * y / GROUP;
+          const float off = lv[gr] - mr;
           float e[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[y >> 1][8 * (y & 1) + j], kq[gr], c));
+            e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[y >> 1][8 * (y & 1) + j], kq[gr], off));
           u32x4 pw;
 #pragma unroll
           for (int j = 0; j < 4; ++j) pw[j] = pack_f16x2(e[2 * j], e[2 * j + 1]);
           pf[y] = __builtin_bit_cast(f16x8, pw);
           const float s8 = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          if (PAGE64 && y > 0) sum[0] += s8;
-          else sum[gr] = s8;
+          if (16 * y % GROUP == 0) sum[gr] = s8;
+          else sum[gr] += s8;
         }
       };
       weigh();
@@ -287,8 +294,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       if (__builtin_expect(__ballot(all > kMostWeight) != 0, 0)) {
         float top = -__builtin_huge_valf();
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int gr = PAGE64 ? 0 : y;
+        for (int y = 0; y < NY; ++y) {
+          const int gr = 16 * y / GROUP;
           float m = sc[y >> 1][8 * (y & 1)];
 #pragma unroll
           for (int j = 1; j < 8; ++j) m = __builtin_fmaxf(m, sc[y >> 1][8 * (y & 1) + j]);
@@ -308,66 +315,40 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int y = 0; y < NG; ++y) lr = __builtin_fmaf(sum[y], iv[y], lr);
-      {
-        f16x8 vf[4 * ND];
-        auto read = [&](int e) {
-          const int d = 32 * (e % ND) + n32;
-          vf[e] = *reinterpret_cast<const f16x8*>(vbuf[buf] + d * kUnit + 8 * swizzle<8>(d, 2 * (e / ND) + h2));
-        };
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) read(e);
-#pragma unroll
-        for (int e = 0; e < 4 * ND; ++e) {
-          if (e + kAhead < 4 * ND) read(e + kAhead);
-          o[e % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[e], pf[e / ND], o[e % ND], 0, 0, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 1);
-#pragma unroll
-        for (int e = 0; e < 4 * ND - kAhead; ++e) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 1);
-      }
     };
 
     if (tiles > 0) {
-      // the wave's way through the tiles: none of its rows sees the first and
-      // last ones, all rows see all of the middle ones; masks between
-      auto tile_floor = [&](int key) { const int x = (key - base) >> 6; return x < 0 ? 0 : x > tiles ? tiles : x; };
-      int b0 = tile_floor(wlo_first), b3 = tile_floor(whi_last + kUnit - 1);
-      if (!live || b3 < b0) b0 = b3 = tiles;
-      int b1 = tile_floor(wlo_last + kUnit - 1), b2 = tile_floor(whi_first);
-      b1 = b1 < b0 ? b0 : b1 > b3 ? b3 : b1;
-      b2 = b2 < b1 ? b1 : b2 > b3 ? b3 : b2;
-      // on their way: the next tile's codes, and the page numbers of the one after
-      Pages pg = load_pages(0), next = load_pages(tiles > 1 ? 1 : 0);
-      Raw<D> x = load_tile(0, pg);
-      pg = load_pages(tiles > 2 ? 2 : 0);
+      // The groups are a ring of two halves.  The first group of waves fills a half
+      // for the tiles after next half, four tiles after the other waves are
+      // done with what it held.
+      constexpr int HALF = kInfo / 2 / NG;   // tiles of a half
       __syncthreads();   // the piece before is done with the buffers
-      stage(0, x);
-      x = load_tile(tiles > 1 ? 1 : 0, next);
+      fill_info(tid);
       __syncthreads();
-      auto run = [&](int from, int to, auto kind) {
-        for (int i = from; i < to; ++i) {
-          const float kq = next_kq, lv = next_lv, iv = next_iv;
-          if (i + 1 < tiles) {
-            stage(i + 1, x);
-            if (i + 2 < tiles) {
-              x = load_tile(i + 2, pg);
-              if (i + 3 < tiles) pg = load_pages(i + 3);
-            }
-          }
-          if constexpr (decltype(kind)::value == 1) compute(i, std::true_type{}, kq, lv, iv);
-          if constexpr (decltype(kind)::value == 2) compute(i, std::false_type{}, kq, lv, iv);
-          __syncthreads();
-        }
-      };
-      run(0, b0, std::integral_constant<int, 0>{});
-      run(b0, b1, std::integral_constant<int, 1>{});
-      run(b1, b2, std::integral_constant<int, 2>{});
-      run(b2, b3, std::integral_constant<int, 1>{});
-      run(b3, tiles, std::integral_constant<int, 0>{});
+      x = load_tile(0);
+      {
+        Raw first = x;
+        x = load_tile(clip(1));
+        clear_values(0, first);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) stage(0, first, e);
+      }
+      __syncthreads();
+      if (second) __syncthreads();   // one turn behind
+      clear_values(1, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) stage(1, x, e);
+      keys(0);
+      for (int i = 0; i < tiles; ++i) {
+        __syncthreads();
+        softmax(i);
+        if (!second && i > HALF && i % HALF == 4) fill_info(NG * (i - 4 + HALF) + tid);
+        __syncthreads();
+        clear_values(i + 2, x);
+        values(i + 1);
+        keys(i + 1);   // past the last tile: of no use, on keys that are there
+      }
+      if (!second) __syncthreads();
     }
 
     // lane pair (l, l + 32) holds row n32: dims 32 u + 8 k + 4 h2 + 0..3
@@ -389,7 +370,7 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
           a.p.lse[token * a.p.ldl + head] =
               lr > 0.0f ? (mr + __builtin_amdgcn_logf(lr)) * 0.693147180559945f : -__builtin_huge_valf();
       } else {
-        float* at = a.part + piece_of(c) * kRows * (D + 2);
+        float* at = a.part + piece_of(c) * kManyRows * (D + 2);
 #pragma unroll
         for (int u = 0; u < ND; ++u)
 #pragma unroll
@@ -397,24 +378,24 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
             *reinterpret_cast<float4*>(at + row * D + 32 * u + 8 * k + 4 * h2) =
                 make_float4(o[u][4 * k], o[u][4 * k + 1], o[u][4 * k + 2], o[u][4 * k + 3]);
         if (h2 == 0) {
-          at[kRows * D + 2 * row] = mr;
-          at[kRows * D + 2 * row + 1] = lr;
+          at[kManyRows * D + 2 * row] = mr;
+          at[kManyRows * D + 2 * row + 1] = lr;
         }
       }
     }
-    end_piece(a, kRows, c);
+    end_piece(a, kManyRows, c);
   }
 }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(const AttnArgs& a, unsigned blocks, hipStream_t st) {
-  const dim3 grid(blocks), block(256);
-  const bool page64 = a.p.page >= kUnit;
-  if (a.p.D == 64 && page64) hipLaunchKernelGGL((attn_prompt_kernel<64, true>), grid, block, 0, st, a);
-  else if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64, false>), grid, block, 0, st, a);
-  else if (page64) hipLaunchKernelGGL((attn_prompt_kernel<128, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((attn_prompt_kernel<128, false>), grid, block, 0, st, a);
+  const dim3 grid(blocks), block(512);
+  const bool wide = a.p.page >= 64;
+  if (a.p.D == 64 && wide) hipLaunchKernelGGL((attn_prompt_kernel<64, 64>), grid, block, 0, st, a);
+  else if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64, 16>), grid, block, 0, st, a);
+  else if (wide) hipLaunchKernelGGL((attn_prompt_kernel<128, 64>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((attn_prompt_kernel<128, 16>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

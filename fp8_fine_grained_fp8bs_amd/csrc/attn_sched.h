@@ -20,6 +20,7 @@
 namespace fp8bs {
 
 constexpr int kUnit = 64;          // keys of a unit
+constexpr int kManyRows = 256;     // rows of a tile of the many-rows kernel
 constexpr int kMaxSlots = 2048;    // tiles a head that the line can hold
 
 struct AttnArgs {
@@ -223,7 +224,7 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
   }
   // prefix sums of every slot in LDS
   int* prefix = static_cast<int*>(lds);
-  const int each = (a.slots + 255) >> 8;
+  const int each = tid < 256 ? (a.slots + 255) >> 8 : 0;   // the first four waves add them up
   int mine = 0;
   for (int i = 0; i < each; ++i) {
     const int s = tid * each + i;
@@ -233,7 +234,7 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
     }
   }
   const int upto = wave_scan(mine);
-  if (lane == 63) sums[tid >> 6] = upto;
+  if (lane == 63 && tid < 256) sums[tid >> 6] = upto;
   __syncthreads();
   int before = upto - mine, all = 0;
   for (int w = 0; w < 4; ++w) {

@@ -384,7 +384,7 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  const int full = p.R == kManyRows ? 256 : 512;   // resident workgroups: one or two a compute unit
+  const int full = 512;   // resident workgroups: two a compute unit
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t items = p.slots * Hkv;
   // whole items where there are enough of them to fill the GPU several times

@@ -2,25 +2,14 @@
 // key/value head (prompts and their pieces), on gfx950.
 //
 // 4 D operations a row and key against 2 D / R bytes of cache: bound by the
-// matrix units at R = 256 rows a tile, with as much vector work (softmax, decoding)
-// to be hidden under them.  A workgroup of eight waves takes 256 rows, a wave 32 of them;
-// the cache goes by in tiles of KT keys, read once a workgroup, decoded once
-// (keys to BF16, values to FP16, both exact) and shared through LDS.
-//
-// A compute unit holds one workgroup, a SIMD two of its waves: one of the first group
-// (waves 0..3), one of the second.  The groups alternate: while one multiplies
-// (the product of the last tile's weights with its values, then of the queries with
-// the next tile's keys), the other does its softmax and its share of the
-// decoding, and a barrier ends each turn.  So the matrix units run in every turn
-// and the vector units beside them; left to themselves two waves did both in
-// step and took the sum of the two times (measured: 618 us against a
-// matrix and LDS time of 400 at 8192 x 8192 keys, 32 heads of 128).
-//
-// turn 2i      first group multiplies (tile i-1 values, tile i keys), second group: softmax of tile i-1
-// turn 2i + 1  first group: softmax of tile i, second group multiplies (tile i-1 values, tile i keys)
-// Decoding of a tile has to be done two turns before its keys are read by the first
-// group, so the first group decodes its half of tile i + 1 beside the softmax of tile i,
-// the second group of tile i + 2.  Keys then need two LDS buffers, values three.
+// matrix units at R = 128 rows a tile, with as much vector work (softmax,
+// decoding) beside them.  A workgroup of four waves takes 128 rows, a wave 32
+// of them; the cache goes by in tiles of 64 keys, read once a workgroup,
+// decoded once (keys to BF16, values to FP16, both exact) and shared through
+// two LDS buffers.  While a tile is multiplied the next one is decoded between
+// the products and the one after is on its way from memory, so a tile costs
+// one barrier.  Two workgroups live on a compute unit and share no barrier,
+// so one's softmax runs under the other's products.
 //
 // Mathematics and number formats are those of the few-rows kernel: S^T = K Q^T
 // (32x32x16 BF16 MFMAs), p' = 2^(s k c + log2 v - m) with the value scale v
@@ -37,7 +26,6 @@ namespace fp8bs {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 constexpr int kAhead = 4;   // LDS reads in flight before their products
 
 // Instructions stay on their side of this: matrix and other work is laid out
@@ -57,19 +45,19 @@ struct __attribute__((aligned(16))) Group {
   float kq, lv, iv;
   int page;
 };
-constexpr int kInfo = 512;
+constexpr int kInfo = 256;
 
 // GROUP: keys that surely share a page, hence a pair of scales: 64 where a page holds as
 // many, else 16.
 template <int D, int GROUP>
-__global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
-  constexpr int KT = 8192 / D;            // keys of a tile: 8 KB of codes each side
+__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
+  constexpr int KT = kUnit;               // keys of a tile
   constexpr int NS = D / 16, NX = KT / 32;   // MFMA steps over the inner dim, 32-key tiles
   constexpr int ND = D / 32, NY = KT / 16;   // 32-dim tiles of the output, 16-key steps
   constexpr int NG = KT / GROUP;          // scale groups of a tile
   constexpr int VC = KT / 8;              // 16-byte chunks of a value row
   __shared__ __attribute__((aligned(16))) uint16_t kbuf[2][KT * D];
-  __shared__ __attribute__((aligned(16))) uint16_t vbuf[3][D * KT];
+  __shared__ __attribute__((aligned(16))) uint16_t vbuf[2][D * KT];
   // factors and page of the piece's groups, kInfo at a time: read in the loop
   // by one LDS access each, where memory would cost a chain of three loads
   __shared__ Group info[kInfo];
@@ -79,7 +67,6 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
   poison_lds<sizeof(vbuf)>(vbuf);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = uniform(tid >> 6);
   const int n32 = lane & 31, h2 = lane >> 5;
-  const bool second = wv >= 4;
   const int page_mask = (1 << a.pshift) - 1;
 
   Cursor c;
@@ -148,41 +135,49 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
       g.iv = __builtin_amdgcn_rcpf(v);
       info[e % kInfo] = g;
     };
-    // Decoding: a thread takes 16 codes of one key, and four values of four
-    // keys.  A wave's keys lie in one sixteen, so in one page.
-    const int kkey = tid / (D / 16), kdim = (tid % (D / 16)) * 16;
-    constexpr int DQ = D / 4;
-    const int dq = tid % DQ, vg = tid / DQ;
-    // values' keys in the order that the weights come in: step, lane half, fours
-    const int vkey = 16 * (vg >> 2) + 8 * (vg & 1) + 4 * ((vg >> 1) & 1);
+    // Decoding: a thread takes D / 4 codes of one key, and D / 16 keys by 4 dims of
+    // the values, in the order of keys that the weights come in.  A wave's keys
+    // lie in one sixteen, so in one page.
+    const int kkey = tid >> 2, kdim = (tid & 3) * (D / 4);
+    constexpr int DQ = D / 4, RV = D / 16;
+    const int dq = tid % DQ, vg = tid / DQ;   // D = 128: 8 groups of 8 keys; D = 64: 16 of 4
+    const int vkey = D == 128 ? 16 * (vg >> 1) + 4 * (vg & 1) : 16 * (vg >> 2) + 8 * (vg & 1) + 4 * ((vg >> 1) & 1);
     struct Raw {
-      u32x4 k;
-      uint32_t v[4];
+      u32x4 k[D / 64];
+      uint32_t v[RV];
     };
     auto load_tile = [&](int i) {
       Raw x;
-      const int page = uniform(info[((KT * i + (wv * (KT / 8) & ~15)) / GROUP) % kInfo].page);
+      const int page = uniform(info[((KT * i + 16 * wv) / GROUP) % kInfo].page);
       const int64_t at = (static_cast<int64_t>(page) * a.p.Hkv + h) << a.pshift;
       const int t0 = base + KT * i, tk = (t0 + kkey) & page_mask, tv = (t0 + vkey) & page_mask;
-      x.k = *reinterpret_cast<const u32x4*>(a.p.kc + at * D + static_cast<unsigned>(tk * D + kdim));
+      const uint8_t* pk = a.p.kc + at * D + static_cast<unsigned>(tk * D + kdim);
       const uint8_t* pv = a.p.vc + at * D + static_cast<unsigned>(tv * D + 4 * dq);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + j * D);
+      for (int e = 0; e < D / 64; ++e) x.k[e] = *reinterpret_cast<const u32x4*>(pk + 16 * e);
+#pragma unroll
+      for (int j = 0; j < RV; ++j) x.v[j] = *reinterpret_cast<const uint32_t*>(pv + (j < 4 ? j : j + 4) * D);
       return x;
     };
-    // Decoding of tile i in parts 0 .. 7: the key's 16 codes, the values' bytes
-    // turned, then four dims of four keys.
-    uint32_t turned[4];
+    // Decoding of tile i in parts: the keys' 8 codes at a time (0 .. D/32 - 1), the
+    // values' bytes turned (4), then four dims (5 .. 8).
+    uint32_t lo4[4], hi4[4];
     auto stage = [&](int i, const Raw& x, int part) {
-      if (part < 2) {
+      if (part < D / 32) {
         *reinterpret_cast<bf16x8*>(kbuf[i & 1] + kkey * D + 8 * swizzle<D / 8>(kkey, kdim / 8 + part)) =
-            bf16_of_codes(x.k[2 * part], x.k[2 * part + 1]);
-      } else if (part == 3) {
-        transpose4(x.v[0], x.v[1], x.v[2], x.v[3], turned);
-      } else if (part >= 4) {
-        const int d = 4 * dq + part - 4;
-        const u32x4 y = __builtin_bit_cast(u32x4, f16_of_codes(turned[part - 4], 0u));
-        *reinterpret_cast<u32x2*>(vbuf[i % 3] + d * KT + 8 * swizzle<VC>(d, vg >> 1) + 4 * (vg & 1)) = u32x2{y[0], y[1]};
+            bf16_of_codes(x.k[part >> 1][2 * (part & 1)], x.k[part >> 1][2 * (part & 1) + 1]);
+      } else if (part == 4) {
+        transpose4(x.v[0], x.v[1], x.v[2], x.v[3], lo4);
+        if (D == 128) transpose4(x.v[RV - 4], x.v[RV - 3], x.v[RV - 2], x.v[RV - 1], hi4);
+      } else if (part > 4) {
+        const int u = part - 5, d = 4 * dq + u;
+        uint16_t* vb = vbuf[i & 1] + d * KT;
+        if (D == 128) {
+          *reinterpret_cast<f16x8*>(vb + 8 * swizzle<VC>(d, vg)) = f16_of_codes(lo4[u], hi4[u]);
+        } else {
+          const u32x4 y = __builtin_bit_cast(u32x4, f16_of_codes(lo4[u], 0u));
+          *reinterpret_cast<u32x2*>(vb + 8 * swizzle<VC>(d, vg >> 1) + 4 * (vg & 1)) = u32x2{y[0], y[1]};
+        }
       }
     };
     // values of keys that no row sees may hold anything: they become zeros
@@ -190,9 +185,9 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
       const int t0 = base + KT * i;
       if (t0 < plo || t0 + KT > phi) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < RV; ++j) {
           asm volatile("" : "+v"(x.v[j]));   // a branch: two tiles an item come here
-          const int key = t0 + vkey + j;
+          const int key = t0 + vkey + (j < 4 ? j : j + 4);
           if (key < plo || key >= phi) x.v[j] = 0u;
         }
       }
@@ -202,47 +197,43 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
     f32x16 sc[NX];
     f16x8 pf[NY];
     Raw x;
-    // Scores of tile i; between the products the values of tile i + 1 are decoded
-    // and the loads after them issued.
-    auto keys = [&](int i) {
-      constexpr int N = NX * NS;
-      const uint16_t* kb = kbuf[i & 1];
-      bf16x8 kf[N];
+    // Operands are read from LDS kAhead products before their use; between the
+    // products the next tile is decoded and the loads after it issued.
+    constexpr int NV = NY * ND, NK = NX * NS;
+    auto scores = [&](int i) {
       auto read = [&](int e) {
         const int key = 32 * (e % NX) + n32;
-        kf[e] = *reinterpret_cast<const bf16x8*>(kb + key * D + 8 * swizzle<D / 8>(key, 2 * (e / NX) + h2));
+        return *reinterpret_cast<const bf16x8*>(kbuf[i & 1] + key * D + 8 * swizzle<D / 8>(key, 2 * (e / NX) + h2));
       };
+      bf16x8 f[NK];
+#pragma unroll
+      for (int e = 0; e < kAhead; ++e) f[e] = read(e);
 #pragma unroll
       for (int q = 0; q < NX; ++q)
 #pragma unroll
         for (int j = 0; j < 16; ++j) sc[q][j] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) read(e);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (e + kAhead < N) read(e + kAhead);
-        sc[e % NX] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[e], qf[e / NX], sc[e % NX], 0, 0, 0);
-        if (e % 3 == 2 && e < 12) stage(i + 1, x, 4 + e / 3);
-        if (e == 12) x = load_tile(clip(i + 2));
+      for (int e = 0; e < NK; ++e) {
+        if (e + kAhead < NK) f[e + kAhead] = read(e + kAhead);
+        sc[e % NX] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[e], qf[e / NX], sc[e % NX], 0, 0, 0);
+        if (e % (NK / 4) == NK / 4 - 1) stage(i + 1, x, e / (NK / 4));
         FP8BS_PIN();
       }
     };
-    // Output of tile i - 1; between the products the keys of tile i + 1 are decoded.
-    auto values = [&](int i) {
-      constexpr int N = NY * ND;
-      const uint16_t* vb = vbuf[(i + 2) % 3];
-      f16x8 vf[N];
+    auto output = [&](int i) {
       auto read = [&](int e) {
         const int d = 32 * (e % ND) + n32;
-        vf[e] = *reinterpret_cast<const f16x8*>(vb + d * KT + 8 * swizzle<VC>(d, 2 * (e / ND) + h2));
+        return *reinterpret_cast<const f16x8*>(vbuf[i & 1] + d * KT + 8 * swizzle<VC>(d, 2 * (e / ND) + h2));
       };
+      f16x8 f[NV];
 #pragma unroll
-      for (int e = 0; e < kAhead; ++e) read(e);
+      for (int e = 0; e < kAhead; ++e) f[e] = read(e);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        if (e + kAhead < N) read(e + kAhead);
-        o[e % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[e], pf[e / ND], o[e % ND], 0, 0, 0);
-        if (e % 4 == 3) stage(i + 1, x, e / 4);
+      for (int e = 0; e < NV; ++e) {
+        if (e + kAhead < NV) f[e + kAhead] = read(e + kAhead);
+        o[e % ND] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[e], pf[e / ND], o[e % ND], 0, 0, 0);
+        if (e < 5) stage(i + 1, x, 4 + e);
+        if (e == 5) x = load_tile(clip(i + 2));
         FP8BS_PIN();
       }
     };
@@ -318,9 +309,8 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
     };
 
     if (tiles > 0) {
-      // The groups are a ring of two halves.  The first group of waves fills a half
-      // for the tiles after next half, four tiles after the other waves are
-      // done with what it held.
+      // The groups are a ring of two halves; a half is filled again four tiles
+      // after the last use of what it held.
       constexpr int HALF = kInfo / 2 / NG;   // tiles of a half
       __syncthreads();   // the piece before is done with the buffers
       fill_info(tid);
@@ -331,24 +321,17 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
         x = load_tile(clip(1));
         clear_values(0, first);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) stage(0, first, e);
+        for (int e = 0; e < 9; ++e) stage(0, first, e);
       }
       __syncthreads();
-      if (second) __syncthreads();   // one turn behind
-      clear_values(1, x);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) stage(1, x, e);
-      keys(0);
       for (int i = 0; i < tiles; ++i) {
-        __syncthreads();
+        clear_values(i + 1, x);
+        scores(i);
         softmax(i);
-        if (!second && i > HALF && i % HALF == 4) fill_info(NG * (i - 4 + HALF) + tid);
+        output(i);
+        if (i > HALF && i % HALF == 4 && tid < kInfo / 2) fill_info(NG * (i - 4 + HALF) + tid);
         __syncthreads();
-        clear_values(i + 2, x);
-        values(i + 1);
-        keys(i + 1);   // past the last tile: of no use, on keys that are there
       }
-      if (!second) __syncthreads();
     }
 
     // lane pair (l, l + 32) holds row n32: dims 32 u + 8 k + 4 h2 + 0..3
@@ -390,7 +373,7 @@ __global__ __launch_bounds__(512, 2) void attn_prompt_kernel(AttnArgs a) {
 }  // namespace
 
 hipError_t launch_attn_prompt(const AttnArgs& a, unsigned blocks, hipStream_t st) {
-  const dim3 grid(blocks), block(512);
+  const dim3 grid(blocks), block(256);
   const bool wide = a.p.page >= 64;
   if (a.p.D == 64 && wide) hipLaunchKernelGGL((attn_prompt_kernel<64, 64>), grid, block, 0, st, a);
   else if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64, 16>), grid, block, 0, st, a);

@@ -20,7 +20,7 @@
 namespace fp8bs {
 
 constexpr int kUnit = 64;          // keys of a unit
-constexpr int kManyRows = 256;     // rows of a tile of the many-rows kernel
+constexpr int kManyRows = 128;     // rows of a tile of the many-rows kernel
 constexpr int kMaxSlots = 2048;    // tiles a head that the line can hold
 
 struct AttnArgs {

@@ -47,7 +47,7 @@ struct Pages {
 };
 
 template <int D, int NR>
-__global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_kernel(AttnArgs a) {
   constexpr int R = 16 * NR, VW = D / 16, NW = D / 64;
   __shared__ __attribute__((aligned(16))) float obuf[4][16][D + 4];
   __shared__ float ml[4][16][2];
@@ -60,14 +60,32 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
 
   Cursor c;
   if (!begin_work(a, R, false, obuf, sums, c)) return;
-  while (c.cur < c.stop) {
-    take_piece(c);
-    const Tile& t = c.t;
-    const int h = c.h;
-
-    // queries: the B operand, row m16 of each 16-row group
-    bf16x8 qf[NR][2 * NW];
-    int rlo[NR], rhi[NR];
+  take_piece(c);
+  const Tile& t = c.t;
+  const int& h = c.h;
+  // The piece at hand: its queries (B operands, row m16 of each 16-row group),
+  // the keys that the lane's rows and all rows see, its steps of 32 keys, and
+  // the page numbers of the wave's next step.
+  bf16x8 qf[NR][2 * NW];
+  int rlo[NR], rhi[NR];
+  int all_lo, all_hi, base, steps;
+  const int32_t* table;
+  Pages pg;
+  const int last_page = static_cast<int>(a.p.max_pages) - 1;
+  auto load_pages = [&](int s) {
+    Pages p;
+    const int t0 = base + 32 * s;
+    const int ik = (t0 + 8 * (m16 >> 2)) >> a.pshift, iv = (t0 + 8 * g) >> a.pshift;
+    p.k = table[ik < last_page ? ik : last_page];
+    p.v = table[iv < last_page ? iv : last_page];
+    return p;
+  };
+  auto open_piece = [&]() {
+    table = a.p.table + t.b * a.p.ldt;
+    base = (t.u0 + c.ub) * kUnit;
+    steps = (c.ue - c.ub) * (kUnit / 32);
+    if (base + 32 * steps > t.hi) steps = t.hi > base ? (t.hi - base + 31) / 32 : 0;
+    if (wv < steps) pg = load_pages(wv);
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int row = 16 * r + m16;
@@ -77,19 +95,20 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       if (!there) rhi[r] = 0;
       const uint16_t* q = a.p.q + row_token(a, t, rr) * a.p.ldq + static_cast<int64_t>(row_head(a, t, h, rr)) * D;
 #pragma unroll
-      for (int c = 0; c < 2 * NW; ++c) {
+      for (int e = 0; e < 2 * NW; ++e) {
         const u32x4 zero = {0u, 0u, 0u, 0u};
-        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 64 * (c >> 1) + 16 * g + 8 * (c & 1));
-        qf[r][c] = __builtin_bit_cast(bf16x8, there ? x : zero);
+        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 64 * (e >> 1) + 16 * g + 8 * (e & 1));
+        qf[r][e] = __builtin_bit_cast(bf16x8, there ? x : zero);
       }
     }
     // keys that every row sees need no mask
-    int64_t pf = static_cast<int64_t>(t.len) - t.n + t.row0 / a.G;
-    int64_t pl = static_cast<int64_t>(t.len) - t.n + (t.row0 + t.rows - 1) / a.G;
-    const int all_hi = a.p.causal && pf + 1 < t.len ? static_cast<int>(pf < -1 ? 0 : pf + 1) : t.len;
-    const int64_t wlo = a.p.window > 0 ? pl - a.p.window + 1 : 0;
-    const int all_lo = wlo > 0 ? static_cast<int>(wlo) : 0;
+    int x;
+    row_keys(a, t, t.row0, x, all_hi);
+    row_keys(a, t, t.row0 + t.rows - 1, all_lo, x);
+  };
+  open_piece();
 
+  while (true) {
     f32x4 o[NR][4 * NW];
     float mr[NR], lr[NR];
 #pragma unroll
@@ -100,22 +119,9 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
       for (int i = 0; i < 4 * NW; ++i) o[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    const int32_t* table = a.p.table + t.b * a.p.ldt;
-    const int last_page = static_cast<int>(a.p.max_pages) - 1;
-    const int base = (t.u0 + c.ub) * kUnit;
-    int steps = (c.ue - c.ub) * (kUnit / 32);
-    if (base + 32 * steps > t.hi) steps = t.hi > base ? (t.hi - base + 31) / 32 : 0;
     auto clamp_page = [&](int id) {
       const unsigned u = static_cast<unsigned>(id), n = static_cast<unsigned>(a.p.n_pages) - 1u;
       return static_cast<int>(u < n ? u : n);
-    };
-    auto load_pages = [&](int s) {
-      Pages p;
-      const int t0 = base + 32 * s;
-      const int ik = (t0 + 8 * (m16 >> 2)) >> a.pshift, iv = (t0 + 8 * g) >> a.pshift;
-      p.k = table[ik < last_page ? ik : last_page];
-      p.v = table[iv < last_page ? iv : last_page];
-      return p;
     };
     auto load_step = [&](int s, const Pages& pg) {
       Step<D> x;
@@ -224,7 +230,6 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
 
     // the wave's steps: wv, wv + 4, ...
     if (wv < steps) {
-      Pages pg = load_pages(wv);
       Step<D> x = load_step(wv, pg);
       if (wv + 4 < steps) pg = load_pages(wv + 4);
       int s = wv;
@@ -245,6 +250,18 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         s += 4;
         if (s >= steps) break;
       }
+    }
+
+    // The next piece's lookups go out before this one's waves are joined.
+    const Tile dt = c.t;
+    const int dh = c.h;
+    const bool whole = c.whole, more = c.cur < c.stop;
+    const int64_t piece = piece_of(c);
+    record_piece(a, c);
+    if (more) {
+      next_item(a, R, c);
+      take_piece(c);
+      open_piece();
     }
 
     // join the four waves: row r of the group, D/16 dims a thread
@@ -281,12 +298,12 @@ __global__ __launch_bounds__(256, 2) void attn_rows_kernel(AttnArgs a) {
         for (int i = 0; i < VW; ++i) sum[i] = __builtin_fmaf(f, obuf[k][row][d0 + i], sum[i]);
       }
       const int tr = 16 * r + row;
-      if (tr < t.rows) {
-        if (c.whole) store_out<VW>(a, row_token(a, t, tr), row_head(a, t, h, tr), D, d0, sum, top, den);
-        else store_part<VW>(a.part, R, D, piece_of(c), tr, d0, sum, top, den);
+      if (tr < dt.rows) {
+        if (whole) store_out<VW>(a, row_token(a, dt, tr), row_head(a, dt, dh, tr), D, d0, sum, top, den);
+        else store_part<VW>(a.part, R, D, piece, tr, d0, sum, top, den);
       }
     }
-    end_piece(a, R, c);
+    if (!more) break;
   }
 }
 
@@ -374,6 +391,7 @@ struct Plan {
 };
 
 constexpr int64_t kMaxInt = 0x7fffffff;
+constexpr int64_t kBrief = 9;
 
 Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
   Plan p;
@@ -384,16 +402,18 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  const int full = 512;   // resident workgroups: two a compute unit
+  // resident workgroups: two a compute unit, of the lightest kernel four
+  const int full = p.R == 16 && D == 64 ? 1024 : 512;
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t items = p.slots * Hkv;
-  // whole items where there are enough of them to fill the GPU several times
-  // over (and where the line cannot hold them)
-  const bool many = p.R == kManyRows && items >= 4 * full;
+  // Whole items where sharing them is not worth its joins: contexts of a few
+  // units (a wave has two to four steps), or prompts with items enough to fill
+  // the GPU several times over; and where the line cannot hold them.
+  const bool brief = units <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 4 * full;
   p.workers = 0;
   p.bytes = 0;
   p.by_item = items <= full;
-  if (p.slots <= kMaxSlots && !many && items <= kMaxInt / units) {
+  if (p.slots <= kMaxSlots && !brief && !many && items <= kMaxInt / units) {
     const int64_t useful = items * ((units + p.min_units - 1) / p.min_units);
     p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
     p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 4 * full) * 4;

@@ -366,7 +366,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         }
       }
     }
-    end_piece(a, kManyRows, c);
+    record_piece(a, c);
+    if (c.cur < c.stop) next_item(a, kManyRows, c);
   }
 }
 

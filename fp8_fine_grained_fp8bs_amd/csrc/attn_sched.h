@@ -208,18 +208,31 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
   }
   if (!a.by_item && tid == 0) a.rec[c.w * 4] = 0;
   int in_head;
-  if (a.slots <= 64) {   // a lane a slot, every wave for itself
-    Place p{0, -1, 0, 0, 0};
-    if (lane < a.slots) p = place_of<false>(a, lane, R);
-    const int units = tile_at(a, p, R).units, upto = wave_scan(units);
-    const int per_head = __builtin_amdgcn_readlane(upto, 63);
+  if (a.slots <= 256) {   // up to four slots a lane, every wave for itself
+    const int each = (a.slots + 63) >> 6;
+    int units[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = lane * each + i;
+      units[i] = 0;
+      if (i < each && s < a.slots) units[i] = tile_at(a, place_of<false>(a, s, R), R).units;
+      mine += units[i];
+    }
+    const int upto = wave_scan(mine), per_head = __builtin_amdgcn_readlane(upto, 63);
     if (!share_line(a, per_head, c, in_head)) return false;
-    c.slot = __popcll(__ballot(upto <= in_head));   // slots that end before: empty ones are passed over
-    const Place s{__builtin_amdgcn_readlane(p.b, c.slot), __builtin_amdgcn_readlane(p.rt, c.slot),
-                  __builtin_amdgcn_readlane(p.off, c.slot), __builtin_amdgcn_readlane(p.n, c.slot),
-                  __builtin_amdgcn_readlane(p.len, c.slot)};
-    c.t = tile_at(a, s, R);
-    c.first = c.cur - in_head + __builtin_amdgcn_readlane(upto, c.slot) - c.t.units;
+    const int owner = __popcll(__ballot(upto <= in_head));   // lanes whose slots all end before it
+    int left = in_head - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner)), k = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int u = __builtin_amdgcn_readlane(units[i], owner);
+      if (k == i && left >= u) {   // also past empty slots
+        left -= u;
+        ++k;
+      }
+    }
+    c.slot = owner * each + k;
+    c.first = c.cur - left;
+    c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
     return true;
   }
   // prefix sums of every slot in LDS
@@ -273,17 +286,19 @@ __device__ __forceinline__ void take_piece(Cursor& c) {
 // it ends in the middle of and of the one it begins in the middle of.
 __device__ __forceinline__ int64_t piece_of(const Cursor& c) { return 2 * static_cast<int64_t>(c.w) + (c.ub == 0 ? 1 : 0); }
 
-// Records an item that others finish and goes on to the next one.
-__device__ __forceinline__ void end_piece(const AttnArgs& a, int R, Cursor& c) {
-  if (a.workers == 0) return;
-  if (c.ub == 0 && (a.by_item || !c.whole) && threadIdx.x == 0) {
+// Records how many pieces the item has, where this worker begins it.
+__device__ __forceinline__ void record_piece(const AttnArgs& a, const Cursor& c) {
+  if (a.workers != 0 && c.ub == 0 && (a.by_item || !c.whole) && threadIdx.x == 0) {
     int32_t* rec = a.rec + 4 * (a.by_item ? c.h * a.slots + c.slot : c.w);
-    rec[0] = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;   // pieces
+    rec[0] = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;
     rec[1] = c.slot;
     rec[2] = c.h;
     rec[3] = c.w;
   }
-  if (c.cur >= c.stop) return;
+}
+
+// Goes on to the next item with rows; only where the stretch holds one.
+__device__ __forceinline__ void next_item(const AttnArgs& a, int R, Cursor& c) {
   c.first += c.t.units;
   do {
     if (++c.slot == a.slots) {

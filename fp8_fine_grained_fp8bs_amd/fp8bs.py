@@ -182,10 +182,24 @@ def _groups(K):
     return K // 128
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """Handle of the current device's current stream (without the stream
+    object, whose making costs as much as a launch)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: get(torch.cuda.current_device())) if get is not None else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if type(stream) is int:
         return stream
     return stream.cuda_stream
@@ -684,7 +698,8 @@ def rope_table(n_pos, rot, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, t
 
 def rope(x, pos, cs, rot_offset=0, layout="half", inverse=False, stream=None):
     """x bf16 [T][H][D] rotated (inverse: the gradient)."""
-    y = x.new_empty(x.shape)
+    import torch
+    y = torch.empty_like(x)
     fp8bs_rope(x, y, pos, rot_offset, layout, inverse, cs, stream)
     return y
 
@@ -701,7 +716,8 @@ def kv_append(k, v, kc, ks, vc, vs, table, kv_len, q_off, max_q, q=None, cs=None
               stream=None):
     """Appends k, v [T][Hkv][D] to the cache (keys rotated when cs is given);
     returns the rotated queries when q is given."""
-    q_out = None if q is None else q.new_empty(q.shape)
+    import torch
+    q_out = None if q is None else torch.empty_like(q)
     fp8bs_kv_append(q, q_out, k, v, cs, rot_offset, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream)
     return q_out
 
@@ -719,8 +735,9 @@ def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None
                with_lse=False, ws=None, stream=None):
     """Attention of q bf16 [T][Hq][D] over the cache; scale None: D^-1/2.
     The working memory is allocated unless given."""
+    import torch
     T, Hq, D = q.shape
-    out = q.new_empty(q.shape)
+    out = torch.empty_like(q)
     lse = ks.new_empty((T, Hq)) if with_lse else None
     if ws is None:
         B, max_pages = table.shape

@@ -98,9 +98,11 @@ fp8bs_status check_packing(const int32_t* q_off, int64_t B, int64_t T, int64_t m
   return FP8BS_OK;
 }
 
-fp8bs_status check_heads(int64_t Hq, int64_t Hkv) {
+// Rows of a key/value head (tokens times query heads) are numbered in 32 bits.
+fp8bs_status check_heads(int64_t Hq, int64_t Hkv, int64_t T) {
   if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return FP8BS_ERR_INVALID_ARG;
   if (Hq > kMaxHeads || Hq / Hkv > 1024) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (T > kMaxInt32 / (Hq / Hkv)) return FP8BS_ERR_UNSUPPORTED_SHAPE;
   return FP8BS_OK;
 }
 
@@ -504,7 +506,7 @@ fp8bs_status fp8bs_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ld
 
 int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_pages, int64_t page) {
-  if (check_heads(Hq, Hkv) != FP8BS_OK || check_packing(nullptr, B, B, max_q) != FP8BS_OK || T < 0 ||
+  if (check_heads(Hq, Hkv, T) != FP8BS_OK || check_packing(nullptr, B, B, max_q) != FP8BS_OK || T < 0 ||
       T > kMaxInt32 || check_cache_shape(D, page, max_pages, 1) != FP8BS_OK)
     return -1;
   if (T == 0 || B == 0) return 0;
@@ -518,7 +520,7 @@ fp8bs_status fp8bs_attn_paged(const void* q, int64_t ldq, void* out, int64_t ldo
                               int64_t max_pages, int64_t page, const uint8_t* kc, const float* ks,
                               const uint8_t* vc, const float* vs, int64_t n_pages, float scale, int causal,
                               int64_t window, void* ws, int64_t ws_bytes, void* stream) {
-  FP8BS_TRY(check_heads(Hq, Hkv));
+  FP8BS_TRY(check_heads(Hq, Hkv, T));
   if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0) return FP8BS_ERR_INVALID_ARG;
   FP8BS_TRY(check_packing(q_off, B, T, max_q));
   FP8BS_TRY(check_cache_shape(D, page, max_pages, n_pages));

@@ -318,19 +318,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
   __shared__ float part[PG][ROWS][16][VW + 2];
   poison_lds<sizeof(part)>(part);
   const int tid = static_cast<int>(threadIdx.x);
-  const int32_t* rec = a.rec + static_cast<int64_t>(blockIdx.x) * 4;
-  Tile t;
-  int h;
+  const int4* rec = reinterpret_cast<const int4*>(a.rec + static_cast<int64_t>(blockIdx.x) * 8);
+  const int4 who = rec[0], what = rec[1];
   if (a.by_item) {   // a slot without rows has no record
-    h = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.slots));
-    t = tile_at(a, place_of<true>(a, static_cast<int>(blockIdx.x) - h * a.slots, R), R);
-    if (t.units == 0 || rec[0] == 0) return;
-  } else {
-    if (rec[0] == 0) return;
-    h = uniform(rec[2]);
-    t = tile_at(a, place_of<true>(a, uniform(rec[1]), R), R);
+    const int slot = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.slots));
+    if (tile_at(a, place_of<true>(a, slot, R), R).units == 0) return;
   }
-  const int pieces = uniform(rec[0]), w = uniform(rec[3]);
+  const int pieces = uniform(who.x), w = uniform(who.y), h = uniform(who.z);
+  if (pieces == 0) return;
+  Tile t;
+  t.off = uniform(what.x);
+  t.row0 = uniform(what.y);
+  t.rows = uniform(what.z);
   const int c16 = tid & 15, lr = (tid >> 4) % ROWS, grp = (tid >> 4) / ROWS;
   const int r = static_cast<int>(blockIdx.y) * ROWS + lr, d0 = c16 * VW;
   if (static_cast<int>(blockIdx.y) * ROWS >= t.rows) return;
@@ -395,28 +394,32 @@ constexpr int64_t kBrief = 9;
 
 Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
   Plan p;
-  const int64_t G = Hq / Hkv, rows = max_q * G;
+  const int64_t G = Hq / Hkv, rows = (max_q < T ? max_q : T) * G;
   p.R = rows <= 16 ? 16 : rows <= 64 ? 32 : kManyRows;
   const int64_t most = (rows + p.R - 1) / p.R;
   const int64_t direct = most > kMaxInt / B ? kMaxInt : B * most, searched = T * G / p.R + B;
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  // resident workgroups: two a compute unit, of the lightest kernel four
-  const int full = p.R == 16 && D == 64 ? 1024 : 512;
+  // Resident workgroups: two a compute unit; with heads of 64 four of few rows, three
+  // of many rows where a page holds whole tiles.
+  const int full = D != 64 ? 512 : p.R == 16 ? 1024 : p.R == kManyRows && page >= kUnit ? 768 : 512;
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t items = p.slots * Hkv;
   // Whole items where sharing them is not worth its joins: contexts of a few
   // units (a wave has two to four steps), or prompts with items enough to fill
-  // the GPU several times over; and where the line cannot hold them.
-  const bool brief = units <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 4 * full;
+  // the GPU twice over (7 packed prompts of 9 to 2999 tokens: 81 us against 142
+  // shared; two pieces of 512 tokens, 256 items: 838 against 572); and where
+  // the line cannot hold them.
+  const bool brief = units <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 2 * full;
   p.workers = 0;
   p.bytes = 0;
-  p.by_item = items <= full;
+  p.by_item = false;
   if (p.slots <= kMaxSlots && !brief && !many && items <= kMaxInt / units) {
     const int64_t useful = items * ((units + p.min_units - 1) / p.min_units);
     p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
-    p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 4 * full) * 4;
+    p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 8 * static_cast<int64_t>(p.workers)) * 4;
+    p.by_item = items * 8 <= p.workers;   // few items in many pieces
   }
   return p;
 }
@@ -454,9 +457,10 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
 #undef FP8BS_ROWS
   const hipError_t e = plan.R == kManyRows ? launch_attn_prompt(a, static_cast<unsigned>(blocks), st) : hipGetLastError();
   if (e != hipSuccess || plan.workers == 0) return e;
-  const int64_t items = plan.slots * p.Hkv, joins = plan.by_item ? items : plan.workers;
-  // pieces an item on average decide how a workgroup's threads are split
-  const bool deep = items * 8 <= plan.workers;
+  // Records are numbered, and joins shared out, by item where a few items lie in
+  // many pieces each, else by the worker that began the item.
+  const int64_t joins = plan.by_item ? plan.slots * p.Hkv : plan.workers;
+  const bool deep = plan.by_item;
   const dim3 jgrid(static_cast<unsigned>(joins), static_cast<unsigned>(deep ? plan.R : plan.R / 16));
 #define FP8BS_JOIN(D_, PG_) hipLaunchKernelGGL((attn_join_kernel<D_, PG_>), jgrid, block, 0, st, a, plan.R)
   if (p.D == 64 && deep) FP8BS_JOIN(64, 16);

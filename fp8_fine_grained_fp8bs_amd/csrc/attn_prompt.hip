@@ -26,7 +26,6 @@ namespace fp8bs {
 namespace {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr int kAhead = 4;   // LDS reads in flight before their products
 
 // Instructions stay on their side of this: matrix and other work is laid out
 // in the order in which it is written.
@@ -50,8 +49,9 @@ constexpr int kInfo = 256;
 // GROUP: keys that surely share a page, hence a pair of scales: 64 where a page holds as
 // many, else 16.
 template <int D, int GROUP>
-__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prompt_kernel(AttnArgs a) {
   constexpr int KT = kUnit;               // keys of a tile
+  constexpr int kAhead = D == 64 && GROUP == 64 ? 2 : 4;   // LDS reads in flight before their products
   constexpr int NS = D / 16, NX = KT / 32;   // MFMA steps over the inner dim, 32-key tiles
   constexpr int ND = D / 32, NY = KT / 16;   // 32-dim tiles of the output, 16-key steps
   constexpr int NG = KT / GROUP;          // scale groups of a tile
@@ -336,11 +336,13 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
 
     // lane pair (l, l + 32) holds row n32: dims 32 u + 8 k + 4 h2 + 0..3
     lr += __shfl_xor(lr, 32);
-    if (there) {
+    int mine = wrow + n32;
+    asm volatile("" : "+v"(mine));   // its token and head are found again, not kept through the loop
+    if (mine < t.rows) {
       if (c.whole) {
         const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
-        const int64_t token = row_token(a, t, row);
-        const int head = row_head(a, t, h, row);
+        const int64_t token = row_token(a, t, mine);
+        const int head = row_head(a, t, h, mine);
         uint16_t* at = a.p.out + token * a.p.ldo + static_cast<int64_t>(head) * D + 4 * h2;
 #pragma unroll
         for (int u = 0; u < ND; ++u)
@@ -358,11 +360,11 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(AttnArgs a) {
         for (int u = 0; u < ND; ++u)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<float4*>(at + row * D + 32 * u + 8 * k + 4 * h2) =
+            *reinterpret_cast<float4*>(at + mine * D + 32 * u + 8 * k + 4 * h2) =
                 make_float4(o[u][4 * k], o[u][4 * k + 1], o[u][4 * k + 2], o[u][4 * k + 3]);
         if (h2 == 0) {
-          at[kManyRows * D + 2 * row] = mr;
-          at[kManyRows * D + 2 * row + 1] = lr;
+          at[kManyRows * D + 2 * mine] = mr;
+          at[kManyRows * D + 2 * mine + 1] = lr;
         }
       }
     }

@@ -15,7 +15,7 @@
 #pragma once
 
 #include "fp8bs_internal.h"
-#include "fp8bs_device.h"
+#include "packed_search.h"
 
 namespace fp8bs {
 
@@ -35,7 +35,7 @@ struct AttnArgs {
   int min_units;      // least stretch of a worker
   bool by_item;       // records are numbered by item, else by worker
   float* part;        // partials: [2 workers][R][D + 2]
-  int32_t* rec;       // records: [items or workers][4]
+  int32_t* rec;       // records: [items or workers][8]
 };
 
 // The many-rows kernel on `blocks` workgroups (a multiple of 8).
@@ -75,17 +75,22 @@ __device__ __forceinline__ Place place_of(const AttnArgs& a, int slot, int R) {
   } else {
     // tiles of b <= floor(n_b G / R) + 1: numbered from floor(q_off[b] G / R) + b
     auto key = [&](int i) {
-      const int64_t o = a.p.q_off == nullptr ? i : same(a.p.q_off[i]);
+      const int64_t o = a.p.q_off == nullptr ? i : a.p.q_off[i];
       return o * a.G / R + i;
     };
-    int lo = 0, hi = a.p.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (key(mid) <= slot) lo = mid;
-      else hi = mid - 1;
+    int lo = 0;
+    if (SAME) {
+      lo = uniform(search64(a.p.B, slot, key));
+    } else {
+      int hi = a.p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (key(mid) <= slot) lo = mid;
+        else hi = mid - 1;
+      }
     }
     p.b = lo;
-    p.rt = static_cast<int>(slot - key(lo));
+    p.rt = same(static_cast<int>(slot - key(lo)));
   }
   int o = p.b, e = p.b + 1, len = a.p.kv_len[p.b];
   if (a.p.q_off != nullptr) {
@@ -206,33 +211,40 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
     c.stop = c.t.units;
     return c.t.units != 0;
   }
-  if (!a.by_item && tid == 0) a.rec[c.w * 4] = 0;
+  if (!a.by_item && tid == 0) a.rec[c.w * 8] = 0;
   int in_head;
   if (a.slots <= 256) {   // up to four slots a lane, every wave for itself
     const int each = (a.slots + 63) >> 6;
+    Place p[4];
     int units[4], mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int s = lane * each + i;
-      units[i] = 0;
-      if (i < each && s < a.slots) units[i] = tile_at(a, place_of<false>(a, s, R), R).units;
+      p[i] = Place{0, -1, 0, 0, 0};
+      if (i < each && s < a.slots) p[i] = place_of<false>(a, s, R);
+      units[i] = tile_at(a, p[i], R).units;
       mine += units[i];
     }
     const int upto = wave_scan(mine), per_head = __builtin_amdgcn_readlane(upto, 63);
     if (!share_line(a, per_head, c, in_head)) return false;
     const int owner = __popcll(__ballot(upto <= in_head));   // lanes whose slots all end before it
     int left = in_head - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner)), k = 0;
+    Place s = p[0];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const int u = __builtin_amdgcn_readlane(units[i], owner);
       if (k == i && left >= u) {   // also past empty slots
         left -= u;
         ++k;
+        s = p[i + 1];
       }
     }
+    s = Place{__builtin_amdgcn_readlane(s.b, owner), __builtin_amdgcn_readlane(s.rt, owner),
+              __builtin_amdgcn_readlane(s.off, owner), __builtin_amdgcn_readlane(s.n, owner),
+              __builtin_amdgcn_readlane(s.len, owner)};
     c.slot = owner * each + k;
     c.first = c.cur - left;
-    c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
+    c.t = tile_at(a, s, R);
     return true;
   }
   // prefix sums of every slot in LDS
@@ -289,11 +301,10 @@ __device__ __forceinline__ int64_t piece_of(const Cursor& c) { return 2 * static
 // Records how many pieces the item has, where this worker begins it.
 __device__ __forceinline__ void record_piece(const AttnArgs& a, const Cursor& c) {
   if (a.workers != 0 && c.ub == 0 && (a.by_item || !c.whole) && threadIdx.x == 0) {
-    int32_t* rec = a.rec + 4 * (a.by_item ? c.h * a.slots + c.slot : c.w);
-    rec[0] = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;
-    rec[1] = c.slot;
-    rec[2] = c.h;
-    rec[3] = c.w;
+    int4* rec = reinterpret_cast<int4*>(a.rec + 8 * (a.by_item ? c.h * a.slots + c.slot : c.w));
+    const int pieces = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;
+    rec[0] = make_int4(pieces, c.w, c.h, 0);
+    rec[1] = make_int4(c.t.off, c.t.row0, c.t.rows, 0);
   }
 }
 

@@ -96,22 +96,18 @@ __device__ __forceinline__ void load_key(const AppendArgs& a, const uint16_t* ro
   const RopeShape& r = a.rope;
   const int o = d - r.off;
   if (a.cs == nullptr || o < 0 || o >= r.rot) return;
+  CosSin k;
   if (r.interleaved) {   // the vector's four pairs are its own
-    const float* row_cs = angles(a, p) + (o >> 1);
-    const float4 cc = *reinterpret_cast<const float4*>(row_cs), ss = *reinterpret_cast<const float4*>(row_cs + (r.rot >> 1));
-    const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x1 = f[2 * i], x2 = f[2 * i + 1];
-      f[2 * i] = x1 * c4[i] - x2 * s4[i];
-      f[2 * i + 1] = x2 * c4[i] + x1 * s4[i];
-    }
+    load_angles4(k, 0, angles(a, p), r.rot, o >> 3);
+    rotate_pairs(f, k, 0);
   } else {
     const int half = r.rot >> 1;
     const bool second = o >= half;
     float g[8];
     unpack8(*reinterpret_cast<const uint4*>(row + (second ? d - half : d + half)), g);
-    const CosSin k = load_cossin(angles(a, p), r.rot, (second ? o - half : o) >> 3);
+    const int j = (second ? o - half : o) >> 2;
+    load_angles4(k, 0, angles(a, p), r.rot, j);
+    load_angles4(k, 1, angles(a, p), r.rot, j + 1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = second ? f[i] * k.c[i] + g[i] * k.s[i] : f[i] * k.c[i] - g[i] * k.s[i];
   }
@@ -150,7 +146,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs a) {
     int n;
     rows_of(a.q_off, a.T, b, off, n);
     const int64_t p = static_cast<int64_t>(a.kv_len[b]) - n + (t - off);
-    rotate_row<D / 16>(a.q + t * a.ldq, a.qo + t * a.ldqo, a.Hq, D, a.rope, 1.0f, angles(a, p));
+    rotate_row<D / 16>(a.q + t * a.ldq, a.qo + t * a.ldqo, a.Hq, D, a.rope, 1.0f, angles(a, p), false);
     return;
   }
   const int h = static_cast<int>(bid % a.Hkv);
@@ -246,7 +242,7 @@ hipError_t launch_kv_append(const KvAppend& p, hipStream_t st) {
   a.table = p.table; a.ldt = p.ldt; a.max_pages = p.max_pages;
   a.pshift = __builtin_ctz(static_cast<unsigned>(p.page));
   a.kc = p.kc; a.ks = p.ks; a.vc = p.vc; a.vs = p.vs; a.n_pages = p.n_pages;
-  const int64_t most = (p.max_q + p.page - 2) / p.page + 1;
+  const int64_t max_q = p.max_q < p.T ? p.max_q : p.T, most = (max_q + p.page - 2) / p.page + 1;
   const int64_t direct = most * p.B, searched = p.T / p.page + 2 * static_cast<int64_t>(p.B);
   a.most = direct <= searched ? static_cast<int>(most) : 0;
   a.slots = direct <= searched ? direct : searched;
@@ -255,7 +251,7 @@ hipError_t launch_kv_append(const KvAppend& p, hipStream_t st) {
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(blocks)), block(256);
   // passes over the tokens that one call can add to a page
-  const int64_t adds = p.max_q < p.page ? p.max_q : p.page;
+  const int64_t adds = max_q < p.page ? max_q : p.page;
   const int need = static_cast<int>((adds * p.D + 2047) / 2048), np = need <= 2 ? need : need <= 4 ? 4 : 8;
 #define FP8BS_APPEND(D_, NP_) \
   if (p.D == D_ && np == NP_) hipLaunchKernelGGL((kv_append_kernel<D_, NP_>), grid, block, 0, st, a)

@@ -440,7 +440,7 @@ fp8bs_status fp8bs_kv_append(const void *q, int64_t ldq, void *q_out, int64_t ld
  * BF16.  Results do not depend on the order in which the GPU runs: equal
  * calls give equal bits.  Value scales below 2^-100 are taken as 2^-100.
  * T >= 0 and B >= 0 (either 0 is a no-op), Hkv > 0, Hq % Hkv == 0,
- * Hq / Hkv <= 1024, window >= 0.
+ * Hq / Hkv <= 1024, T * Hq / Hkv < 2^31, window >= 0.  out must not overlap q.
  */
 fp8bs_status fp8bs_attn_paged(const void *q, int64_t ldq, void *out, int64_t ldo, float *lse, int64_t ldl,
                               const int32_t *q_off, const int32_t *kv_len, int64_t B, int64_t T, int64_t max_q,

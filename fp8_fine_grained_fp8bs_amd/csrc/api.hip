@@ -74,6 +74,7 @@ fp8bs_status check_scales(const float* p, int64_t cols, int64_t ld) {
 constexpr int64_t kMaxHeads = int64_t(1) << 16;
 constexpr int64_t kMaxHeadDim = 512;
 constexpr int64_t kMaxInt32 = 0x7fffffff;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;   // of a sequence: positions a little past its end still fit 32 bits
 
 fp8bs_status check_rotation(int64_t rot, int64_t off, fp8bs_rope_layout layout, int64_t D) {
   if (layout != FP8BS_ROPE_HALF && layout != FP8BS_ROPE_INTERLEAVED) return FP8BS_ERR_INVALID_ARG;
@@ -110,8 +111,7 @@ fp8bs_status check_cache_shape(int64_t D, int64_t page, int64_t max_pages, int64
   if (D <= 0 || page <= 0 || max_pages <= 0 || n_pages <= 0) return FP8BS_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return FP8BS_ERR_UNSUPPORTED_SHAPE;
   if (page != 16 && page != 32 && page != 64 && page != 128) return FP8BS_ERR_UNSUPPORTED_SHAPE;
-  // positions are 32-bit, page numbers too
-  if (max_pages > kMaxInt32 / page || n_pages > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (max_pages > kMaxTokens / page || n_pages > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
   return FP8BS_OK;
 }
 

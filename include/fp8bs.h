@@ -347,7 +347,7 @@ fp8bs_status fp8bs_grouped_gemm(const uint8_t *a, const float *sa, int64_t ldsa,
  * DEVICE memory and not checked: lengths are cut to what table holds
  * (max_pages * page), page numbers outside 0 .. n_pages-1 are never followed, so wrong
  * contents give unspecified results but no access out of bounds.
- * page is 16, 32, 64 or 128; D is 64 or 128.
+ * page is 16, 32, 64 or 128; D is 64 or 128; max_pages * page <= 2^30.
  * ---------------------------------------------------------------------- */
 
 typedef enum {

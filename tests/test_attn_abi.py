@@ -64,11 +64,13 @@ def attn(q=A, ldq=512, out=A, ldo=512, lse=A, ldl=4, q_off=A, kv_len=A, B=3, T=4
     (lambda: attn(Hq=0), INV), (lambda: attn(Hq=5), INV), (lambda: attn(Hkv=-1), INV),
     (lambda: attn(Hq=2050, Hkv=2, ldq=1 << 19, ldo=1 << 19, ldl=4096), SHAPE), (lambda: attn(scale=0.0), INV),
     (lambda: attn(scale=NAN), INV), (lambda: attn(scale=float("inf")), INV), (lambda: attn(window=-1), INV),
-    (lambda: attn(D=32), SHAPE), (lambda: attn(page=24), SHAPE), (lambda: attn(T=1 << 32), SHAPE), (lambda: attn(max_q=-1), INV),
+    (lambda: attn(T=1 << 30, B=1 << 30, Hq=8, Hkv=2, ldq=1024, ldo=1024, ldl=8), SHAPE),
+    (lambda: attn(max_pages=1 << 27, ldt=1 << 27), SHAPE), (lambda: attn(D=32), SHAPE), (lambda: attn(page=24), SHAPE), (lambda: attn(T=1 << 32), SHAPE), (lambda: attn(max_q=-1), INV),
     (lambda: attn(max_q=0), INV), (lambda: attn(q_off=NULL), INV), (lambda: attn(q=NULL), INV), (lambda: attn(out=NULL), INV),
     (lambda: attn(ldq=256), INV), (lambda: attn(ldo=516), ALIGN), (lambda: attn(q=A + 2), ALIGN), (lambda: attn(ldl=3), INV),
     (lambda: attn(lse=A + 2), ALIGN), (lambda: attn(kc=NULL), INV), (lambda: attn(vc=A + 4), ALIGN),
-    (lambda: attn(q_off=A + 2), ALIGN), (lambda: attn(ldt=2), INV), (lambda: attn(ws=NULL), INV), (lambda: attn(ws_bytes=16), INV),
+    (lambda: attn(q_off=A + 2), ALIGN), (lambda: attn(ldt=2), INV), (lambda: attn(ws=NULL, max_pages=500, ldt=500), INV),
+    (lambda: attn(ws_bytes=16, max_pages=500, ldt=500), INV),
     (lambda: attn(ws=A + 8), ALIGN), (lambda: attn(T=0, B=0, q=NULL, ws=NULL, ws_bytes=0), OK),
 ])
 def test_refusals(call, expect):
@@ -80,7 +82,8 @@ def test_working_memory_sizes():
     assert f(0, 0, 1, 8, 2, 128, 10, 64) == 0
     assert f(4, 4, 1, 8, 3, 128, 10, 64) == -1 and f(4, 4, 1, 8, 2, 100, 10, 64) == -1 and f(-1, 4, 1, 8, 2, 128, 10, 64) == -1
     assert 0 < f(1, 1, 1, 8, 2, 128, 2048, 64) < 1 << 28
-    assert f(5000, 5000, 1, 8, 2, 128, 10, 64) == 0          # one workgroup an item
+    assert f(5000, 5000, 1, 8, 2, 128, 1000, 64) == 0        # one workgroup an item
+    assert f(4, 4, 1, 8, 2, 128, 5, 16) == 0                 # contexts too short to share
 
 
 def tensors(T=4, Hq=4, Hkv=2, D=64, B=2, pages=5, page=16):

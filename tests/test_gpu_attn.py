@@ -162,6 +162,71 @@ def test_many_sequences():
     check(make(15, lens, [1] * 2100, 2, 1, 64, 16), no_off=True)
 
 
+@pytest.mark.parametrize("B", [65, 100, 256, 300, 700])
+def test_ragged_batches_share_their_work(B):
+    """Batches that fill one, two or four slots a lane, and those past them,
+    with sequences without rows in between."""
+    rng = np.random.default_rng(B)
+    lens = np.exp(rng.uniform(0, 7, B)).astype(int)
+    lens[B // 2] = 3000
+    new = (rng.random(B) < 0.9).astype(int)
+    new[0] = 1
+    check(make(B, lens.tolist(), new.tolist(), 4, 2, 64, 16), name="ragged")
+    check(make(B + 1, lens.tolist(), (2 * new).tolist(), 16, 1, 128, 32), name="ragged two rows")
+
+
+def test_many_prompts_whole_items():
+    """Tiles enough to fill the GPU: one workgroup an item."""
+    check(make(19, [260] * 8, [260] * 8, 64, 8, 64, 16))
+    check(make(20, [190, 1, 333, 260, 70, 300, 250, 320], [190, 1, 333, 260, 70, 300, 250, 320], 96, 12, 128, 64), window=77)
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 128), (128, 64), (128, 16)])
+def test_long_prompt_pieces(d, page):
+    """Contexts long enough for the many-rows kernel to go round its ring of
+    page numbers and scales several times; sampled heads against binary64 on the
+    GPU, with the tolerance above."""
+    hkv, G, q, n = 64, 2, 128, 18000 if page >= 64 else 6000
+    hq, B = hkv * G, 8
+    g = torch.Generator(device=dev())
+    g.manual_seed(d + page)
+    lens = [n - 17 * b for b in range(B)]
+    per = [(x + page - 1) // page for x in lens]
+    pages = sum(per)
+    kc = torch.randint(0, 127, (pages, hkv, page, d), generator=g, device=dev(), dtype=torch.uint8)
+    vc = torch.randint(0, 127, (pages, hkv, page, d), generator=g, device=dev(), dtype=torch.uint8)
+    vc ^= (torch.rand(vc.shape[:3], generator=g, device=dev()) < 0.5)[..., None].to(torch.uint8) * 128
+    ks, vs = (torch.rand((2, pages, hkv), generator=g, device=dev()) + 0.5) * 2.0 ** -9
+    ks, vs = ks.contiguous(), vs.contiguous()
+    order = torch.randperm(pages, generator=g, device=dev()).int()
+    tab = torch.full((B, max(per)), -1, dtype=torch.int32, device=dev())
+    at = 0
+    for b in range(B):
+        tab[b, :per[b]] = order[at:at + per[b]]
+        at += per[b]
+    qq = torch.randn((B * q, hq, d), generator=g, device=dev()).bfloat16()
+    off = torch.arange(0, B * q + 1, q, dtype=torch.int32, device=dev())
+    kv = torch.tensor(lens, dtype=torch.int32, device=dev())
+    announce(f"attn long pieces d {d} page {page}: {B} x {q} rows over {n}, {hq}/{hkv} heads")
+    out = fp8bs.attn_paged(qq, kc, ks, vc, vs, tab, kv, off, q)
+    scale = d ** -0.5
+    for b, h in ((0, 0), (3, 77), (7, hq - 1)):
+        ids = tab[b, :per[b]].long()
+        deco = lambda c, s: (c[ids, h // G].view(torch.float8_e4m3fn).double()  # noqa: E731
+                             * s[ids, h // G].double()[:, None, None]).reshape(-1, d)[:lens[b]]
+        k, v = deco(kc, ks), deco(vc, vs)
+        x = qq[b * q:(b + 1) * q, h].double()
+        sc = x @ k.t().contiguous() * scale
+        hide = torch.arange(lens[b], device=dev()) > (lens[b] - q + torch.arange(q, device=dev()))[:, None]
+        p = torch.softmax(sc.masked_fill(hide, float("-inf")), -1)
+        want, mag = p @ v, p @ v.abs()
+        sabs = (x.abs() @ k.abs().t().contiguous()).max() * scale
+        E = (d + 16) * 2.0 ** -24 * sabs + 2.0 ** -20
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * E) * mag + n * 2.0 ** -33 * 448 * vs.max()
+        got = out[b * q:(b + 1) * q, h].double()
+        assert bool(((got - want).abs() <= tol).all()), (b, h, float((got - want).abs().max()))
+
+
 def test_strides_and_another_stream():
     """Queries and outputs as parts of wider rows, on a stream of their own."""
     c = make(16, [100, 40], [2, 3], 4, 2, 64, 32)

@@ -395,14 +395,15 @@ fp8bs_status fp8bs_rope(const void *x, int64_t ldx, void *y, int64_t ldy, const 
                         int inverse, const float *cs, int64_t n_pos, void *stream);
 
 /*
- * Append to the cache: the call's keys (rotated to their positions in FP32)
- * and values are quantized into their pages; the call's queries can be
- * rotated in the same launch.
+ * Append to the cache: the call's keys (rotated to their positions) and values are
+ * quantized into their pages; the call's queries can be rotated in the same
+ * launch.
  * A block that already held tokens keeps its scale s unless the new tokens
  * need a larger one: s' = max(s, fl32(amax(new) / 448)).  Where s' > s its
- * earlier codes become the nearest-even E4M3 of fl32(dec(code) * s) / s';
+ * earlier codes become the nearest-even E4M3 of dec(code) * s / s';
  * new codes are the nearest-even E4M3 of x / s' ([p1] para 3: the tile's
- * max-abs taken online).  A block whose first token arrives ignores what its
+ * max-abs taken online); a rotated key's x and its max-abs are not rounded
+ * before that.  A block whose first token arrives ignores what its
  * codes and scale held.  Codes past the last token stay as they were.
  *   q    bf16 [T][ldq] or NULL   q_out bf16 [T][ldqo]   Hq heads of D; q_out may be q
  *   k, v bf16 [T][ldk], [T][ldv] Hkv heads of D

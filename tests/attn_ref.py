@@ -23,11 +23,11 @@ def bf16_round(x32):
 
 def encode(x, s):
     """Nearest-even E4M3 codes of the exact quotients x / s (s one scale)."""
-    x = np.asarray(x, np.float32)
+    x = np.asarray(x, np.float64)
     sign = (np.signbit(x).astype(np.uint8) << 7)
     if s == 0:
         return sign
-    a = np.abs(x).astype(np.float64)
+    a = np.abs(x)
     t = MIDS * np.float64(s)                    # exact: 5 bits by 24
     i = np.searchsorted(t, a, side="left")      # thresholds below a
     tie = (i < len(t)) & (a == t[np.minimum(i, len(t) - 1)])
@@ -71,18 +71,18 @@ def rotate(x, cs, rot, off, layout, inverse=False):
 
 def append_block(codes, scale, there, new):
     """One block: codes [page][D] and scale before, `there` tokens in it, new
-    values [m][D] (float32) appended.  Returns (codes, scale)."""
+    values [m][D] (float64) appended.  Returns (codes, scale)."""
     codes = codes.copy()
     old = np.float32(scale) if there > 0 else np.float32(0)
-    s = max(old, np.float32(np.abs(new).max() / np.float32(448.0)))
+    s = max(old, np.float32(np.abs(new).max() / 448.0))
     if there > 0 and s > old:
-        codes[:there] = encode(decode(codes[:there]).astype(np.float32) * old, s)
+        codes[:there] = encode(decode(codes[:there]) * np.float64(old), s)
     codes[there:there + len(new)] = encode(new, s)
     return codes, s
 
 
-def append(k32, v32, kc, ks, vc, vs, tab, kv_len, off):
-    """The whole cache after the call (k32 rotated, float32 [T][H][D])."""
+def append(k, v, kc, ks, vc, vs, tab, kv_len, off):
+    """The whole cache after the call (k rotated, float64 [T][H][D])."""
     kc, ks, vc, vs = kc.copy(), ks.copy(), vc.copy(), vs.copy()
     page, H = kc.shape[2], kc.shape[1]
     for b in range(len(kv_len)):
@@ -92,8 +92,8 @@ def append(k32, v32, kc, ks, vc, vs, tab, kv_len, off):
             i = tab[b, p]
             rows = slice(off[b] + lo - (n - m), off[b] + hi - (n - m))
             for h in range(H):
-                kc[i, h], ks[i, h] = append_block(kc[i, h], ks[i, h], lo - p * page, k32[rows, h])
-                vc[i, h], vs[i, h] = append_block(vc[i, h], vs[i, h], lo - p * page, v32[rows, h])
+                kc[i, h], ks[i, h] = append_block(kc[i, h], ks[i, h], lo - p * page, k[rows, h])
+                vc[i, h], vs[i, h] = append_block(vc[i, h], vs[i, h], lo - p * page, v[rows, h])
     return kc, ks, vc, vs
 
 

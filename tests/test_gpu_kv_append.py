@@ -1,6 +1,6 @@
 """GPU: the append to the paged cache, codes and scales bit for bit against
-NumPy (FP32 rotation with each product and sum rounded, FP32 max-abs and scale,
-nearest-even codes decided by exact comparisons), over pages that fill
+NumPy (rotation and max-abs in binary64, an FP32 scale, nearest-even codes
+decided by exact comparisons), over pages that fill
 across calls, ragged prompts, scales that grow, and everything the call must
 leave alone."""
 import numpy as np
@@ -45,9 +45,9 @@ def expect(c, rot, off, layout):
     f = ref.bf16_values(c["qkv"])
     pos = np.concatenate([np.arange(n - m, n) for n, m in zip(c["lens"], np.diff(c["off"]))]).astype(int)
     hq, hkv = c["hq"], c["hkv"]
-    turned = ref.rotate(f[:, :hq + hkv], c["cs"][pos], rot, off, layout) if rot else f[:, :hq + hkv]
-    return ref.bf16_round(turned[:, :hq]), ref.append(turned[:, hq:], f[:, hq + hkv:], c["kc"], c["ks"], c["vc"], c["vs"],
-                                                      c["tab"], c["lens"], c["off"])
+    turn = lambda x: ref.rotate(x, c["cs"][pos].astype(x.dtype), rot, off, layout) if rot else x  # noqa: E731
+    k, v = f[:, hq:].astype(np.float64)[:, :hkv], f[:, hq:].astype(np.float64)[:, hkv:]
+    return ref.bf16_round(turn(f[:, :hq])), ref.append(turn(k), v, c["kc"], c["ks"], c["vc"], c["vs"], c["tab"], c["lens"], c["off"])
 
 
 def check(c, off=0, layout="half", rotate=True, queries=True, no_off=False, max_q=None):

@@ -59,8 +59,7 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
   const int page_mask = (1 << a.pshift) - 1;
 
   Cursor c;
-  if (!begin_work(a, R, false, obuf, sums, c)) return;
-  take_piece(c);
+  if (!begin_work(a, R, false, obuf, sums, c) || !take_piece(c)) return;
   const Tile& t = c.t;
   const int& h = c.h;
   // The piece at hand: its queries (B operands, row m16 of each 16-row group),
@@ -255,7 +254,7 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
     // The next piece's lookups go out before this one's waves are joined.
     const Tile dt = c.t;
     const int dh = c.h;
-    const bool whole = c.whole, more = c.cur < c.stop;
+    const bool whole = c.whole, more = goes_on(c);
     const int64_t piece = piece_of(c);
     record_piece(a, c);
     if (more) {
@@ -405,6 +404,7 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
   // of many rows where a page holds whole tiles.
   const int full = D != 64 ? 512 : p.R == 16 ? 1024 : p.R == kManyRows && page >= kUnit ? 768 : 512;
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
+  const int64_t line = units + kOpen;
   const int64_t items = p.slots * Hkv;
   // Whole items where sharing them is not worth its joins: contexts of a few
   // units (a wave has two to four steps), or prompts with items enough to fill
@@ -415,8 +415,8 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
   p.workers = 0;
   p.bytes = 0;
   p.by_item = false;
-  if (p.slots <= kMaxSlots && !brief && !many && items <= kMaxInt / units) {
-    const int64_t useful = items * ((units + p.min_units - 1) / p.min_units);
+  if (p.slots <= kMaxSlots && !brief && !many && items <= kMaxInt / line) {
+    const int64_t useful = items * ((line + p.min_units - 1) / p.min_units);
     p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
     p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 8 * static_cast<int64_t>(p.workers)) * 4;
     p.by_item = items * 8 <= p.workers;   // few items in many pieces

@@ -70,9 +70,8 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
   const int page_mask = (1 << a.pshift) - 1;
 
   Cursor c;
-  if (!begin_work(a, kManyRows, true, kbuf, sums, c)) return;
-  while (c.cur < c.stop) {
-    take_piece(c);
+  if (!begin_work(a, kManyRows, true, kbuf, sums, c) || !take_piece(c)) return;
+  while (true) {
     const Tile& t = c.t;
     const int h = c.h;
 
@@ -375,7 +374,9 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
       }
     }
     record_piece(a, c);
-    if (c.cur < c.stop) next_item(a, kManyRows, c);
+    if (!goes_on(c)) break;
+    next_item(a, kManyRows, c);
+    take_piece(c);
   }
 }
 

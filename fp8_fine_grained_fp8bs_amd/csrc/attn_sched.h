@@ -7,7 +7,10 @@
 // on the device only, and differ by orders of magnitude inside a batch, so
 // the items' units are laid end to end (heads outermost: neighbouring workers
 // read the same head's cache) and every worker, a workgroup, takes an equal
-// stretch of that line.  A stretch that starts or ends inside an item leaves
+// stretch of that line.  An item takes kOpen units of the line more than it has:
+// lookups, queries and the first keys' way from memory cost a worker 2 to 6 us, as
+// much as some units (a stretch that ends in them has nothing of the item).
+// A stretch that starts or ends inside an item leaves
 // a partial result (sums, maximum and denominator in FP32) in the workspace;
 // a second kernel joins an item's partials in their order, so results do not
 // depend on timing.  Every worker computes the line for itself: one load a
@@ -22,6 +25,10 @@ namespace fp8bs {
 constexpr int kUnit = 64;          // keys of a unit
 constexpr int kManyRows = 128;     // rows of a tile of the many-rows kernel
 constexpr int kMaxSlots = 2048;    // tiles a head that the line can hold
+// Opening an item, in units.  With 0, 2, 4, 6 and 8: 96 requests of one token
+// 141 133 133 135 137 us, heads of 64 34.1 31.0 29.7 30.3 32.0, drafted tokens
+// 46.9 46.2 42.7 42.1 42.5.
+constexpr int kOpen = 4;
 
 struct AttnArgs {
   AttnPaged p;
@@ -134,6 +141,9 @@ __device__ __forceinline__ Tile tile_at(const AttnArgs& a, const Place& p, int R
   return t;
 }
 
+// What a tile takes of the line.
+__device__ __forceinline__ int line_units(const Tile& t) { return t.units == 0 ? 0 : t.units + kOpen; }
+
 // Keys that one row sees.
 __device__ __forceinline__ void row_keys(const AttnArgs& a, const Tile& t, int row, int& lo, int& hi) {
   const int64_t p = static_cast<int64_t>(t.len) - t.n + static_cast<unsigned>(row) / static_cast<unsigned>(a.G);
@@ -208,7 +218,7 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
     if (c.h >= a.p.Hkv) return false;
     c.t = tile_at(a, place_of<true>(a, c.slot, R), R);
     c.cur = c.first = 0;
-    c.stop = c.t.units;
+    c.stop = line_units(c.t);
     return c.t.units != 0;
   }
   if (!a.by_item && tid == 0) a.rec[c.w * 8] = 0;
@@ -222,7 +232,7 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
       const int s = lane * each + i;
       p[i] = Place{0, -1, 0, 0, 0};
       if (i < each && s < a.slots) p[i] = place_of<false>(a, s, R);
-      units[i] = tile_at(a, p[i], R).units;
+      units[i] = line_units(tile_at(a, p[i], R));
       mine += units[i];
     }
     const int upto = wave_scan(mine), per_head = __builtin_amdgcn_readlane(upto, 63);
@@ -255,7 +265,7 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
     const int s = tid * each + i;
     if (s < a.slots) {
       prefix[s] = mine;
-      mine += tile_at(a, place_of<false>(a, s, R), R).units;
+      mine += line_units(tile_at(a, place_of<false>(a, s, R), R));
     }
   }
   const int upto = wave_scan(mine);
@@ -286,13 +296,18 @@ __device__ __forceinline__ bool begin_work(const AttnArgs& a, int R, bool backwa
   return true;
 }
 
-__device__ __forceinline__ void take_piece(Cursor& c) {
-  c.ub = c.cur - c.first;
-  const int end = c.stop - c.first;
-  c.ue = end < c.t.units ? end : c.t.units;
-  c.cur = c.first + c.ue;
-  c.whole = c.ub == 0 && c.ue == c.t.units;
+// The part of the stretch that lies in the item at hand; false where it holds none
+// of the item's units.
+__device__ __forceinline__ bool take_piece(Cursor& c) {
+  const int from = c.cur - c.first - kOpen, all = c.t.units, to = c.stop - c.first - kOpen;
+  c.ub = from > 0 ? from : 0;
+  c.ue = to < all ? to : all;
+  c.cur = c.first + kOpen + c.ue;
+  c.whole = c.ub == 0 && c.ue == all;
+  return c.ue > c.ub;
 }
+// Whether the stretch goes on into units of another item.
+__device__ __forceinline__ bool goes_on(const Cursor& c) { return c.stop - c.cur > kOpen; }
 
 // Where the piece's partial belongs: a worker leaves two at most, of the item
 // it ends in the middle of and of the one it begins in the middle of.
@@ -302,7 +317,7 @@ __device__ __forceinline__ int64_t piece_of(const Cursor& c) { return 2 * static
 __device__ __forceinline__ void record_piece(const AttnArgs& a, const Cursor& c) {
   if (a.workers != 0 && c.ub == 0 && (a.by_item || !c.whole) && threadIdx.x == 0) {
     int4* rec = reinterpret_cast<int4*>(a.rec + 8 * (a.by_item ? c.h * a.slots + c.slot : c.w));
-    const int pieces = c.whole ? 0 : worker_of(c, c.first + c.t.units - 1) - c.w + 1;
+    const int pieces = c.whole ? 0 : worker_of(c, c.first + kOpen + c.t.units - 1) - c.w + 1;
     rec[0] = make_int4(pieces, c.w, c.h, 0);
     rec[1] = make_int4(c.t.off, c.t.row0, c.t.rows, 0);
   }
@@ -310,7 +325,7 @@ __device__ __forceinline__ void record_piece(const AttnArgs& a, const Cursor& c)
 
 // Goes on to the next item with rows; only where the stretch holds one.
 __device__ __forceinline__ void next_item(const AttnArgs& a, int R, Cursor& c) {
-  c.first += c.t.units;
+  c.first += line_units(c.t);
   do {
     if (++c.slot == a.slots) {
       c.slot = 0;

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
   int rlo[NR], rhi[NR];
   int all_lo, all_hi, base, steps;
   const int32_t* table;
-  Pages pg;
+  Pages pg, pg4;
   const int last_page = static_cast<int>(a.p.max_pages) - 1;
   auto load_pages = [&](int s) {
     Pages p;
@@ -84,7 +84,10 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
     base = (t.u0 + c.ub) * kUnit;
     steps = (c.ue - c.ub) * (kUnit / 32);
     if (base + 32 * steps > t.hi) steps = t.hi > base ? (t.hi - base + 31) / 32 : 0;
-    if (wv < steps) pg = load_pages(wv);
+    if (wv < steps) {
+      pg = load_pages(wv);
+      pg4 = load_pages(wv + 4);
+    }
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
       const int row = 16 * r + m16;
@@ -94,11 +97,8 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
       if (!there) rhi[r] = 0;
       const uint16_t* q = a.p.q + row_token(a, t, rr) * a.p.ldq + static_cast<int64_t>(row_head(a, t, h, rr)) * D;
 #pragma unroll
-      for (int e = 0; e < 2 * NW; ++e) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 64 * (e >> 1) + 16 * g + 8 * (e & 1));
-        qf[r][e] = __builtin_bit_cast(bf16x8, there ? x : zero);
-      }
+      for (int e = 0; e < 2 * NW; ++e)   // a row beyond the last computes row 0 and is not stored
+        qf[r][e] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(q + 64 * (e >> 1) + 16 * g + 8 * (e & 1)));
     }
     // keys that every row sees need no mask
     int x;
@@ -227,28 +227,36 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
       }
     };
 
-    // the wave's steps: wv, wv + 4, ...
+    // The wave's steps: wv, wv + 4, ...  Loads wait for what was issued before them,
+    // so page numbers go out a step ahead of the keys that need them, and no load
+    // depends on a branch inside the loop: a wait after one would be for both.  The
+    // step computed next is not begun before they are out.
     if (wv < steps) {
-      Step<D> x = load_step(wv, pg);
-      if (wv + 4 < steps) pg = load_pages(wv + 4);
       int s = wv;
-      while (true) {
-        Step<D> y;
-        if (s + 4 < steps) {
-          y = load_step(s + 4, pg);
-          if (s + 8 < steps) pg = load_pages(s + 8);
-        }
+      auto ahead = [&](int s) {
+        __builtin_amdgcn_sched_barrier(0);
+        const Pages then = load_pages(s + 4);
+        const Step<D> x = load_step(s, pg);
+        pg = then;
+        __builtin_amdgcn_sched_barrier(0);
+        return x;
+      };
+      Step<D> x = load_step(s, pg);
+      pg = pg4;
+      while (s + 8 < steps) {
+        Step<D> y = ahead(s + 4);
+        compute(s, x);
+        x = ahead(s + 8);
+        compute(s + 4, y);
+        s += 8;
+      }
+      if (s + 4 < steps) {
+        Step<D> y = ahead(s + 4);
         compute(s, x);
         s += 4;
-        if (s >= steps) break;
-        if (s + 4 < steps) {
-          x = load_step(s + 4, pg);
-          if (s + 8 < steps) pg = load_pages(s + 8);
-        }
-        compute(s, y);
-        s += 4;
-        if (s >= steps) break;
+        x = y;
       }
+      compute(s, x);
     }
 
     // The next piece's lookups go out before this one's waves are joined.

@@ -103,11 +103,8 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
       const int rr = there ? row : 0;
       const uint16_t* q = a.p.q + row_token(a, t, rr) * a.p.ldq + static_cast<int64_t>(row_head(a, t, h, rr)) * D + 8 * h2;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-        const u32x4 x = *reinterpret_cast<const u32x4*>(q + 16 * s);
-        qf[s] = __builtin_bit_cast(bf16x8, there ? x : zero);
-      }
+      for (int s = 0; s < NS; ++s)   // a row beyond the last computes row 0 and is not stored
+        qf[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(q + 16 * s));
     }
     f32x16 o[ND];
 #pragma unroll

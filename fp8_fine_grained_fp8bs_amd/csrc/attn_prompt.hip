@@ -46,12 +46,11 @@ struct __attribute__((aligned(16))) Group {
 };
 constexpr int kInfo = 256;
 
-// GROUP: keys that surely share a page, hence a pair of scales: 64 where a page holds as
-// many, else 16.
+// GROUP: keys that surely share a page, hence a pair of scales: a page's, 64 at most.
 template <int D, int GROUP>
-__global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prompt_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prompt_kernel(AttnArgs a) {
   constexpr int KT = kUnit;               // keys of a tile
-  constexpr int kAhead = D == 64 && GROUP == 64 ? 2 : 4;   // LDS reads in flight before their products
+  constexpr int kAhead = D == 64 && GROUP >= 32 ? 2 : 4;   // LDS reads in flight before their products
   constexpr int NS = D / 16, NX = KT / 32;   // MFMA steps over the inner dim, 32-key tiles
   constexpr int ND = D / 32, NY = KT / 16;   // 32-dim tiles of the output, 16-key steps
   constexpr int NG = KT / GROUP;          // scale groups of a tile
@@ -235,13 +234,12 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
     };
     auto softmax = [&](int i) {
       const int t0 = base + KT * i;
-      float kq[NG], lv[NG], iv[NG];
+      float kq[NG], lv[NG];
 #pragma unroll
       for (int y = 0; y < NG; ++y) {
         const Group g = info[(NG * i + y) % kInfo];
         kq[y] = g.kq;
         lv[y] = g.lv;
-        iv[y] = g.iv;
       }
       if (i < b1 || i >= b2) {
         const int from = rlo - t0 - 4 * h2, to = rhi - t0 - 4 * h2;
@@ -301,7 +299,7 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
         weigh();
       }
 #pragma unroll
-      for (int y = 0; y < NG; ++y) lr = __builtin_fmaf(sum[y], iv[y], lr);
+      for (int y = 0; y < NG; ++y) lr = __builtin_fmaf(sum[y], info[(NG * i + y) % kInfo].iv, lr);
     };
 
     if (tiles > 0) {
@@ -381,11 +379,14 @@ __global__ __launch_bounds__(256, D == 64 && GROUP == 64 ? 3 : 2) void attn_prom
 
 hipError_t launch_attn_prompt(const AttnArgs& a, unsigned blocks, hipStream_t st) {
   const dim3 grid(blocks), block(256);
-  const bool wide = a.p.page >= 64;
-  if (a.p.D == 64 && wide) hipLaunchKernelGGL((attn_prompt_kernel<64, 64>), grid, block, 0, st, a);
-  else if (a.p.D == 64) hipLaunchKernelGGL((attn_prompt_kernel<64, 16>), grid, block, 0, st, a);
-  else if (wide) hipLaunchKernelGGL((attn_prompt_kernel<128, 64>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((attn_prompt_kernel<128, 16>), grid, block, 0, st, a);
+#define FP8BS_PROMPT(D_, G_) hipLaunchKernelGGL((attn_prompt_kernel<D_, G_>), grid, block, 0, st, a)
+  if (a.p.D == 64 && a.p.page >= 64) FP8BS_PROMPT(64, 64);
+  else if (a.p.D == 64 && a.p.page == 32) FP8BS_PROMPT(64, 32);
+  else if (a.p.D == 64) FP8BS_PROMPT(64, 16);
+  else if (a.p.page >= 64) FP8BS_PROMPT(128, 64);
+  else if (a.p.page == 32) FP8BS_PROMPT(128, 32);
+  else FP8BS_PROMPT(128, 16);
+#undef FP8BS_PROMPT
   return hipGetLastError();
 }
 

@@ -397,30 +397,35 @@ struct Plan {
 };
 
 constexpr int64_t kMaxInt = 0x7fffffff;
-constexpr int64_t kBrief = 9;
+constexpr int64_t kBrief = 25;   // units of a context that is not worth sharing
 
-Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
+// window: keys that a row sees at most, 0 where that is not known.
+Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page, int64_t window) {
   Plan p;
   const int64_t G = Hq / Hkv, rows = (max_q < T ? max_q : T) * G;
+  // 24 requests of 500 to 8000 tokens, heads of 128: 32 rows take 40 us in tiles of 32,
+  // 53 in tiles of 16; 64 rows 61 in tiles of 32, 63 in the many-rows kernel; 96 rows
+  // 87 in tiles of 32, 66 in the many-rows kernel.
   p.R = rows <= 16 ? 16 : rows <= 64 ? 32 : kManyRows;
   const int64_t most = (rows + p.R - 1) / p.R;
   const int64_t direct = most > kMaxInt / B ? kMaxInt : B * most, searched = T * G / p.R + B;
   p.most = direct <= searched ? static_cast<int>(most) : 0;
   p.slots = direct <= searched ? direct : searched;
   p.min_units = 4;
-  // Resident workgroups: two a compute unit; with heads of 64 four of few rows, three
-  // of many rows where scales are shared by 32 keys or more (7 packed prompts on pages
-  // of 32: 73 us against 79 with two).
-  const int full = D != 64 ? 512 : p.R == 16 ? 1024 : p.R == kManyRows && page >= 32 ? 768 : 512;
+  // Workers: two a compute unit; with heads of 64 three of many rows where scales are
+  // shared by 32 keys or more (7 packed prompts on pages of 32: 73 us against 79 with
+  // two).  Four of few rows gave 30.4 us against 28.9 (48 requests of 99 to 4001 tokens).
+  const int full = D == 64 && p.R == kManyRows && page >= 32 ? 768 : 512;
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t line = units + kOpen;
   const int64_t items = p.slots * Hkv;
-  // Whole items where sharing them is not worth its joins: contexts of a few
-  // units (a wave has two to four steps), or prompts with items enough to fill
-  // the GPU twice over (7 packed prompts of 9 to 2999 tokens: 81 us against 142
-  // shared; two pieces of 512 tokens, 256 items: 838 against 572); and where
-  // the line cannot hold them.
-  const bool brief = units <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 2 * full;
+  // Whole items where sharing them is not worth its joins: short contexts (4 requests
+  // of 1000 tokens 12.0 us against 16.3 shared, 64 of 100 to 1500 20.4 against 24.3;
+  // 4 of 2000 18.9 against 15.9), or prompts with items enough to fill the GPU twice
+  // over (7 packed prompts of 9 to 2999 tokens: 81 us against 142 shared; two pieces
+  // of 512 tokens, 256 items: 838 against 572); and where the line cannot hold them.
+  const int64_t seen = window > 0 ? (window + p.R / G) / kUnit + 2 : units;
+  const bool brief = (units < seen ? units : seen) <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 2 * full;
   p.workers = 0;
   p.bytes = 0;
   p.by_item = false;
@@ -428,7 +433,8 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
     const int64_t useful = items * ((line + p.min_units - 1) / p.min_units);
     p.workers = static_cast<int>(useful < full ? (useful + 7) / 8 * 8 : full);
     p.bytes = (2 * static_cast<int64_t>(p.workers) * p.R * (D + 2) + 8 * static_cast<int64_t>(p.workers)) * 4;
-    p.by_item = items * 8 <= p.workers;   // few items in many pieces
+    // few items in many pieces (one request of 20000 tokens: 16.6 us against 25.4)
+    p.by_item = items * 8 <= p.workers;
   }
   return p;
 }
@@ -436,11 +442,11 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
 }  // namespace
 
 int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page) {
-  return plan_of(B, T, max_q, Hq, Hkv, D, max_pages, page).bytes;
+  return plan_of(B, T, max_q, Hq, Hkv, D, max_pages, page, 0).bytes;
 }
 
 hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st) {
-  const Plan plan = plan_of(p.B, p.T, p.max_q, p.Hq, p.Hkv, p.D, p.max_pages, p.page);
+  const Plan plan = plan_of(p.B, p.T, p.max_q, p.Hq, p.Hkv, p.D, p.max_pages, p.page, p.causal ? p.window : 0);
   AttnArgs a;
   a.p = p;
   a.G = p.Hq / p.Hkv;

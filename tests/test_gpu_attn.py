@@ -125,6 +125,15 @@ def test_long_axis_is_split():
     check(make(11, [7000, 300], [3, 40], 8, 1, 128, 64))
 
 
+@pytest.mark.parametrize("window", [1, 100, 1400, 1600, 5000])
+def test_windows_over_long_contexts(window):
+    """Windows that are short and long contexts that are not, a token and several at a
+    time; without causality a window bounds the keys from below only."""
+    check(make(window, [7000, 2, 1500, 4001], [1, 1, 1, 1], 8, 2, 128, 32), window=window, no_off=True)
+    check(make(window + 1, [6000, 33, 2500], [3, 5, 0], 10, 2, 64, 16), window=window)
+    check(make(window + 2, [3000, 700], [2, 4], 4, 1, 128, 64), window=window, causal=False)
+
+
 def test_scales_of_very_different_size():
     c = make(12, [900, 400], [1, 2], 8, 2, 128, 16, spread=4.0)
     c["vs"][::3] *= np.float32(2.0 ** 20)

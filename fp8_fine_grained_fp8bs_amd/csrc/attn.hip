@@ -397,7 +397,8 @@ struct Plan {
 };
 
 constexpr int64_t kMaxInt = 0x7fffffff;
-constexpr int64_t kBrief = 25;   // units of a context that is not worth sharing
+// Units of a context that is not worth sharing, of few rows and of many.
+constexpr int64_t kBrief = 25, kManyBrief = 17;
 
 // window: keys that a row sees at most, 0 where that is not known.
 Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page, int64_t window) {
@@ -419,13 +420,18 @@ Plan plan_of(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_
   const int64_t units = (max_pages * page + kUnit - 1) / kUnit + 1;   // of an item, at most
   const int64_t line = units + kOpen;
   const int64_t items = p.slots * Hkv;
-  // Whole items where sharing them is not worth its joins: short contexts (4 requests
-  // of 1000 tokens 12.0 us against 16.3 shared, 64 of 100 to 1500 20.4 against 24.3;
-  // 4 of 2000 18.9 against 15.9), or prompts with items enough to fill the GPU twice
-  // over (7 packed prompts of 9 to 2999 tokens: 81 us against 142 shared; two pieces
-  // of 512 tokens, 256 items: 838 against 572); and where the line cannot hold them.
+  // Whole items where sharing them is not worth its joins, and where the line cannot
+  // hold them.  Short contexts or windows: 4 requests of 1000 tokens 12.0 us against
+  // 16.3 shared, 64 of 100 to 1500 20.4 against 24.3 (4 of 2000 18.9 against 15.9); a
+  // prompt of 500 21.3 against 27.3 (2 pieces of 64 over 1500 45.5 against 30.5).
+  // Prompts that fill the GPU once, whose tiles' work is graded and dealt from
+  // the longest on: two of 2100 tokens 104 us against 129, one of 8192 621 against 660.
+  // Pieces of longer contexts are as unequal as those: 80 pieces of 64 over 100 to 9000
+  // tokens (1280 items) take 315 us against 269, 160 of them 507 against 511.
   const int64_t seen = window > 0 ? (window + p.R / G) / kUnit + 2 : units;
-  const bool brief = (units < seen ? units : seen) <= kBrief && p.R != kManyRows, many = p.R == kManyRows && items >= 2 * full;
+  const bool brief = (units < seen ? units : seen) <= (p.R == kManyRows ? kManyBrief : kBrief);
+  const bool prompts = 2 * max_q >= max_pages * page;
+  const bool many = p.R == kManyRows && items >= (prompts ? 1 : 4) * full;
   p.workers = 0;
   p.bytes = 0;
   p.by_item = false;

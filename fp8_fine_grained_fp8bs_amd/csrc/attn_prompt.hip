@@ -11,6 +11,17 @@
 // one barrier.  Two workgroups live on a compute unit and share no barrier,
 // so one's softmax runs under the other's products.
 //
+// Measured, heads of 128, 32 query heads on 8: a prompt of 8192 tokens 587 us, 937
+// TFLOP/s (a large library product of BF16 matrices reaches 1230); two pieces of 512
+// tokens 546 us with the join, 914.  Products, LDS reads and barriers alone took 367 us
+// of the pieces (in the form with two groups, below): the rest is vector work that does
+// not fit under the products, 7.5 VALU instructions a matrix instruction of 32
+// cycles, 2 of them exponentials at a quarter rate.  With heads of 64 it is 19: 7
+// packed prompts 73 us, 460 TFLOP/s.  Also built, in us for prompt / pieces: 128 rows with decoding before the
+// products 618 / 602; 256 rows on eight waves in two alternating groups 583 / 519, but
+// 189 against 143 on packed prompts; one wave a SIMD with 64 rows 756 / 638; codes kept
+// in LDS and decoded by each wave 643 / 568.
+//
 // Mathematics and number formats are those of the few-rows kernel: S^T = K Q^T
 // (32x32x16 BF16 MFMAs), p' = 2^(s k c + log2 v - m) with the value scale v
 // inside, O^T += V^T P'^T in FP16 on bare codes, denominator p' / v.  In the

@@ -7,7 +7,10 @@
 // bytes a value (BF16 in and out) for 3 operations: HBM-bound.  The angles
 // come from a table made once (they need binary64: at position 10^5 a
 // binary32 angle is already off by 2^-8); a row of it serves all heads of a
-// token, so the rows' reads stay in the caches.
+// token, so the rows' reads stay in the caches.  Measured: the gradient of 16383
+// tokens, 40 heads of 128 of which 64 dims turn, 340 MB: 51 us in the kernel, 6.7
+// TB/s, 57 a call (65 with plain loads, 61 with non-temporal stores too); 3 tokens
+// 2.5 us, a launch.
 #include <hip/hip_runtime.h>
 
 #include "fp8bs_internal.h"

@@ -49,7 +49,17 @@ ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_a
 _lib = None
 _lib_path = LIB_PATH
 _functions = {}      # the loaded library's entry points by name
-_dtype_names = {}
+
+
+class _Names(dict):
+    """Names of dtypes (str() of one costs more than a call's other checks)."""
+
+    def __missing__(self, dtype):
+        name = self[dtype] = str(dtype).replace("torch.", "")
+        return name
+
+
+_dtype_names = _Names()
 
 
 def use_library(path: str) -> str:
@@ -125,13 +135,11 @@ def _ptr(t):
     """Device pointer of a GPU tensor (or an int address, or None for NULL).
     A host tensor is refused here: its address would reach the kernels as a
     device pointer."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda:
-        raise ValueError("libfp8bs takes device tensors; got a tensor on " + str(t.device))
-    return t.data_ptr()
+    if t.is_cuda:
+        return t.data_ptr()
+    raise ValueError("libfp8bs takes device tensors; got a tensor on " + str(t.device))
 
 
 def _ld(t):
@@ -145,21 +153,13 @@ def _ld(t):
 _CODES = ("uint8", "float8_e4m3fn")
 
 
-def _dtype(t):
-    """Name of a tensor's dtype (str() of a dtype costs more than a call's other checks)."""
-    name = _dtype_names.get(t.dtype)
-    if name is None:
-        name = _dtype_names[t.dtype] = str(t.dtype).replace("torch.", "")
-    return name
-
-
 def _check(t, what, shape, dtypes, contiguous=False):
     """Refuse a tensor whose shape or dtype does not fit what the kernels
     will read or write (a short output would be written past its end).
     shape entries: an int (exact), (">=", n) (at least n) or None (any)."""
     if t is None:
         raise ValueError(f"{what}: missing tensor")
-    if _dtype(t) not in dtypes:
+    if _dtype_names[t.dtype] not in dtypes:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != len(shape):
         raise ValueError(f"{what}: {t.dim()}-D tensor, expected {len(shape)}-D")
@@ -376,7 +376,7 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
 def _heads(t, what):
     """Row stride (elements) of a [T][H][D] view whose heads are contiguous in a row, and its shape."""
     shape = t.shape
-    if len(shape) != 3 or _dtype(t) != "bfloat16":
+    if len(shape) != 3 or _dtype_names[t.dtype] != "bfloat16":
         raise ValueError(f"{what}: expected a 3-D bfloat16 tensor [T][H][D], got {len(shape)}-D {t.dtype}")
     T, H, D = shape
     row, head, one = t.stride()
@@ -394,13 +394,13 @@ def _layout(layout):
 
 
 def _int32s(t, what, n):
-    if t.shape != (n,) or _dtype(t) != "int32" or not t.is_contiguous():
+    if t.shape != (n,) or _dtype_names[t.dtype] != "int32" or not t.is_contiguous():
         raise ValueError(f"{what}: expected {n} contiguous int32, got {t.dtype} {tuple(t.shape)}")
 
 
 def _check_angles(cs):
     """(n_pos, rot) of a table of angles."""
-    if _dtype(cs) != "float32" or cs.dim() != 2 or not cs.is_contiguous():
+    if _dtype_names[cs.dtype] != "float32" or cs.dim() != 2 or not cs.is_contiguous():
         raise ValueError(f"cs: expected a contiguous float32 table [n_pos][rot], got {cs.dtype} {tuple(cs.shape)}")
     return cs.shape
 
@@ -408,19 +408,19 @@ def _check_angles(cs):
 def _check_cache(kc, ks, vc, vs, table, kv_len, q_off, T):
     """Shapes of a paged cache and its packing; returns
     (B, Hkv, D, page, n_pages, ldt, max_pages)."""
-    shape, name = kc.shape, _dtype(kc)
+    shape, name = kc.shape, _dtype_names[kc.dtype]
     if len(shape) != 4 or name not in _CODES or not kc.is_contiguous():
         raise ValueError(f"kc: expected contiguous codes [n_pages][Hkv][page][D], got {kc.dtype} {tuple(shape)}")
-    if vc.shape != shape or _dtype(vc) != name or not vc.is_contiguous():
+    if vc.shape != shape or _dtype_names[vc.dtype] != name or not vc.is_contiguous():
         raise ValueError("vc: must have kc's shape and dtype, contiguous")
     n_pages, Hkv, page, D = shape
     blocks = (n_pages, Hkv)
-    if ks.shape != blocks or _dtype(ks) != "float32" or not ks.is_contiguous():
+    if ks.shape != blocks or _dtype_names[ks.dtype] != "float32" or not ks.is_contiguous():
         raise ValueError(f"ks: expected contiguous float32 {blocks}, got {ks.dtype} {tuple(ks.shape)}")
-    if vs.shape != blocks or _dtype(vs) != "float32" or not vs.is_contiguous():
+    if vs.shape != blocks or _dtype_names[vs.dtype] != "float32" or not vs.is_contiguous():
         raise ValueError(f"vs: expected contiguous float32 {blocks}, got {vs.dtype} {tuple(vs.shape)}")
     listed = table.shape
-    if len(listed) != 2 or _dtype(table) != "int32":
+    if len(listed) != 2 or _dtype_names[table.dtype] != "int32":
         raise ValueError(f"table: expected int32 [B][max_pages], got {table.dtype} {tuple(listed)}")
     B, max_pages = listed
     ldt, one = table.stride()

@@ -20,11 +20,14 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
+# the Python binding's short way into the attention operators (host code)
+MARSHAL = os.path.join(PKG, "_marshal.so")
 # debug build for race checks: kernels fill their LDS with 0xFF before use
 POISON_LIB = os.path.join(PKG, "libfp8bs_poison.so")
 SOURCES = ["api.hip", "quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "e5m6.hip", "swiglu.hip",
            "rope.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]
-LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]   # the sources whose kernels use LDS
+# the sources whose kernels use LDS
+LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]
 ARCH = "gfx950"
 
 
@@ -65,18 +68,39 @@ def _link(objs, out):
     os.replace(tmp, out)
 
 
+def _build_marshal():
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for d in include:
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL + ".tmp", "-L" + cpp_extension.TORCH_LIB_PATH,
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for marshal.cpp:\n" + r.stderr)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source and link libfp8bs.so next to this file, and
-    the LDS-poisoning debug build libfp8bs_poison.so (tests only)."""
+    """Compile every HIP source and link libfp8bs.so next to this file, the
+    LDS-poisoning debug build libfp8bs_poison.so (tests only), and the Python
+    binding's _marshal.so."""
     jobs = [(src, False) for src in SOURCES] + [(src, True) for src in LDS_SOURCES]
-    with ThreadPoolExecutor(max_workers=len(jobs)) as ex:
+    with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda j: _compile(*j), jobs))
+        marshal.result()
     plain = dict(zip(SOURCES, objs[:len(SOURCES)]))
     poisoned = dict(zip(LDS_SOURCES, objs[len(SOURCES):]))
     _link([plain[s] for s in SOURCES], LIB)
     _link([poisoned.get(s, plain[s]) for s in SOURCES], POISON_LIB)
     if verbose:
-        print("built", LIB, "and", POISON_LIB)
+        print("built", LIB + ",", POISON_LIB, "and", MARSHAL)
     return LIB
 
 

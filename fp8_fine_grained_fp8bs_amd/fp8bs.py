@@ -49,6 +49,8 @@ ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_a
 _lib = None
 _lib_path = LIB_PATH
 _functions = {}      # the loaded library's entry points by name
+_addresses = {}      # and their addresses
+_marshal = None      # the compiled short way into the attention operators
 
 
 class _Names(dict):
@@ -70,6 +72,7 @@ def use_library(path: str) -> str:
     prev = _lib_path
     _lib_path, _lib = path, None
     _functions.clear()
+    _addresses.clear()
     _ws_bytes.cache_clear()
     return prev
 
@@ -371,6 +374,37 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
     _check(d, "d", (M_total, N), ("float32",) if int(dt) == OUT_F32 else ("bfloat16",), contiguous=True)
     _call("fp8bs_grouped_gemm", _ptr(a), _ptr(sa), _ld(sa), _ptr(b), _ptr(sb), _ptr(offsets),
           int(E), M_total, _ptr(d), int(dt), N, K, _stream(stream))
+
+
+def _short(name, *args):
+    """The named attention operator by the compiled short way (csrc/marshal.cpp): its
+    result, or None where an argument is not as it should be (the checks below then
+    say which)."""
+    global _marshal
+    if _marshal is None:
+        import torch  # noqa: F401  (its libraries are the module's)
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing: build it with "
+                               "`python -m fp8_fine_grained_fp8bs_amd.build`") from e
+        _marshal = {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
+    result = _marshal[name](_address(name), *args)
+    if type(result) is int:
+        raise Fp8bsError(result, name)
+    return result
+
+
+def _address(name):
+    address = _addresses.get(name)
+    if address is None:
+        address = _addresses[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+    return address
+
+
+def _stream_later(stream):
+    """A stream's handle, or for the current one the function that gives it."""
+    return _current_stream if stream is None else _stream(stream)
 
 
 def _heads(t, what):
@@ -698,6 +732,9 @@ def rope_table(n_pos, rot, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, t
 
 def rope(x, pos, cs, rot_offset=0, layout="half", inverse=False, stream=None):
     """x bf16 [T][H][D] rotated (inverse: the gradient)."""
+    y = _short("fp8bs_rope", x, pos, cs, rot_offset, _layout(layout), bool(inverse), _stream_later(stream))
+    if y is not None:
+        return y
     import torch
     y = torch.empty_like(x)
     fp8bs_rope(x, y, pos, rot_offset, layout, inverse, cs, stream)
@@ -716,6 +753,11 @@ def kv_append(k, v, kc, ks, vc, vs, table, kv_len, q_off, max_q, q=None, cs=None
               stream=None):
     """Appends k, v [T][Hkv][D] to the cache (keys rotated when cs is given);
     returns the rotated queries when q is given."""
+    if q is not None and cs is not None:
+        q_out = _short("fp8bs_kv_append", kc, ks, vc, vs, table, kv_len, q_off, k, v, q, cs, rot_offset, _layout(layout),
+                       max_q, _stream_later(stream))
+        if q_out is not None:
+            return q_out
     import torch
     q_out = None if q is None else torch.empty_like(q)
     fp8bs_kv_append(q, q_out, k, v, cs, rot_offset, layout, q_off, kv_len, max_q, table, kc, ks, vc, vs, stream)
@@ -735,6 +777,11 @@ def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None
                with_lse=False, ws=None, stream=None):
     """Attention of q bf16 [T][Hq][D] over the cache; scale None: D^-1/2.
     The working memory is allocated unless given."""
+    if ws is None and stream is None and not with_lse:
+        out = _short("fp8bs_attn_paged", kc, ks, vc, vs, table, kv_len, q_off, _address("fp8bs_attn_paged_ws"), q, max_q,
+                     scale, bool(causal), window, _current_stream)
+        if out is not None:
+            return out
     import torch
     T, Hq, D = q.shape
     out = torch.empty_like(q)

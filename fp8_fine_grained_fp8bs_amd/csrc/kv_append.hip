@@ -180,25 +180,38 @@ __device__ __forceinline__ void turn_key(const AppendArgs& a, const KeyLoad& v, 
   }
 }
 
-// Encodes the `there` tokens a block already holds for its larger scale.
+// Encodes the `there` tokens a block already holds for its larger scale, four
+// vectors a thread on their way at a time (64 requests whose blocks all grow: 9.8 us
+// with the events around them, 10.3 one after the other).
 template <int D>
 __device__ __forceinline__ void rescale_old(uint8_t* codes, int there, float s_old, const TileScale& ts) {
+  constexpr int STEP = 2048 / D;
   const int sub = (static_cast<int>(threadIdx.x) % (D / 8)) * 8;
-  for (int r = static_cast<int>(threadIdx.x) / (D / 8); r < there; r += 2048 / D) {
-    uint2* at = reinterpret_cast<uint2*>(codes + r * D + sub);
-    const uint2 c = *at;
-    float f[8];
-    auto value = [&](int j) { return e4m3_dec(((j < 4 ? c.x : c.y) >> (8 * (j & 3))) & 0xffu); };
+  for (int r0 = static_cast<int>(threadIdx.x) / (D / 8); r0 < there; r0 += 4 * STEP) {
+    uint2 c[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = value(j) * s_old;
-    bool open = false;
-    uint32_t w[2] = {encode_or_open(f, ts, open), encode_or_open(f + 4, ts, open)};
-    if (__builtin_expect(open, 0)) {
-      w[0] = w[1] = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j >> 2] |= code_of(static_cast<double>(value(j)) * s_old, ts.s) << (8 * (j & 3));
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * STEP;
+      c[u] = *reinterpret_cast<const uint2*>(codes + (r < there ? r : r0) * D + sub);
     }
-    *at = make_uint2(w[0], w[1]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = r0 + u * STEP;
+      if (r < there) {
+        float f[8];
+        auto value = [&](int j) { return e4m3_dec(((j < 4 ? c[u].x : c[u].y) >> (8 * (j & 3))) & 0xffu); };
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = value(j) * s_old;
+        bool open = false;
+        uint32_t w[2] = {encode_or_open(f, ts, open), encode_or_open(f + 4, ts, open)};
+        if (__builtin_expect(open, 0)) {
+          w[0] = w[1] = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j >> 2] |= code_of(static_cast<double>(value(j)) * s_old, ts.s) << (8 * (j & 3));
+        }
+        *reinterpret_cast<uint2*>(codes + r * D + sub) = make_uint2(w[0], w[1]);
+      }
+    }
   }
 }
 

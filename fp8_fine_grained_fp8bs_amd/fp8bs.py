@@ -379,17 +379,19 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
 def _short(name, *args):
     """The named attention operator by the compiled short way (csrc/marshal.cpp): its
     result, or None where an argument is not as it should be (the checks below then
-    say which)."""
+    say which) or the short way has not been built (the library is then called
+    through ctypes)."""
     global _marshal
     if _marshal is None:
-        import torch  # noqa: F401  (its libraries are the module's)
-        try:
+        _marshal = {}
+        if os.path.exists(os.path.join(PKG, "_marshal.so")):
+            import torch  # noqa: F401  (its libraries are the module's)
             from . import _marshal as module
-        except ImportError as e:
-            raise RuntimeError("_marshal.so is missing: build it with "
-                               "`python -m fp8_fine_grained_fp8bs_amd.build`") from e
-        _marshal = {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
-    result = _marshal[name](_address(name), *args)
+            _marshal = {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
+    way = _marshal.get(name)
+    if way is None:
+        return None
+    result = way(_address(name), *args)
     if type(result) is int:
         raise Fp8bsError(result, name)
     return result

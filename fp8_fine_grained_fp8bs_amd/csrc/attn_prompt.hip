@@ -20,7 +20,8 @@
 // packed prompts 73 us, 460 TFLOP/s.  Also built, in us for prompt / pieces: 128 rows with decoding before the
 // products 618 / 602; 256 rows on eight waves in two alternating groups 583 / 519, but
 // 189 against 143 on packed prompts; one wave a SIMD with 64 rows 756 / 638; codes kept
-// in LDS and decoded by each wave 643 / 568.
+// in LDS and decoded by each wave 643 / 568; half a tile's weights between the
+// products of the other half's scores 620 / 593 (against 581 / 560 in the same run).
 //
 // Mathematics and number formats are those of the few-rows kernel: S^T = K Q^T
 // (32x32x16 BF16 MFMAs), p' = 2^(s k c + log2 v - m) with the value scale v

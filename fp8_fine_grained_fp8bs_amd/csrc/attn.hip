@@ -28,7 +28,10 @@
 // would double the output's rounding error) and the codes too, exactly.
 // m is a reference, not the exact maximum: it is moved (and O, l rescaled)
 // only when a score exceeds it by 2^15; a move sets the largest p' to 2^8, so
-// FP16 neither overflows nor loses weights above 2^-33 of the largest.
+// FP16 neither overflows nor loses weights above 2^-33 of the largest.  Keys whose v is
+// below 2^-32, blocks of zeros above all, reach the denominator as p / 2^m instead, in a
+// second pass over the steps of a piece that has some (kTinyV): p' / v would overflow for a
+// long context of them, and vanish beside values 2^43 and larger.
 //
 // Layouts.  Key rows of the two 16-row MFMA tiles are assigned so that
 // lane group g = lane / 16 gets the scores of keys 8g .. 8g+7: those are the
@@ -158,6 +161,31 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
       x.vs = a.p.vs[bv];
       return x;
     };
+    auto scores = [&](const Step<D>& x, f32x4 (&sc)[NR][2]) {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < 2 * NW; ++c) {
+          const bf16x8 kf = bf16_of_codes(x.k[i][c >> 1][2 * (c & 1)], x.k[i][c >> 1][2 * (c & 1) + 1]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            sc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][c], sc[r][i], 0, 0, 0);
+        }
+    };
+    auto of_row = [](float x) {   // the largest of a row's four lanes
+      x = __builtin_fmaxf(x, __shfl_xor(x, 16));
+      return __builtin_fmaxf(x, __shfl_xor(x, 32));
+    };
+    auto move = [&](int r, float to) {   // the reference
+      const Moved by(mr[r] - to);
+      lr[r] = by.den(lr[r]);
+      mr[r] = to;
+#pragma unroll
+      for (int i = 0; i < 4 * NW; ++i) o[r][i] *= by.factor();
+    };
+    bool tiny = false;   // a step had keys with a tiny value scale
     auto compute = [&](int s, Step<D>& x) {
       const int t0 = base + 32 * s, mine = t0 + 8 * g;
       const bool clear = t0 >= all_lo && t0 + 32 <= all_hi;
@@ -175,19 +203,12 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
 #pragma unroll
             for (int c = 0; c < NW; ++c) x.v[j][c] = 0u;
       }
-      const float lv = __builtin_amdgcn_logf(vs), iv = __builtin_amdgcn_rcpf(vs);
+      const float lv = __builtin_amdgcn_logf(vs);
+      const bool few = vs < kTinyV;   // summed apart
+      const float iv = few ? 0.0f : __builtin_amdgcn_rcpf(vs);
+      tiny |= __ballot(few) != 0;
       f32x4 sc[NR][2];
-#pragma unroll
-      for (int r = 0; r < NR; ++r) sc[r][0] = sc[r][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int c = 0; c < 2 * NW; ++c) {
-          const bf16x8 kf = bf16_of_codes(x.k[i][c >> 1][2 * (c & 1)], x.k[i][c >> 1][2 * (c & 1) + 1]);
-#pragma unroll
-          for (int r = 0; r < NR; ++r)
-            sc[r][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[r][c], sc[r][i], 0, 0, 0);
-        }
+      scores(x, sc);
       f16x8 pf16[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
@@ -203,14 +224,8 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
 #pragma unroll
         for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, e[j]);
         if (__ballot(top > mr[r] + kHeadroom) != 0) {
-          top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-          const float to = top > mr[r] + kHeadroom ? top - kTop : mr[r];
-          const float f = __builtin_amdgcn_exp2f(mr[r] - to);
-          mr[r] = to;
-          lr[r] *= f;
-#pragma unroll
-          for (int i = 0; i < 4 * NW; ++i) o[r][i] *= f;
+          top = of_row(top);
+          move(r, top > mr[r] + kHeadroom ? top - kTop : mr[r]);
         }
         u32x4 pw;
 #pragma unroll
@@ -267,6 +282,35 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
         x = y;
       }
       compute(s, x);
+      // the denominators of keys with a tiny value scale: their scores once more
+      if (__builtin_expect(tiny, 0)) {
+#pragma unroll 1
+        for (s = wv; s < steps; s += 4) {
+          const Step<D> y = load_step(s, load_pages(s));
+          const int mine = base + 32 * s + 8 * g;
+          const bool none = mine >= t.hi || mine + 8 <= t.lo;
+          const bool few = !none && !(y.vs >= kTinyV);
+          const float kq = none ? 0.0f : y.ks * a.scale_log2;
+          f32x4 sc[NR][2];
+          scores(y, sc);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            float e[8];
+            float top = -__builtin_huge_valf();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              e[j] = few && mine + j >= rlo[r] && mine + j < rhi[r] ? sc[r][j >> 2][j & 3] * kq : -__builtin_huge_valf();
+              top = __builtin_fmaxf(top, e[j]);
+            }
+            if (__ballot(top > mr[r] + kDenHeadroom) != 0) {
+              top = of_row(top);
+              move(r, top > mr[r] + kDenHeadroom ? top - kDenTop : mr[r]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) lr[r] += __builtin_amdgcn_exp2f(e[j] - mr[r]);
+          }
+        }
+      }
     }
 
     // The next piece's lookups go out before this one's waves are joined.
@@ -309,8 +353,9 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
       for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float f = __builtin_amdgcn_exp2f(ml[k][row][0] - top);
-        den = __builtin_fmaf(f, ml[k][row][1], den);
+        const Moved by(ml[k][row][0] - top);
+        const float f = by.factor();
+        den += by.den(ml[k][row][1]);
 #pragma unroll
         for (int i = 0; i < VW; ++i) sum[i] = __builtin_fmaf(f, obuf[k][row][d0 + i], sum[i]);
       }
@@ -363,8 +408,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
     const float* piece = a.part + (2 * static_cast<int64_t>(w + k) + (k == 0 ? 1 : 0)) * size;
     const float m = piece[R * D + 2 * rr], l = piece[R * D + 2 * rr + 1];
     const float to = __builtin_fmaxf(top, m);
-    const float f = __builtin_amdgcn_exp2f(top - to), g = __builtin_amdgcn_exp2f(m - to);
-    den = __builtin_fmaf(g, l, den * f);
+    const Moved before(top - to), now(m - to);
+    const float f = before.factor(), g = now.factor();
+    den = before.den(den) + now.den(l);
 #pragma unroll
     for (int i = 0; i < VW / 4; ++i) {
       const float4 x = *reinterpret_cast<const float4*>(piece + rr * D + d0 + 4 * i);
@@ -389,8 +435,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int R) {
     for (int i = 0; i < VW; ++i) sum[i] = 0.0f;
     for (int k = 0; k < PG; ++k) {
       const float* from = part[k][lr][c16];
-      const float f = __builtin_amdgcn_exp2f(from[VW] - top);
-      den = __builtin_fmaf(f, from[VW + 1], den);
+      const Moved by(from[VW] - top);
+      const float f = by.factor();
+      den += by.den(from[VW + 1]);
 #pragma unroll
       for (int i = 0; i < VW; ++i) sum[i] = __builtin_fmaf(f, from[i], sum[i]);
     }

@@ -15,6 +15,14 @@ constexpr float kHeadroom = 15.0f;      // log2 of the largest p' before the ref
 constexpr float kMostWeight = 0x1p15f;  // the same, as a sum of weights
 constexpr float kTop = 8.0f;            // log2 of the largest p' after a move
 constexpr float kMinVScale = 0x1p-100f;
+// Keys of a block with a smaller value scale than this (a block of zeros has none) go
+// into the denominator as p / 2^m, by an exponential of their own: by way of p' / v they
+// would be lost where p' falls below FP32's least (beside scales of 2^34 and more), and
+// leave its range at 2^115 a key.  The reference then also keeps p / 2^m below 2^97, so
+// that the sums of 2^30 keys stay in range.
+constexpr float kTinyV = 0x1p-32f, kTinyLog = -32.0f;
+constexpr float kDenHeadroom = 97.0f, kDenTop = 96.0f;   // log2, as kHeadroom and kTop
+constexpr float kMostDen = 0x1p102f;    // the headroom, as a sum of 32 keys
 constexpr float kMinKScale = 0x1p-120f; // of a key block's factor, so that it keeps a masked score's -infinity
 
 // Eight codes (two dwords) to eight BF16 / FP16 values, exact.

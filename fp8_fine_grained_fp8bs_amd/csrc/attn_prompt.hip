@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
       const float v = none ? 1.0f : vs > kMinVScale ? vs : kMinVScale;
       g.kq = none ? 1.0f : f > kMinKScale ? f : kMinKScale;
       g.lv = __builtin_amdgcn_logf(v);
-      g.iv = __builtin_amdgcn_rcpf(v);
+      g.iv = v < kTinyV ? 0.0f : __builtin_amdgcn_rcpf(v);   // tiny: summed apart
       info[e % kInfo] = g;
     };
     // Decoding: a thread takes D / 4 codes of one key, and D / 16 keys by 4 dims of
@@ -244,6 +244,15 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
         FP8BS_PIN();
       }
     };
+    auto move = [&](float to) {   // the reference
+      const Moved by(mr - to);
+      lr = by.den(lr);
+      mr = to;
+#pragma unroll
+      for (int u = 0; u < ND; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[u][j] *= by.factor();
+    };
     auto softmax = [&](int i) {
       const int t0 = base + KT * i;
       float kq[NG], lv[NG];
@@ -262,6 +271,39 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
             const int key = 32 * x + 8 * (j >> 2) + (j & 3);
             sc[x][j] = key >= from && key < to ? sc[x][j] : -__builtin_huge_valf();
           }
+      }
+      bool tiny = false;
+#pragma unroll
+      for (int y = 0; y < NG; ++y) tiny |= lv[y] < kTinyLog;   // the same in all lanes
+      if (__builtin_expect(__ballot(tiny) != 0, 0)) {
+        // one score at a time: the registers are full
+        auto each = [&](auto take) {
+#pragma unroll
+          for (int y = 0; y < NY; ++y)
+            if (__ballot(lv[16 * y / GROUP] < kTinyLog) != 0)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                FP8BS_PIN();
+                take(sc[y >> 1][8 * (y & 1) + j], kq[16 * y / GROUP]);
+              }
+        };
+        float den;
+        auto weigh = [&]() {
+          float ref = mr;
+          asm volatile("" : "+v"(ref));   // nothing is kept from one sum for the next
+          den = 0.0f;
+          each([&](float s, float k) { den += __builtin_amdgcn_exp2f(__builtin_fmaf(s, k, -ref)); });
+        };
+        weigh();
+        if (__ballot(den > kMostDen) != 0) {
+          float top = -__builtin_huge_valf();
+          each([&](float s, float k) { top = __builtin_fmaxf(top, s * k); });
+          den = __builtin_fmaxf(den, __shfl_xor(den, 32));   // both halves of a row move together
+          top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+          move(den > kMostDen ? top - kDenTop : mr);
+          weigh();
+        }
+        lr += den;
       }
       // weights under the reference as it stands; their sum shows whether it
       // still holds (no weight above 2^15), which spares the maximum
@@ -300,14 +342,7 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
         }
         all = __builtin_fmaxf(all, __shfl_xor(all, 32));   // both halves of a row move together
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        const float to = all > kMostWeight ? top - kTop : mr;
-        const float f = __builtin_amdgcn_exp2f(mr - to);
-        mr = to;
-        lr *= f;
-#pragma unroll
-        for (int u = 0; u < ND; ++u)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[u][j] *= f;
+        move(all > kMostWeight ? top - kTop : mr);
         weigh();
       }
 #pragma unroll

@@ -309,6 +309,15 @@ __device__ __forceinline__ bool take_piece(Cursor& c) {
 // Whether the stretch goes on into units of another item.
 __device__ __forceinline__ bool goes_on(const Cursor& c) { return c.stop - c.cur > kOpen; }
 
+// To another reference, d = old - new (log2): its factor, and a denominator taken there.  That
+// goes in two steps, for 2^d may fall below FP32's least where the product does not.
+struct Moved {
+  float half;
+  __device__ __forceinline__ explicit Moved(float d) : half(__builtin_amdgcn_exp2f(0.5f * d)) {}
+  __device__ __forceinline__ float factor() const { return half * half; }
+  __device__ __forceinline__ float den(float l) const { return l * half * half; }
+};
+
 // Where the piece's partial belongs: a worker leaves two at most, of the item
 // it ends in the middle of and of the one it begins in the middle of.
 __device__ __forceinline__ int64_t piece_of(const Cursor& c) { return 2 * static_cast<int64_t>(c.w) + (c.ub == 0 ? 1 : 0); }

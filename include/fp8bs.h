@@ -439,7 +439,8 @@ fp8bs_status fp8bs_kv_append(const void *q, int64_t ldq, void *q_out, int64_t ld
  * the output sums are held in FP32; each weight is rounded to FP16 for the
  * product with the values (codes are exact in FP16), the output once to
  * BF16.  Results do not depend on the order in which the GPU runs: equal
- * calls give equal bits.  Value scales below 2^-100 are taken as 2^-100.
+ * calls give equal bits.  Value scales below 2^-100, zero among them, are taken
+ * as 2^-100; scales of every size up to 2^75 may stand side by side.
  * T >= 0 and B >= 0 (either 0 is a no-op), Hkv > 0, Hq % Hkv == 0,
  * Hq / Hkv <= 1024, T * Hq / Hkv < 2^31, window >= 0.  out must not overlap q.
  */

@@ -387,7 +387,7 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
     asm volatile("" : "+v"(mine));   // its token and head are found again, not kept through the loop
     if (mine < t.rows) {
       if (c.whole) {
-        const float inv = lr > 0.0f ? 1.0f / lr : 0.0f;
+        const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;   // a NaN goes on
         const int64_t token = row_token(a, t, mine);
         const int head = row_head(a, t, h, mine);
         uint16_t* at = a.p.out + token * a.p.ldo + static_cast<int64_t>(head) * D + 4 * h2;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
                            pack_bf16x2_rne(o[u][4 * k + 2] * inv, o[u][4 * k + 3] * inv));
         if (h2 == 0 && a.p.lse != nullptr)
           a.p.lse[token * a.p.ldl + head] =
-              lr > 0.0f ? (mr + __builtin_amdgcn_logf(lr)) * 0.693147180559945f : -__builtin_huge_valf();
+              lr == 0.0f ? -__builtin_huge_valf() : (mr + __builtin_amdgcn_logf(lr)) * 0.693147180559945f;
       } else {
         float* at = a.part + piece_of(c) * kManyRows * (D + 2);
 #pragma unroll

@@ -356,7 +356,7 @@ __device__ __forceinline__ int row_head(const AttnArgs& a, const Tile& t, int h,
 template <int VW>
 __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t token, int head, int D, int d0, const float* o,
                                           float m, float l) {
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // a NaN goes on
   uint32_t w[VW / 2];
 #pragma unroll
   for (int i = 0; i < VW / 2; ++i) w[i] = pack_bf16x2_rne(o[2 * i] * inv, o[2 * i + 1] * inv);
@@ -365,7 +365,7 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t token, int 
   else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
   if (d0 == 0 && a.p.lse != nullptr)
     a.p.lse[token * a.p.ldl + head] =
-        l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * 0.693147180559945f : -__builtin_huge_valf();
+        l == 0.0f ? -__builtin_huge_valf() : (m + __builtin_amdgcn_logf(l)) * 0.693147180559945f;
 }
 
 // One partial row's 1/16th.

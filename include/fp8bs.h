@@ -428,7 +428,9 @@ fp8bs_status fp8bs_kv_append(const void *q, int64_t ldq, void *q_out, int64_t ld
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = e^(scale q.k_j)
  * over the keys a row sees: j < kv_len; with causal != 0 j <= its position;
  * with window > 0 j > its position - window.  A row that sees nothing gives
- * zeros (and lse = -infinity).
+ * zeros (and lse = -infinity), one whose query holds a NaN NaNs (lse too).  Codes
+ * and scales of the tokens in the cache have to be finite: a NaN among the values of one
+ * token reaches other rows of its sequence, also such as do not see it.
  *   q    bf16 [T][ldq]    out bf16 [T][ldo]   Hq heads of D
  *   lse  f32 [T][ldl] or NULL  log of sum_j p_j, a value a head
  *   scale > 0 and finite

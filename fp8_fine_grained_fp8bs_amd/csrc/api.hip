@@ -466,6 +466,7 @@ fp8bs_status fp8bs_kv_append(const void* q, int64_t ldq, void* q_out, int64_t ld
   if (q != nullptr) {
     FP8BS_TRY(check_matrix(q, Hq * D, ldq, 2));
     FP8BS_TRY(check_matrix(q_out, Hq * D, ldqo, 2));
+    if (q == q_out && ldq != ldqo) return FP8BS_ERR_INVALID_ARG;   // rows would overwrite others yet unread
   }
   if (cs != nullptr) FP8BS_TRY(check_table(cs, n_pos));
   FP8BS_TRY(check_cache(q_off, kv_len, table, ldt, max_pages, kc, ks, vc, vs));

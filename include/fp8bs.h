@@ -406,6 +406,7 @@ fp8bs_status fp8bs_rope(const void *x, int64_t ldx, void *y, int64_t ldy, const 
  * before that.  A block whose first token arrives ignores what its
  * codes and scale held.  Codes past the last token stay as they were.
  *   q    bf16 [T][ldq] or NULL   q_out bf16 [T][ldqo]   Hq heads of D; q_out may be q
+ *        (with ldqo = ldq), else must not overlap q, k or v
  *   k, v bf16 [T][ldk], [T][ldv] Hkv heads of D
  *   cs   f32 [n_pos][rot] or NULL (no rotation; q must then be NULL);
  *        positions are cut to 0 .. n_pos-1; rot, rot_off and layout as for fp8bs_rope

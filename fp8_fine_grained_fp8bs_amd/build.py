@@ -12,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -89,18 +90,27 @@ def _build_marshal():
 def build(verbose: bool = False) -> str:
     """Compile every HIP source and link libfp8bs.so next to this file, the
     LDS-poisoning debug build libfp8bs_poison.so (tests only), and the Python
-    binding's _marshal.so."""
+    binding's _marshal.so.  The libraries need hipcc alone; without g++ or the headers
+    of Python and torch there is a warning and no _marshal.so, an older one
+    included (the binding then goes through ctypes)."""
     jobs = [(src, False) for src in SOURCES] + [(src, True) for src in LDS_SOURCES]
     with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         marshal = ex.submit(_build_marshal)
         objs = list(ex.map(lambda j: _compile(*j), jobs))
-        marshal.result()
     plain = dict(zip(SOURCES, objs[:len(SOURCES)]))
     poisoned = dict(zip(LDS_SOURCES, objs[len(SOURCES):]))
     _link([plain[s] for s in SOURCES], LIB)
     _link([poisoned.get(s, plain[s]) for s in SOURCES], POISON_LIB)
+    built = [LIB, POISON_LIB]
+    try:
+        marshal.result()
+        built.append(MARSHAL)
+    except Exception as e:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        warnings.warn(f"no {os.path.basename(MARSHAL)}, the attention helpers go through ctypes: {e}")
     if verbose:
-        print("built", LIB + ",", POISON_LIB, "and", MARSHAL)
+        print("built", ", ".join(built))
     return LIB
 
 

@@ -8,6 +8,7 @@ packed-FP32 instructions disabled.
 """
 from __future__ import annotations
 
+import importlib.machinery
 import os
 import shutil
 import subprocess
@@ -22,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
 # the Python binding's short way into the attention operators (host code)
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 # debug build for race checks: kernels fill their LDS with 0xFF before use
 POISON_LIB = os.path.join(PKG, "libfp8bs_poison.so")
 SOURCES = ["api.hip", "quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "e5m6.hip", "swiglu.hip",
@@ -76,6 +77,7 @@ def _build_marshal():
     from torch.utils import cpp_extension
     include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f'-DFP8BS_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
     for d in include:
         cmd += ["-isystem", d]
@@ -90,8 +92,8 @@ def _build_marshal():
 def build(verbose: bool = False) -> str:
     """Compile every HIP source and link libfp8bs.so next to this file, the
     LDS-poisoning debug build libfp8bs_poison.so (tests only), and the Python
-    binding's _marshal.so.  The libraries need hipcc alone; without g++ or the headers
-    of Python and torch there is a warning and no _marshal.so, an older one
+    binding's _marshal module.  The libraries need hipcc alone; without g++ or the headers
+    of Python and torch there is a warning and no module, an older one
     included (the binding then goes through ctypes)."""
     jobs = [(src, False) for src in SOURCES] + [(src, True) for src in LDS_SOURCES]
     with ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:

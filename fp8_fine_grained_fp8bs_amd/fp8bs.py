@@ -13,10 +13,13 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.machinery
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfp8bs.so")
+# the compiled short way into the attention operators, of this Python
+MARSHAL_PATH = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 OK = 0
 ERR_INVALID_ARG = 1
@@ -376,18 +379,30 @@ def fp8bs_grouped_gemm(a, sa, b, sb, offsets, d, dt, stream=None):
           int(E), M_total, _ptr(d), int(dt), N, K, _stream(stream))
 
 
+def _load_marshal():
+    """The short way's functions by entry point: none where it has not been built, or,
+    with a warning, was built for another torch."""
+    if not os.path.exists(MARSHAL_PATH):
+        return {}
+    import torch  # its libraries are the module's
+    try:
+        from . import _marshal as module
+        if module.torch_version != torch.__version__:
+            raise ImportError(f"built for torch {module.torch_version}, this is {torch.__version__}")
+        return {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
+    except (ImportError, AttributeError) as e:
+        import warnings
+        warnings.warn(f"{MARSHAL_PATH}: {e}; the attention helpers go through ctypes")
+        return {}
+
+
 def _short(name, *args):
     """The named attention operator by the compiled short way (csrc/marshal.cpp): its
     result, or None where an argument is not as it should be (the checks below then
-    say which) or the short way has not been built (the library is then called
-    through ctypes)."""
+    say which) or there is no short way (the library is then called through ctypes)."""
     global _marshal
     if _marshal is None:
-        _marshal = {}
-        if os.path.exists(os.path.join(PKG, "_marshal.so")):
-            import torch  # noqa: F401  (its libraries are the module's)
-            from . import _marshal as module
-            _marshal = {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
+        _marshal = _load_marshal()
     way = _marshal.get(name)
     if way is None:
         return None

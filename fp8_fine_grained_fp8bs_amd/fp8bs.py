@@ -206,7 +206,7 @@ def _current_stream():
 def _stream(stream):
     if stream is None:
         return _current_stream()
-    if type(stream) is int:
+    if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 

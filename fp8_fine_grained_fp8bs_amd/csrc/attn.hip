@@ -67,6 +67,8 @@ __global__ __launch_bounds__(256, D == 64 && NR == 1 ? 4 : 2) void attn_rows_ker
   static_assert(sizeof(obuf) >= kMaxSlots * sizeof(int), "the line's prefix sums fit");
   __shared__ int sums[4];
   poison_lds<sizeof(obuf)>(obuf);
+  poison_lds<sizeof(ml)>(ml);
+  poison_lds<sizeof(sums)>(sums);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = uniform(tid >> 6);
   const int m16 = lane & 15, g = lane >> 4;
   const int page_mask = (1 << a.pshift) - 1;

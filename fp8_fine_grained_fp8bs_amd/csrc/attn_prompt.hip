@@ -76,6 +76,8 @@ __global__ __launch_bounds__(256, D == 64 && GROUP >= 32 ? 3 : 2) void attn_prom
   static_assert(sizeof(kbuf) >= kMaxSlots * sizeof(int), "the line's prefix sums fit");
   poison_lds<sizeof(kbuf)>(kbuf);
   poison_lds<sizeof(vbuf)>(vbuf);
+  poison_lds<sizeof(info)>(info);
+  poison_lds<sizeof(sums)>(sums);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 63, wv = uniform(tid >> 6);
   const int n32 = lane & 31, h2 = lane >> 5;
   const int page_mask = (1 << a.pshift) - 1;

@@ -6,17 +6,22 @@
 // around loads in flight.  A wave takes steps of 32 keys, its loads going
 // straight from the cache to registers (no LDS, no barrier in the loop), two
 // steps in flight, page numbers a further step ahead.  Loads are
-// non-temporal: each byte is read once (152 us against 142 with plain ones, 96
-// requests of one token).
+// non-temporal: each byte is read once (96 requests of one token: 123 us, with plain
+// loads 137.  A cache of 100 MB that is attended again right away, with nothing between,
+// stays in the last-level cache with plain loads: 25.0 against 26.7 with heads of 64).
 //
 // Measured, heads of 128, pages of 64, 32 query heads on 8: 96 requests of 200 to
 // 16384 tokens 117 us in this kernel, 6.3 TB/s of the cache's bytes (blocks of 8 KB
 // in random order are read at 6.4 by loads alone, a linear copy's reads at 7.1); one
 // request of 130000 tokens 45 us, 5.9 TB/s.  Those are bound by HBM.  48 requests with
 // heads of 64 take 24 us for 106 MB, 24 requests of 4 drafted tokens and 7 query
-// heads a key/value head 34 us for 139 MB: with every page in the caches they would take
-// 22 and 33 with the join, so the vector work of a step (decoding, softmax) and a piece's
-// start bound these.
+// heads a key/value head 35 us for 139 MB: with every page in the caches they would take
+// 22 and 33 with the join, so HBM does not bound these.  A wave has 8 steps in the second:
+// 393 VALU instructions a step by the counters, 260 in the listing of a step, the rest
+// the pieces' starts and joins; VALU is active in 22 % of the wave cycles (two waves a SIMD),
+// the matrix units in less.  So it is the chain of each start and join, which few steps
+// pay for, and the second launch (5 us) that bound these, with some 58 of a step's
+// instructions finding pages and 64-bit addresses by lane.
 //
 // Mathematics of a step.  S^T = K Q^T on 16x16x32 BF16 MFMAs (every E4M3 code
 // is a BF16 value, products are exact), so a lane holds scores of one query row

@@ -11,13 +11,16 @@
 // one barrier.  Two workgroups live on a compute unit and share no barrier,
 // so one's softmax runs under the other's products.
 //
-// Measured, heads of 128, 32 query heads on 8: a prompt of 8192 tokens 587 us, 937
+// Measured, heads of 128, 32 query heads on 8: a prompt of 8192 tokens 581 us, 947
 // TFLOP/s (a large library product of BF16 matrices reaches 1230); two pieces of 512
-// tokens 546 us with the join, 914.  Products, LDS reads and barriers alone took 367 us
+// tokens 545 us with the join, 916.  Products, LDS reads and barriers alone took 367 us
 // of the pieces (in the form with two groups, below): the rest is vector work that does
-// not fit under the products, 7.5 VALU instructions a matrix instruction of 32
-// cycles, 2 of them exponentials at a quarter rate.  With heads of 64 it is 19: 7
-// packed prompts 73 us, 460 TFLOP/s.  Also built, in us for prompt / pieces: 128 rows with decoding before the
+// not fit under the products, 7 VALU instructions a matrix instruction of 32
+// cycles in a tile without a mask, 1 of them an exponential at a quarter rate.  With heads of 64
+// it is 12; 7 packed prompts with a window, 74 us, 457 TFLOP/s, issue 20 over the whole
+// call: an item has about 12 tiles there, and beside them its start, the filling of all
+// groups, a first tile weighed twice, masked tiles at both ends and its output, none
+// of it under its own products.  Also built, in us for prompt / pieces: 128 rows with decoding before the
 // products 618 / 602; 256 rows on eight waves in two alternating groups 583 / 519, but
 // 189 against 143 on packed prompts; one wave a SIMD with 64 rows 756 / 638; codes kept
 // in LDS and decoded by each wave 643 / 568; half a tile's weights between the

@@ -748,7 +748,8 @@ def rope_table(n_pos, rot, base=10000.0, factor=1.0, orig_len=0, turns_lo=1.0, t
 
 
 def rope(x, pos, cs, rot_offset=0, layout="half", inverse=False, stream=None):
-    """x bf16 [T][H][D] rotated (inverse: the gradient)."""
+    """x bf16 [T][H][D] rotated.  Not recorded by autograd: y is detached, and the
+    gradient of x is rope(dy, ..., inverse=True)."""
     y = _short("fp8bs_rope", x, pos, cs, rot_offset, _layout(layout), bool(inverse), _stream_later(stream))
     if y is not None:
         return y
@@ -793,7 +794,8 @@ def _scratch(nbytes, device, stream):
 def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None, causal=True, window=0,
                with_lse=False, ws=None, stream=None):
     """Attention of q bf16 [T][Hq][D] over the cache; scale None: D^-1/2.
-    The working memory is allocated unless given."""
+    The working memory is allocated unless given.  A table no wider than the longest
+    context needs, and single tokens in a call of their own, are faster."""
     if ws is None and stream is None and not with_lse:
         out = _short("fp8bs_attn_paged", kc, ks, vc, vs, table, kv_len, q_off, _address("fp8bs_attn_paged_ws"), q, max_q,
                      scale, bool(causal), window, _current_stream)

@@ -27,9 +27,10 @@ MARSHAL = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[
 # debug build for race checks: kernels fill their LDS with 0xFF before use
 POISON_LIB = os.path.join(PKG, "libfp8bs_poison.so")
 SOURCES = ["api.hip", "quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "e5m6.hip", "swiglu.hip",
-           "rope.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]
+           "rope.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip", "norm.hip", "moe.hip"]
 # the sources whose kernels use LDS
-LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip"]
+LDS_SOURCES = ["quant.hip", "requant.hip", "gemm.hip", "gemm_bf16a.hip", "kv_append.hip", "attn.hip", "attn_prompt.hip",
+               "norm.hip", "moe.hip"]
 ARCH = "gfx950"
 
 

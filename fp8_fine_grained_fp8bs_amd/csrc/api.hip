@@ -127,11 +127,126 @@ fp8bs_status check_cache(const int32_t* q_off, const int32_t* kv_len, const int3
   return FP8BS_OK;
 }
 
+// Rows of the norm live in a workgroup's registers.
+constexpr int64_t kMaxNormWidth = 16384;
+// Assignments of a sort are numbered in 32 bits, its counts' sums too.
+constexpr int64_t kMaxAssignments = int64_t(1) << 30;
+
+fp8bs_status check_type(fp8bs_out_dtype t) {
+  return t == FP8BS_OUT_BF16 || t == FP8BS_OUT_F32 ? FP8BS_OK : FP8BS_ERR_INVALID_ARG;
+}
+
+fp8bs_status check_norm_sizes(int64_t T, int64_t C) {
+  if (T < 0 || C <= 0) return FP8BS_ERR_INVALID_ARG;
+  if (C % 128 != 0 || C > kMaxNormWidth || T > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_gamma(const void* gamma, fp8bs_out_dtype gt) {
+  if (gamma == nullptr || check_type(gt) != FP8BS_OK) return FP8BS_ERR_INVALID_ARG;
+  return aligned(gamma, 16) ? FP8BS_OK : FP8BS_ERR_MISALIGNED;
+}
+
+// An output that may be an input itself, but not one with other rows.
+fp8bs_status check_in_place(const void* out, int64_t ldo, const void* in, int64_t ldi) {
+  return out != nullptr && out == in && ldo != ldi ? FP8BS_ERR_INVALID_ARG : FP8BS_OK;
+}
+
+// Codes with their scales, both or neither.
+fp8bs_status check_codes(const uint8_t* q, int64_t ldq, const float* s, int64_t lds, int64_t cols) {
+  if ((q == nullptr) != (s == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (q == nullptr) return FP8BS_OK;
+  const fp8bs_status st = check_matrix(q, cols, ldq, 1);
+  return st != FP8BS_OK ? st : check_scales(s, cols / 128, lds);
+}
+
+fp8bs_status check_choices(int64_t T, int64_t k, int64_t M) {
+  if (T < 0 || k <= 0 || M < 0) return FP8BS_ERR_INVALID_ARG;
+  if (k > fp8bs::kMaxChoices || T > kMaxInt32 || M > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  return FP8BS_OK;
+}
+
+fp8bs_status check_columns(int64_t C) {
+  if (C <= 0) return FP8BS_ERR_INVALID_ARG;
+  return C % 128 == 0 && C <= kMaxInt32 - 65536 ? FP8BS_OK : FP8BS_ERR_UNSUPPORTED_SHAPE;   // columns in 32 bits
+}
+
+fp8bs_status check_sort_sizes(int64_t T, int64_t k, int64_t E) {
+  const fp8bs_status st = check_choices(T, k, 0);
+  if (st != FP8BS_OK) return st;
+  if (E <= 0) return FP8BS_ERR_INVALID_ARG;
+  return E <= fp8bs::kMaxExperts && T <= kMaxAssignments / k ? FP8BS_OK : FP8BS_ERR_UNSUPPORTED_SHAPE;
+}
+
 #define FP8BS_TRY(expr)                 \
   do {                                  \
     fp8bs_status _s = (expr);           \
     if (_s != FP8BS_OK) return _s;      \
   } while (0)
+
+// The sort's arguments, checked.
+fp8bs_status sort_of(const void* ids, fp8bs_index_type it, int64_t ldi, int64_t T, int64_t k, int64_t first, int64_t E,
+                     int64_t M, int32_t* offsets, int32_t* slot, void* ws, int64_t ws_bytes, fp8bs::MoeIds& p) {
+  if (it != FP8BS_INDEX_I32 && it != FP8BS_INDEX_I64) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_sort_sizes(T, k, E));
+  FP8BS_TRY(check_choices(T, k, M));
+  if (first < 0 || offsets == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(offsets, 4) || !aligned(ws, 4)) return FP8BS_ERR_MISALIGNED;
+  if (T > 0) {
+    if (ids == nullptr || slot == nullptr || ldi < k) return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(ids, it == FP8BS_INDEX_I64 ? 8 : 4) || !aligned(slot, 4)) return FP8BS_ERR_MISALIGNED;
+    const int64_t need = fp8bs_moe_sort_ws(T, k, E);
+    if (ws_bytes < need || (need > 0 && ws == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  }
+  p.ids = ids;
+  p.wide = it == FP8BS_INDEX_I64;
+  p.ldi = ldi;
+  p.T = T;
+  p.k = static_cast<int>(k);
+  p.first = first;
+  p.E = static_cast<int>(E);
+  p.offsets = offsets;
+  p.slot = slot;
+  p.M = M;
+  p.ws = static_cast<int32_t*>(ws);
+  return FP8BS_OK;
+}
+
+// The arguments of rows to their places, checked (those of T > 0 tokens).
+fp8bs_status rows_of(fp8bs_requant_src src, const void* x, int64_t ldx, const float* s_in, int64_t lds_in, int64_t T,
+                     int64_t C, const int32_t* slot, int64_t k, uint8_t* q, int64_t ldq, float* s, int64_t lds, void* y,
+                     int64_t ldy, int64_t M, fp8bs::MoeRows& p) {
+  if (src != FP8BS_SRC_FP8_1x128 && src != FP8BS_SRC_BF16) return FP8BS_ERR_INVALID_ARG;
+  const bool codes = src == FP8BS_SRC_FP8_1x128;
+  FP8BS_TRY(check_choices(T, k, M));
+  FP8BS_TRY(check_columns(C));
+  if ((q == nullptr && y == nullptr) || (codes && y != nullptr)) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_codes(q, ldq, s, lds, C));
+  if (y != nullptr) FP8BS_TRY(check_matrix(y, C, ldy, 2));
+  if (T > 0) {
+    FP8BS_TRY(check_matrix(x, C, ldx, codes ? 1 : 2));
+    if (codes) FP8BS_TRY(check_scales(s_in, C / 128, lds_in));
+    if (slot == nullptr) return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(slot, 4)) return FP8BS_ERR_MISALIGNED;
+  }
+  p.codes_in = codes;
+  p.x = x;
+  p.ldx = ldx;
+  p.s_in = s_in;
+  p.lds_in = lds_in;
+  p.T = T;
+  p.C = static_cast<int>(C);
+  p.slot = slot;
+  p.k = static_cast<int>(k);
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  p.lds = lds;
+  p.y = static_cast<uint16_t*>(y);
+  p.ldy = ldy;
+  p.M = M;
+  return FP8BS_OK;
+}
 
 }  // namespace
 
@@ -563,6 +678,263 @@ fp8bs_status fp8bs_attn_paged(const void* q, int64_t ldq, void* out, int64_t ldo
   p.window = window;
   p.ws = ws;
   return launched(fp8bs::launch_attn_paged(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_rmsnorm_quant_1x128(const void* x, int64_t ldx, const void* r, int64_t ldr, const void* gamma,
+                                       fp8bs_out_dtype gt, float eps, int64_t T, int64_t C, void* h, int64_t ldh,
+                                       uint8_t* q, int64_t ldq, float* s, int64_t lds, void* y, int64_t ldy,
+                                       float* rstd, void* stream) {
+  FP8BS_TRY(check_norm_sizes(T, C));
+  if (!(eps > 0.0f) || !std::isfinite(eps)) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_type(gt));
+  if (T == 0) return FP8BS_OK;
+  if ((r == nullptr) != (h == nullptr)) return FP8BS_ERR_INVALID_ARG;
+  if (q == nullptr && y == nullptr) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_matrix(x, C, ldx, 2));
+  FP8BS_TRY(check_gamma(gamma, gt));
+  if (r != nullptr) {
+    FP8BS_TRY(check_matrix(r, C, ldr, 2));
+    FP8BS_TRY(check_matrix(h, C, ldh, 2));
+    FP8BS_TRY(check_in_place(h, ldh, x, ldx));
+    FP8BS_TRY(check_in_place(h, ldh, r, ldr));
+  }
+  FP8BS_TRY(check_codes(q, ldq, s, lds, C));
+  if (y != nullptr) FP8BS_TRY(check_matrix(y, C, ldy, 2));
+  if (!aligned(rstd, 4)) return FP8BS_ERR_MISALIGNED;
+  FP8BS_TRY(check_device());
+  fp8bs::RmsNorm p;
+  p.x = static_cast<const uint16_t*>(x);
+  p.ldx = ldx;
+  p.r = static_cast<const uint16_t*>(r);
+  p.ldr = ldr;
+  p.gamma = gamma;
+  p.gamma_f32 = gt == FP8BS_OUT_F32;
+  p.eps = eps;
+  p.T = T;
+  p.C = static_cast<int>(C);
+  p.h = static_cast<uint16_t*>(h);
+  p.ldh = ldh;
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  p.lds = lds;
+  p.y = static_cast<uint16_t*>(y);
+  p.ldy = ldy;
+  p.rstd = rstd;
+  return launched(fp8bs::launch_rmsnorm(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8bs_rmsnorm_bwd_ws(int64_t T, int64_t C) {
+  if (check_norm_sizes(T, C) != FP8BS_OK) return -1;
+  return fp8bs::rmsnorm_bwd_ws(T, static_cast<int>(C));
+}
+
+fp8bs_status fp8bs_rmsnorm_bwd(const void* dn, int64_t lddn, const void* dres, int64_t lddr, const void* h,
+                               int64_t ldh, const void* gamma, fp8bs_out_dtype gt, const float* rstd, int64_t T,
+                               int64_t C, void* dx, int64_t lddx, float* dgamma, void* ws, int64_t ws_bytes,
+                               void* stream) {
+  FP8BS_TRY(check_norm_sizes(T, C));
+  FP8BS_TRY(check_type(gt));
+  if (!aligned(dgamma, 16) || !aligned(ws, 16)) return FP8BS_ERR_MISALIGNED;
+  if (T == 0 && dgamma == nullptr) return FP8BS_OK;
+  if (T > 0) {
+    FP8BS_TRY(check_matrix(dn, C, lddn, 2));
+    if (dres != nullptr) FP8BS_TRY(check_matrix(dres, C, lddr, 2));
+    FP8BS_TRY(check_matrix(h, C, ldh, 2));
+    FP8BS_TRY(check_matrix(dx, C, lddx, 2));
+    FP8BS_TRY(check_gamma(gamma, gt));
+    FP8BS_TRY(check_in_place(dx, lddx, dn, lddn));
+    FP8BS_TRY(check_in_place(dx, lddx, dres, lddr));
+    FP8BS_TRY(check_in_place(dx, lddx, h, ldh));
+    if (rstd == nullptr) return FP8BS_ERR_INVALID_ARG;
+    if (!aligned(rstd, 4)) return FP8BS_ERR_MISALIGNED;
+    if (dgamma != nullptr && (ws == nullptr || ws_bytes < fp8bs_rmsnorm_bwd_ws(T, C))) return FP8BS_ERR_INVALID_ARG;
+  }
+  FP8BS_TRY(check_device());
+  fp8bs::RmsNormBwd p;
+  p.dn = static_cast<const uint16_t*>(dn);
+  p.lddn = lddn;
+  p.dres = static_cast<const uint16_t*>(dres);
+  p.lddr = lddr;
+  p.h = static_cast<const uint16_t*>(h);
+  p.ldh = ldh;
+  p.gamma = gamma;
+  p.gamma_f32 = gt == FP8BS_OUT_F32;
+  p.rstd = rstd;
+  p.T = T;
+  p.C = static_cast<int>(C);
+  p.dx = static_cast<uint16_t*>(dx);
+  p.lddx = lddx;
+  p.dgamma = dgamma;
+  p.ws = static_cast<float*>(ws);
+  return launched(fp8bs::launch_rmsnorm_bwd(p, static_cast<hipStream_t>(stream)));
+}
+
+int64_t fp8bs_moe_sort_ws(int64_t T, int64_t k, int64_t E) {
+  if (check_sort_sizes(T, k, E) != FP8BS_OK) return -1;
+  return fp8bs::moe_sort_ws(T, static_cast<int>(k), static_cast<int>(E));
+}
+
+fp8bs_status fp8bs_moe_sort(const void* ids, fp8bs_index_type it, int64_t ldi, int64_t T, int64_t k, int64_t first,
+                            int64_t E, int64_t M, int32_t* offsets, int32_t* slot, void* ws, int64_t ws_bytes,
+                            void* stream) {
+  fp8bs::MoeIds p;
+  FP8BS_TRY(sort_of(ids, it, ldi, T, k, first, E, M, offsets, slot, ws, ws_bytes, p));
+  FP8BS_TRY(check_device());
+  return launched(fp8bs::launch_moe_sort(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_moe_gather(fp8bs_requant_src src, const void* x, int64_t ldx, const float* s_in, int64_t lds_in,
+                              int64_t T, int64_t C, const int32_t* slot, int64_t k, uint8_t* q, int64_t ldq,
+                              float* s, int64_t lds, void* y, int64_t ldy, int64_t M, void* stream) {
+  fp8bs::MoeRows p;
+  if (T == 0 || M == 0) {   // nothing to write: the buffers need not be there
+    if (src != FP8BS_SRC_FP8_1x128 && src != FP8BS_SRC_BF16) return FP8BS_ERR_INVALID_ARG;
+    FP8BS_TRY(check_choices(T, k, M));
+    return check_columns(C);
+  }
+  FP8BS_TRY(rows_of(src, x, ldx, s_in, lds_in, T, C, slot, k, q, ldq, s, lds, y, ldy, M, p));
+  FP8BS_TRY(check_device());
+  return launched(fp8bs::launch_moe_gather(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_moe_dispatch(fp8bs_requant_src src, const void* x, int64_t ldx, const float* s_in,
+                                int64_t lds_in, int64_t T, int64_t C, const void* ids, fp8bs_index_type it,
+                                int64_t ldi, int64_t k, int64_t first, int64_t E, int32_t* offsets, int32_t* slot,
+                                uint8_t* q, int64_t ldq, float* s, int64_t lds, void* y, int64_t ldy, int64_t M,
+                                void* ws, int64_t ws_bytes, void* stream) {
+  fp8bs::MoeIds p;
+  fp8bs::MoeRows r;
+  FP8BS_TRY(sort_of(ids, it, ldi, T, k, first, E, M, offsets, slot, ws, ws_bytes, p));
+  if (T == 0 || M == 0) {   // no rows: the sort alone
+    if (src != FP8BS_SRC_FP8_1x128 && src != FP8BS_SRC_BF16) return FP8BS_ERR_INVALID_ARG;
+    FP8BS_TRY(check_columns(C));
+    FP8BS_TRY(check_device());
+    return launched(fp8bs::launch_moe_sort(p, static_cast<hipStream_t>(stream)));
+  }
+  FP8BS_TRY(rows_of(src, x, ldx, s_in, lds_in, T, C, slot, k, q, ldq, s, lds, y, ldy, M, r));
+  FP8BS_TRY(check_device());
+  return launched(fp8bs::launch_moe_dispatch(p, r, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_moe_combine(const void* y, fp8bs_out_dtype yt, int64_t ldy, int64_t M, const int32_t* slot,
+                               const float* w, int64_t ldw, int64_t T, int64_t k, int64_t N, const void* add,
+                               int64_t ldadd, void* out, int64_t ldo, void* stream) {
+  FP8BS_TRY(check_type(yt));
+  FP8BS_TRY(check_choices(T, k, M));
+  FP8BS_TRY(check_columns(N));
+  if (T == 0) return FP8BS_OK;
+  if (M > 0) FP8BS_TRY(check_matrix(y, N, ldy, yt == FP8BS_OUT_F32 ? 4 : 2));
+  if (slot == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(slot, 4)) return FP8BS_ERR_MISALIGNED;
+  if (w != nullptr) FP8BS_TRY(check_scales(w, k, ldw));
+  if (add != nullptr) FP8BS_TRY(check_matrix(add, N, ldadd, 2));
+  FP8BS_TRY(check_matrix(out, N, ldo, 2));
+  FP8BS_TRY(check_in_place(out, ldo, add, ldadd));
+  if (M > 0 && out == y) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_device());
+  fp8bs::MoeCombine p;
+  p.y = y;
+  p.y_f32 = yt == FP8BS_OUT_F32;
+  p.ldy = ldy;
+  p.M = M;
+  p.slot = slot;
+  p.w = w;
+  p.ldw = ldw;
+  p.T = T;
+  p.k = static_cast<int>(k);
+  p.N = static_cast<int>(N);
+  p.add = static_cast<const uint16_t*>(add);
+  p.ldadd = ldadd;
+  p.out = static_cast<uint16_t*>(out);
+  p.ldo = ldo;
+  return launched(fp8bs::launch_moe_combine(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_moe_combine_bwd(const void* dout, int64_t lddo, const void* y, fp8bs_out_dtype yt, int64_t ldy,
+                                   const int32_t* slot, const float* w, int64_t ldw, int64_t T, int64_t k,
+                                   int64_t N, uint8_t* q, int64_t ldq, float* s, int64_t lds, void* dy,
+                                   int64_t lddy, int64_t M, float* dw, int64_t lddw, void* stream) {
+  FP8BS_TRY(check_type(yt));
+  FP8BS_TRY(check_choices(T, k, M));
+  FP8BS_TRY(check_columns(N));
+  if (T == 0) return FP8BS_OK;
+  // without rows there is only dw, all zeros
+  if (M == 0) {
+    q = nullptr;
+    s = nullptr;
+    dy = nullptr;
+    if (dw == nullptr) return FP8BS_OK;
+  }
+  if (q == nullptr && dy == nullptr && dw == nullptr) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_matrix(dout, N, lddo, 2));
+  if (slot == nullptr) return FP8BS_ERR_INVALID_ARG;
+  if (!aligned(slot, 4)) return FP8BS_ERR_MISALIGNED;
+  FP8BS_TRY(check_scales(w, k, ldw));
+  FP8BS_TRY(check_codes(q, ldq, s, lds, N));
+  if (dy != nullptr) FP8BS_TRY(check_matrix(dy, N, lddy, 2));
+  if (dw != nullptr) {
+    FP8BS_TRY(check_scales(dw, k, lddw));
+    if (M > 0) FP8BS_TRY(check_matrix(y, N, ldy, yt == FP8BS_OUT_F32 ? 4 : 2));
+  }
+  if (dy != nullptr && (dy == y || dy == dout)) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_device());
+  fp8bs::MoeCombineBwd p;
+  p.dout = static_cast<const uint16_t*>(dout);
+  p.lddo = lddo;
+  p.y = y;
+  p.y_f32 = yt == FP8BS_OUT_F32;
+  p.ldy = ldy;
+  p.slot = slot;
+  p.w = w;
+  p.ldw = ldw;
+  p.T = T;
+  p.k = static_cast<int>(k);
+  p.N = static_cast<int>(N);
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  p.lds = lds;
+  p.dy = static_cast<uint16_t*>(dy);
+  p.lddy = lddy;
+  p.M = M;
+  p.dw = dw;
+  p.lddw = lddw;
+  return launched(fp8bs::launch_moe_combine_bwd(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8bs_status fp8bs_swiglu_bwd_quant_1x128(const void* dh, int64_t lddh, const void* g, int64_t ldg, const void* u,
+                                          int64_t ldu, int64_t T, int64_t I, uint8_t* q, int64_t ldq, float* s,
+                                          int64_t lds, void* d, int64_t ldd, void* h, int64_t ldh, void* stream) {
+  if (T < 0 || I <= 0) return FP8BS_ERR_INVALID_ARG;
+  if (I % 128 != 0 || I > kMaxInt32 / 4 || T > kMaxInt32) return FP8BS_ERR_UNSUPPORTED_SHAPE;
+  if (T == 0) return FP8BS_OK;
+  if (q == nullptr && d == nullptr && h == nullptr) return FP8BS_ERR_INVALID_ARG;
+  FP8BS_TRY(check_matrix(dh, I, lddh, 2));
+  FP8BS_TRY(check_matrix(g, I, ldg, 2));
+  FP8BS_TRY(check_matrix(u, I, ldu, 2));
+  FP8BS_TRY(check_codes(q, ldq, s, lds, 2 * I));
+  if (d != nullptr) FP8BS_TRY(check_matrix(d, 2 * I, ldd, 2));
+  if (h != nullptr) FP8BS_TRY(check_matrix(h, I, ldh, 2));
+  FP8BS_TRY(check_device());
+  fp8bs::SwigluBwd p;
+  p.dh = static_cast<const uint16_t*>(dh);
+  p.lddh = lddh;
+  p.g = static_cast<const uint16_t*>(g);
+  p.ldg = ldg;
+  p.u = static_cast<const uint16_t*>(u);
+  p.ldu = ldu;
+  p.T = T;
+  p.I = I;
+  p.q = q;
+  p.ldq = ldq;
+  p.s = s;
+  p.lds = lds;
+  p.d = static_cast<uint16_t*>(d);
+  p.ldd = ldd;
+  p.h = static_cast<uint16_t*>(h);
+  p.ldh = ldh;
+  return launched(fp8bs::launch_swiglu_bwd(p, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

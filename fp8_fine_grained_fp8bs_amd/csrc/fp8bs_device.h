@@ -303,6 +303,29 @@ __device__ __forceinline__ float wave_max(float v) {
   return __int_as_float(x);
 }
 
+// Sum over the 16 lanes of a DPP row; every lane of the row gets the same bits
+// (both operands of every addition are the same two numbers in each lane).
+template <int CTRL>
+__device__ __forceinline__ float dpp_move(float v) {
+  const int x = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  v += dpp_move<0xB1>(v);    // quad_perm [1,0,3,2]
+  v += dpp_move<0x4E>(v);    // quad_perm [2,3,0,1]
+  v += dpp_move<0x141>(v);   // row_half_mirror
+  v += dpp_move<0x140>(v);   // row_mirror
+  return v;
+}
+
+// Sum over all 64 lanes (result in every lane).
+__device__ __forceinline__ float wave_sum(float v) {
+  const int x = __float_as_int(row16_sum(v));
+  const float a = __int_as_float(__builtin_amdgcn_readlane(x, 0)), b = __int_as_float(__builtin_amdgcn_readlane(x, 16));
+  const float c = __int_as_float(__builtin_amdgcn_readlane(x, 32)), d = __int_as_float(__builtin_amdgcn_readlane(x, 48));
+  return (a + b) + (c + d);
+}
+
 // Two floats to two bf16 (low half = a), round to nearest even: one
 // v_cvt_pk_bf16_f32 (IEEE rounding of the default mode; FP32 subnormals
 // kept).
@@ -310,6 +333,19 @@ typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t pack_bf16x2_rne(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
+}
+
+// Eight bf16 of a 16-byte vector to floats, and back (nearest even).
+__device__ __forceinline__ void bf16x8_unpack(const u32x4& v, float (&f)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = bf16_lo(v[j]);
+    f[2 * j + 1] = bf16_hi(v[j]);
+  }
+}
+__device__ __forceinline__ u32x4 bf16x8_pack(const float (&f)[8]) {
+  return u32x4{pack_bf16x2_rne(f[0], f[1]), pack_bf16x2_rne(f[2], f[3]), pack_bf16x2_rne(f[4], f[5]),
+               pack_bf16x2_rne(f[6], f[7])};
 }
 
 // Debug builds with FP8BS_POISON_LDS fill a kernel's LDS with 0xFF bytes

@@ -127,4 +127,142 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st);
 // Working memory of launch_attn_paged: a function of the sizes alone.
 int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page);
 
+// Arguments of fp8bs_rmsnorm_quant_1x128 (r, q, y, rstd may be null; q with s, r with h).
+struct RmsNorm {
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* r;
+  int64_t ldr;
+  const void* gamma;
+  bool gamma_f32;
+  float eps;
+  int64_t T;
+  int C;
+  uint16_t* h;
+  int64_t ldh;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  uint16_t* y;
+  int64_t ldy;
+  float* rstd;
+};
+hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t st);
+
+// Arguments of fp8bs_rmsnorm_bwd (dres, dgamma may be null; ws with dgamma).
+struct RmsNormBwd {
+  const uint16_t* dn;
+  int64_t lddn;
+  const uint16_t* dres;
+  int64_t lddr;
+  const uint16_t* h;
+  int64_t ldh;
+  const void* gamma;
+  bool gamma_f32;
+  const float* rstd;
+  int64_t T;
+  int C;
+  uint16_t* dx;
+  int64_t lddx;
+  float* dgamma;
+  float* ws;
+};
+hipError_t launch_rmsnorm_bwd(const RmsNormBwd& p, hipStream_t st);
+int64_t rmsnorm_bwd_ws(int64_t T, int C);
+
+constexpr int kMaxExperts = 1024;   // held here
+constexpr int kMaxChoices = 64;     // experts of a token
+
+// The assignments of a sort, and what it writes.
+struct MoeIds {
+  const void* ids;
+  bool wide;   // int64
+  int64_t ldi, T;
+  int k;
+  int64_t first;
+  int E;
+  int32_t* offsets;
+  int32_t* slot;
+  int64_t M;
+  int32_t* ws;
+};
+int64_t moe_sort_ws(int64_t T, int k, int E);
+hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st);
+
+// Rows of T tokens and where they go (q with s, y may be null; codes in go out as codes).
+struct MoeRows {
+  bool codes_in;
+  const void* x;
+  int64_t ldx;
+  const float* s_in;
+  int64_t lds_in, T;
+  int C;
+  const int32_t* slot;
+  int k;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  uint16_t* y;
+  int64_t ldy, M;
+};
+hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st);
+hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st);
+
+struct MoeCombine {
+  const void* y;
+  bool y_f32;
+  int64_t ldy, M;
+  const int32_t* slot;
+  const float* w;   // null: 1
+  int64_t ldw, T;
+  int k, N;
+  const uint16_t* add;   // may be null
+  int64_t ldadd;
+  uint16_t* out;
+  int64_t ldo;
+};
+hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st);
+
+struct MoeCombineBwd {
+  const uint16_t* dout;
+  int64_t lddo;
+  const void* y;   // with dw
+  bool y_f32;
+  int64_t ldy;
+  const int32_t* slot;
+  const float* w;
+  int64_t ldw, T;
+  int k, N;
+  uint8_t* q;   // with s; may be null
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  uint16_t* dy;   // may be null
+  int64_t lddy, M;
+  float* dw;   // may be null
+  int64_t lddw;
+};
+hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st);
+
+// Arguments of fp8bs_swiglu_bwd_quant_1x128 (q with s, d, h may be null).
+struct SwigluBwd {
+  const uint16_t* dh;
+  int64_t lddh;
+  const uint16_t* g;
+  int64_t ldg;
+  const uint16_t* u;
+  int64_t ldu, T, I;
+  uint8_t* q;
+  int64_t ldq;
+  float* s;
+  int64_t lds;
+  uint16_t* d;
+  int64_t ldd;
+  uint16_t* h;
+  int64_t ldh;
+};
+hipError_t launch_swiglu_bwd(const SwigluBwd& p, hipStream_t st);
+
 }  // namespace fp8bs

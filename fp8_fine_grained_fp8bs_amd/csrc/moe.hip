@@ -1,0 +1,531 @@
+// moe.hip -- tokens sorted by expert and brought back, with their gradients
+// (gfx950): what stands before and behind the grouped GEMM.
+//
+// An assignment (t, j) sends token t to expert ids[t][j].  The assignments to
+// the experts held here, ordered by (expert, t, j), are the rows of the
+// grouped GEMM's operand; slot[t][j] is an assignment's row, -1 where it has
+// none.  Everything else goes by token: a token's row of activations is
+// quantized once and written to its k rows, its k rows of outputs are summed
+// with their weights, and in the gradient the token's row of dout is
+// quantized once and written to k rows.  All of it moves memory: two or three
+// operations a byte.
+#include <hip/hip_runtime.h>
+
+#include "fp8bs_device.h"
+#include "fp8bs_internal.h"
+
+namespace fp8bs {
+namespace {
+
+// ---------------------------------------------------------------------
+// The sort: a stable counting sort by expert.
+//
+// Large batches take two kernels: workgroups count their stretch of the
+// assignments by expert, then each finds the rows before its stretch from all
+// counts (at most kMaxStretches x E numbers, from the caches) and places its
+// own.  Within a stretch the order is kept without atomics: a wave compares
+// its 64 assignments bit by bit (ballots), which gives an assignment's rank
+// among those of its expert, and counts per wave are summed over the waves.
+// ---------------------------------------------------------------------
+constexpr int kPlaceThreads = 1024;
+constexpr int kSteps = 4;                             // assignments of a lane and round
+constexpr int kRound = kPlaceThreads * kSteps;        // of a workgroup and round
+constexpr int kMaxStretches = 256;
+
+// Expert of assignment i among those held here, or -1.
+__device__ __forceinline__ int expert_of(const MoeIds& p, int64_t i) {
+  const int64_t t = i <= 0xffffffffll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(p.k) : i / p.k;
+  const int64_t at = t * p.ldi + (i - t * p.k);
+  const int64_t id = p.wide ? static_cast<const int64_t*>(p.ids)[at] : static_cast<const int32_t*>(p.ids)[at];
+  return id >= p.first && id - p.first < p.E ? static_cast<int>(id - p.first) : -1;
+}
+
+__global__ __launch_bounds__(kPlaceThreads) void moe_count_kernel(MoeIds p, int64_t n, int64_t stretch, int32_t* counts) {
+  __shared__ int count[kMaxExperts];
+  poison_lds<sizeof(count)>(count);
+  for (int e = threadIdx.x; e < p.E; e += kPlaceThreads) count[e] = 0;
+  __syncthreads();
+  const int64_t a = blockIdx.x * stretch, b = a + stretch < n ? a + stretch : n;
+  for (int64_t i = a + threadIdx.x; i < b; i += kPlaceThreads) {
+    const int e = expert_of(p, i);
+    if (e >= 0) atomicAdd(&count[e], 1);   // whole numbers: their order changes nothing
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kPlaceThreads) counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
+}
+
+// Exclusive sum of every thread's v over the workgroup's threads, and the
+// whole sum in `all`.  sums: one number a wave.
+__device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  int s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d);
+    if (lane >= d) s += o;
+  }
+  if (lane == 63) sums[wave] = s;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+  for (int k = 0; k < waves; ++k) {
+    const int x = sums[k];
+    before += k < wave ? x : 0;
+    all += x;
+  }
+  return before + s - v;
+}
+
+// counts: of every stretch, or null with a single stretch (counted here).
+__global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeIds p, int64_t n, int64_t stretch, int stretches,
+                                                                  int bits, const int32_t* __restrict__ counts) {
+  constexpr int kWaves = kPlaceThreads / 64;
+  __shared__ int rows[kWaves][kMaxExperts];   // a wave's counts, then what the waves before it have
+  __shared__ int start[kMaxExperts];          // row of an expert's next assignment
+  __shared__ int sums[kWaves];
+  poison_lds<sizeof(rows)>(rows);
+  poison_lds<sizeof(start)>(start);
+  poison_lds<sizeof(sums)>(sums);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint64_t below = (uint64_t(1) << lane) - 1;
+  const int64_t a = blockIdx.x * stretch, b = a + stretch < n ? a + stretch : n;
+  static_assert(kMaxExperts <= kPlaceThreads, "a thread an expert");
+  int total = 0, before = 0;
+  if (counts != nullptr && tid < p.E) {
+#pragma unroll 8
+    for (int s = 0; s < stretches; ++s) {
+      const int c = counts[static_cast<int64_t>(s) * p.E + tid];
+      total += c;
+      before += s < static_cast<int>(blockIdx.x) ? c : 0;
+    }
+  }
+  int64_t round = a;
+  do {   // once where there is nothing to place: the offsets are still written
+    int e[kSteps], rank[kSteps];
+    for (int x = lane; x < p.E; x += 64) rows[wave][x] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int64_t i = round + (wave * kSteps + s) * 64 + lane;
+      e[s] = i < b ? expert_of(p, i) : -1;
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      uint64_t same = __ballot(e[s] >= 0);
+      for (int bit = 0; bit < bits; ++bit) {
+        const uint64_t ones = __ballot((e[s] >> bit) & 1);
+        same &= (e[s] >> bit) & 1 ? ones : ~ones;
+      }
+      rank[s] = __popcll(same & below);
+      int had = 0;
+      if (e[s] >= 0) had = rows[wave][e[s]];
+      // all lanes have read before the first of each expert writes: LDS
+      // serves a wave's accesses in their order
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (e[s] >= 0 && rank[s] == 0) rows[wave][e[s]] = had + __popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      rank[s] += had;
+    }
+    __syncthreads();
+    int mine = 0;
+    if (tid < p.E) {
+      for (int w = 0; w < kWaves; ++w) {
+        const int c = rows[w][tid];
+        rows[w][tid] = mine;
+        mine += c;
+      }
+    }
+    if (round == a) {
+      if (counts == nullptr) total = mine;   // a single round then (see the launch)
+      int all;
+      const int first = exclusive_sum(tid < p.E ? total : 0, sums, all);
+      if (tid < p.E) start[tid] = first + before;
+      if (blockIdx.x == 0) {
+        if (tid < p.E) p.offsets[tid] = first < p.M ? first : static_cast<int32_t>(p.M);
+        if (tid == 0) p.offsets[p.E] = all < p.M ? all : static_cast<int32_t>(p.M);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int64_t i = round + (wave * kSteps + s) * 64 + lane;
+      if (i >= b) continue;
+      const int at = e[s] >= 0 ? start[e[s]] + rows[wave][e[s]] + rank[s] : -1;
+      p.slot[i] = at < p.M ? at : -1;
+    }
+    __syncthreads();
+    if (tid < p.E) start[tid] += mine;
+    round += kRound;
+  } while (round < b);
+}
+
+// ---------------------------------------------------------------------
+// Rows to their places.  A lane has 16 values: 16-byte stores of codes, a
+// tile is 8 lanes.
+// ---------------------------------------------------------------------
+// Max over 8 lanes (a half of a DPP row) of non-negative floats.
+__device__ __forceinline__ float half8_max(float v) {
+  int x = __float_as_int(v);
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xf, 0xf, false));   // quad_perm [1,0,3,2]
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xf, 0xf, false));   // quad_perm [2,3,0,1]
+  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x141, 0xf, 0xf, false));  // row_half_mirror
+  return __int_as_float(x);
+}
+
+// 16 bf16 values to codes and their tile's scale (all lanes of a tile).
+__device__ __forceinline__ u32x4 quantize16(const u32x4& v0, const u32x4& v1, float& scale) {
+  float a[8], b[8];
+  bf16x8_unpack(v0, a);
+  bf16x8_unpack(v1, b);
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) am = __builtin_fmaxf(am, __builtin_fmaxf(__builtin_fabsf(a[i]), __builtin_fabsf(b[i])));
+  am = half8_max(am);
+  const TileScale t = make_tile_scale(am);
+  const Bf16Side k = bf16_side(t.s, am);
+  scale = t.s;
+  return u32x4{encode4_bf16(a, t, k), encode4_bf16(a + 4, t, k), encode4_bf16(b, t, k), encode4_bf16(b + 4, t, k)};
+}
+
+// 16 values of a row on their way.
+struct Unit {
+  u32x4 x0, x1;   // bf16 values (x0 alone: codes)
+  float s;        // the tile's scale of a row of codes
+};
+
+__device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, int c, Unit& u) {
+  if (p.codes_in) {
+    u.x0 = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c));
+    u.s = p.s_in[t * p.lds_in + (c >> 7)];
+  } else {
+    const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + t * p.ldx + c);
+    u.x0 = __builtin_nontemporal_load(x);
+    u.x1 = __builtin_nontemporal_load(x + 1);
+  }
+}
+
+// A unit to the rows that row(0 .. k - 1) gives.  Called by whole tiles.
+template <class Row>
+__device__ __forceinline__ void store_unit(const MoeRows& p, int c, const Unit& u, Row row_of) {
+  u32x4 code = u.x0;
+  float scale = u.s;
+  if (p.q != nullptr && !p.codes_in) code = quantize16(u.x0, u.x1, scale);
+  for (int j = 0; j < p.k; ++j) {
+    const int64_t row = row_of(j);
+    if (row < 0 || row >= p.M) continue;
+    if (p.q != nullptr) {
+      *reinterpret_cast<u32x4*>(p.q + row * p.ldq + c) = code;
+      if ((threadIdx.x & 7) == 0) p.s[row * p.lds + (c >> 7)] = scale;
+    }
+    if (p.y != nullptr) {
+      u32x4* y = reinterpret_cast<u32x4*>(p.y + row * p.ldy + c);
+      y[0] = u.x0;
+      y[1] = u.x1;
+    }
+  }
+}
+
+// A wave takes 1024 columns of a token.
+__global__ __launch_bounds__(256) void moe_gather_kernel(MoeRows p, int chunks) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = item <= 0xffffffffll ? static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks) : item / chunks;
+  if (t >= p.T) return;
+  const int lane = threadIdx.x & 63;
+  const int c = static_cast<int>(item - t * chunks) * 1024 + lane * 16;
+  const int mine = lane < p.k ? p.slot[t * p.k + lane] : -1;   // lane j holds the token's slot j
+  if (c >= p.C) return;
+  Unit u;
+  load_unit(p, t, c, u);
+  store_unit(p, c, u, [mine](int j) { return __builtin_amdgcn_readlane(mine, j); });
+}
+
+// Few assignments: sort and rows in one launch.  A workgroup a token counts
+// the assignments before each of its own, (e', i') < (e, i), by itself: n
+// comparisons of a wave for an assignment, from the caches.  One more
+// workgroup counts the experts' offsets.
+constexpr int64_t kFew = 2048;
+__device__ __forceinline__ uint32_t order_key(int e, int64_t i) {
+  return e >= 0 ? (static_cast<uint32_t>(e) << 20) | static_cast<uint32_t>(i) : 0xffffffffu;
+}
+static_assert(kMaxExperts <= 2048 && kFew <= (1 << 20), "a key's 32 bits");
+
+__global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
+  __shared__ int32_t slot[kMaxChoices];
+  __shared__ int count[kMaxExperts];
+  __shared__ int sums[16];
+  poison_lds<sizeof(slot)>(slot);
+  poison_lds<sizeof(count)>(count);
+  poison_lds<sizeof(sums)>(sums);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int n = static_cast<int>(ids.T) * ids.k;
+  const int64_t t = blockIdx.x;
+  if (t == ids.T) {
+    for (int e = tid; e < ids.E; e += blockDim.x) count[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += blockDim.x) {
+      const int e = expert_of(ids, i);
+      if (e >= 0) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    int done = 0;
+    for (int e0 = 0; e0 < ids.E; e0 += blockDim.x) {
+      const int e = e0 + tid;
+      int all;
+      const int first = done + exclusive_sum(e < ids.E ? count[e] : 0, sums, all);
+      if (e < ids.E) ids.offsets[e] = first < ids.M ? first : static_cast<int32_t>(ids.M);
+      done += all;
+      __syncthreads();
+    }
+    if (tid == 0) ids.offsets[ids.E] = done < ids.M ? done : static_cast<int32_t>(ids.M);
+    return;
+  }
+  const int c0 = tid * 16;
+  Unit u;
+  if (c0 < p.C) load_unit(p, t, c0, u);
+  for (int j = wave; j < ids.k; j += waves) {
+    const int64_t i = t * ids.k + j;
+    const uint32_t key = order_key(expert_of(ids, i), i);
+    int before = 0;
+    for (int o = 0; o < n; o += 64) {
+      const int other = o + lane;
+      before += __popcll(__ballot(other < n && order_key(expert_of(ids, other < n ? other : 0), other) < key));
+    }
+    const int at = key != 0xffffffffu && before < ids.M ? before : -1;
+    if (lane == 0) {
+      slot[j] = at;
+      ids.slot[i] = at;
+    }
+  }
+  __syncthreads();
+  const auto row_of = [](int j) { return __builtin_amdgcn_readfirstlane(slot[j]); };
+  if (c0 < p.C) store_unit(p, c0, u, row_of);
+  for (int c = c0 + blockDim.x * 16; c < p.C; c += blockDim.x * 16) {
+    load_unit(p, t, c, u);
+    store_unit(p, c, u, row_of);
+  }
+}
+
+// ---------------------------------------------------------------------
+// Rows back: out[t] = add[t] + sum over j of w[t][j] y[slot[t][j]], j
+// ascending, one FMA a row in FP32.  A wave takes 512 columns of a token, with
+// up to kAhead rows' loads in flight.
+// ---------------------------------------------------------------------
+constexpr int kAhead = 8;
+
+template <bool F32>
+struct Values8 {
+  u32x4 a, b;   // b: of FP32 rows
+};
+template <bool F32>
+__device__ __forceinline__ Values8<F32> load8(const void* y, int64_t at) {
+  Values8<F32> v;
+  if (F32) {
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(y) + at);
+    v.a = __builtin_nontemporal_load(p);
+    v.b = __builtin_nontemporal_load(p + 1);
+  } else {
+    v.a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(y) + at));
+  }
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ void values8(const Values8<F32>& v, float (&f)[8]) {
+  if (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = __uint_as_float(v.a[i]);
+      f[4 + i] = __uint_as_float(v.b[i]);
+    }
+  } else {
+    bf16x8_unpack(v.a, f);
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeCombine p, int chunks) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = item <= 0xffffffffll ? static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks) : item / chunks;
+  if (t >= p.T) return;
+  const int lane = threadIdx.x & 63;
+  const int c = static_cast<int>(item - t * chunks) * 512 + lane * 8;
+  // lane j holds the token's slot j and its weight
+  const int mine = lane < p.k ? p.slot[t * p.k + lane] : -1;
+  const float weight = p.w != nullptr && lane < p.k ? p.w[t * p.ldw + lane] : 1.0f;
+  if (c >= p.N) return;
+  float acc[8];
+  u32x4 add{0u, 0u, 0u, 0u};
+  if (p.add != nullptr) add = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.add + t * p.ldadd + c));
+  bf16x8_unpack(add, acc);
+  for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+    Values8<F32> v[kAhead];
+    float w[kAhead];
+    bool there[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int64_t row = j0 + j < p.k ? __builtin_amdgcn_readlane(mine, (j0 + j) & 63) : -1;
+      there[j] = row >= 0 && row < p.M;   // the same in the whole wave
+      w[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), (j0 + j) & 63));
+      if (there[j]) v[j] = load8<F32>(p.y, row * p.ldy + c);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (!there[j]) continue;
+      float f[8];
+      values8<F32>(v[j], f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+    }
+  }
+  *reinterpret_cast<u32x4*>(p.out + t * p.ldo + c) = bf16x8_pack(acc);
+}
+
+// ---------------------------------------------------------------------
+// Gradient of the way back: dy[slot] = w dout[t] as codes (dout's tile is
+// quantized once; a row's scales are those of dout times |w|, its signs those
+// of w dout) and in BF16, dw[t][j] = dout[t] . y[slot].  A workgroup a token,
+// 16 values a lane; every wave has columns in its first turn.
+// ---------------------------------------------------------------------
+template <bool F32>
+__global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) {
+  __shared__ float part[kMaxChoices][16];
+  poison_lds<sizeof(part)>(part);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int64_t t = blockIdx.x;
+  const int32_t* slot = p.slot + t * p.k;
+  const float* weight = p.w + t * p.ldw;
+  for (int c = tid * 16; c - lane * 16 < p.N; c += blockDim.x * 16) {   // whole waves
+    const bool in = c < p.N;
+    const bool opening = c == tid * 16;
+    u32x4 d0{0u, 0u, 0u, 0u}, d1{0u, 0u, 0u, 0u};
+    if (in) {
+      const u32x4* d = reinterpret_cast<const u32x4*>(p.dout + t * p.lddo + c);
+      d0 = __builtin_nontemporal_load(d);
+      d1 = __builtin_nontemporal_load(d + 1);
+    }
+    float a[8], b[8];
+    bf16x8_unpack(d0, a);
+    bf16x8_unpack(d1, b);
+    float scale = 0.0f;
+    u32x4 code{0u, 0u, 0u, 0u};
+    if (p.q != nullptr) code = quantize16(d0, d1, scale);
+    for (int j = 0; j < p.k; ++j) {
+      const int64_t row = slot[j];
+      if (row < 0 || row >= p.M) continue;
+      const float w = weight[j];
+      if (p.dw != nullptr) {
+        float dot = 0.0f;
+        if (in) {
+          float f[8], g[8];
+          values8<F32>(load8<F32>(p.y, row * p.ldy + c), f);
+          values8<F32>(load8<F32>(p.y, row * p.ldy + c + 8), g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(a[i], f[i], dot);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(b[i], g[i], dot);
+        }
+        dot = wave_sum(dot);
+        if (lane == 0) part[j][wave] = opening ? dot : part[j][wave] + dot;
+      }
+      if (!in) continue;
+      if (p.q != nullptr) {
+        const uint32_t turn = w < 0.0f ? 0x80808080u : 0u;
+        *reinterpret_cast<u32x4*>(p.q + row * p.ldq + c) = code ^ u32x4{turn, turn, turn, turn};
+        if ((lane & 7) == 0) p.s[row * p.lds + (c >> 7)] = __builtin_fabsf(w) * scale;
+      }
+      if (p.dy != nullptr) {
+        float f[8], g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = w * a[i];
+          g[i] = w * b[i];
+        }
+        u32x4* y = reinterpret_cast<u32x4*>(p.dy + row * p.lddy + c);
+        y[0] = bf16x8_pack(f);
+        y[1] = bf16x8_pack(g);
+      }
+    }
+  }
+  if (p.dw == nullptr) return;
+  __syncthreads();
+  for (int j = tid; j < p.k; j += blockDim.x) {
+    const int64_t row = slot[j];
+    float s = 0.0f;
+    if (row >= 0 && row < p.M)
+      for (int w = 0; w < waves; ++w) s += part[j][w];
+    p.dw[t * p.lddw + j] = s;
+  }
+}
+
+// Stretches of the sort and their length (whole rounds).
+int64_t stretch_of(int64_t n) {
+  const int64_t rounds = n > 0 ? (n + kRound - 1) / kRound : 1;
+  return (rounds + kMaxStretches - 1) / kMaxStretches * kRound;
+}
+
+}  // namespace
+
+int64_t moe_sort_ws(int64_t T, int k, int E) {
+  const int64_t n = T * k, stretch = stretch_of(n), stretches = (n + stretch - 1) / stretch;
+  return stretches > 1 ? stretches * E * static_cast<int64_t>(sizeof(int32_t)) : 0;
+}
+
+hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st) {
+  const int64_t n = p.T * p.k, stretch = stretch_of(n);
+  const int stretches = n > 0 ? static_cast<int>((n + stretch - 1) / stretch) : 1;
+  int bits = 0;
+  while ((p.E - 1) >> bits) ++bits;
+  int32_t* counts = nullptr;
+  if (stretches > 1) {
+    counts = p.ws;
+    hipLaunchKernelGGL(moe_count_kernel, dim3(stretches), dim3(kPlaceThreads), 0, st, p, n, stretch, counts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(moe_place_kernel, dim3(stretches), dim3(kPlaceThreads), 0, st, p, n, stretch, stretches, bits,
+                     counts);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
+  const int chunks = (p.C + 1023) / 1024;
+  const int64_t blocks = (p.T * chunks + 3) / 4;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(moe_gather_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, chunks);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st) {
+  if (ids.T * ids.k <= kFew) {
+    int waves = (p.C + 1023) / 1024;
+    waves = waves < 4 ? 4 : waves > 16 ? 16 : waves;
+    hipLaunchKernelGGL(moe_few_kernel, dim3(static_cast<unsigned>(ids.T + 1)), dim3(64 * waves), 0, st, ids, p);
+    return hipGetLastError();
+  }
+  const hipError_t e = launch_moe_sort(ids, st);
+  return e != hipSuccess ? e : launch_moe_gather(p, st);
+}
+
+hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st) {
+  const int chunks = (p.N + 511) / 512;
+  const int64_t blocks = (p.T * chunks + 3) / 4;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true>), grid, block, 0, st, p, chunks);
+  else hipLaunchKernelGGL((moe_combine_kernel<false>), grid, block, 0, st, p, chunks);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st) {
+  if (p.T > 0x7fffffff) return hipErrorInvalidValue;
+  int waves = (p.N + 1023) / 1024;
+  waves = waves > 16 ? 16 : waves;
+  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * waves);
+  if (p.y_f32) hipLaunchKernelGGL((moe_combine_bwd_kernel<true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((moe_combine_bwd_kernel<false>), grid, block, 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bs

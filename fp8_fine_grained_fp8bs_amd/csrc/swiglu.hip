@@ -54,6 +54,14 @@ __device__ __forceinline__ float swiglu1(float g, float u) {
   return (g * sig) * u;
 }
 
+// sigma(g) and 1 - sigma(g), both to a few units in the last place.
+__device__ __forceinline__ void sigmoids(float g, float& sig, float& rest) {
+  const float e = exp_neg(__builtin_fabsf(g));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e);
+  sig = g >= 0.0f ? r : e * r;
+  rest = g >= 0.0f ? e * r : r;
+}
+
 template <bool CODES, bool HOUT>
 __global__ __launch_bounds__(256) void swiglu_quant_kernel(const uint16_t* __restrict__ g, int64_t ldg,
                                                            const uint16_t* __restrict__ u, int64_t ldu,
@@ -133,7 +141,69 @@ __global__ __launch_bounds__(256) void swiglu_quant_kernel(const uint16_t* __res
   }
 }
 
+// Gradient: with sigma = sigma(g)
+//   dg = dh u sigma (1 + g (1 - sigma)),   du = dh g sigma
+// in the layout of the up-projection's output, dg's I columns and then du's,
+// as codes with 1x128 scales (the input gradient's operand) and in BF16 (the
+// weight gradient's source), and optionally h again.  A DPP row takes one tile
+// of dh, g and u, 8 values a lane, and gives one tile of dg and one of du.
+__global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
+  const int sub = threadIdx.x & 15;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const int64_t t = tile <= 0xffffffffll ? static_cast<uint32_t>(tile) / static_cast<uint32_t>(G) : tile / G;
+  if (t >= p.T) return;   // whole DPP rows
+  const int c = static_cast<int>(tile - t * G) * 128 + sub * 8;
+  const auto load = [&](const uint16_t* x, int64_t ld) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(x + t * ld + c));
+  };
+  const u32x4 vd = load(p.dh, p.lddh), vg = load(p.g, p.ldg), vu = load(p.u, p.ldu);
+  float d[8], g[8], u[8], h[8];
+  bf16x8_unpack(vd, d);
+  bf16x8_unpack(vg, g);
+  bf16x8_unpack(vu, u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float sig, rest;
+    sigmoids(g[i], sig, rest);
+    const float silu = g[i] * sig;
+    h[i] = silu * u[i];
+    const float slope = __builtin_fmaf(silu, rest, sig);
+    g[i] = (d[i] * u[i]) * slope;
+    u[i] = d[i] * silu;
+  }
+  if (p.q != nullptr) {
+    float ag = 0.0f, au = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ag = __builtin_fmaxf(ag, __builtin_fabsf(g[i]));
+      au = __builtin_fmaxf(au, __builtin_fabsf(u[i]));
+    }
+    const TileScale tg = make_tile_scale(row16_max(ag)), tu = make_tile_scale(row16_max(au));
+    uint8_t* q = p.q + t * p.ldq + c;
+    *reinterpret_cast<uint2*>(q) = make_uint2(encode4(g, tg), encode4(g + 4, tg));
+    *reinterpret_cast<uint2*>(q + p.I) = make_uint2(encode4(u, tu), encode4(u + 4, tu));
+    if (sub == 0) {
+      p.s[t * p.lds + (c >> 7)] = tg.s;
+      p.s[t * p.lds + G + (c >> 7)] = tu.s;
+    }
+  }
+  if (p.d != nullptr) {
+    uint16_t* out = p.d + t * p.ldd + c;
+    *reinterpret_cast<u32x4*>(out) = bf16x8_pack(g);
+    *reinterpret_cast<u32x4*>(out + p.I) = bf16x8_pack(u);
+  }
+  if (p.h != nullptr) *reinterpret_cast<u32x4*>(p.h + t * p.ldh + c) = bf16x8_pack(h);
+}
+
 }  // namespace
+
+hipError_t launch_swiglu_bwd(const SwigluBwd& p, hipStream_t st) {
+  const int G = static_cast<int>(p.I / 128);
+  const int64_t blocks = (p.T * G + 15) / 16;
+  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, G);
+  return hipGetLastError();
+}
 
 hipError_t launch_swiglu_quant_1x128(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,
                                      int64_t T, int64_t I, uint8_t* q, int64_t ldq, float* s,

@@ -37,6 +37,8 @@ SRC_BF16 = 1
 SRC_E5M6 = 2
 ROPE_HALF = 0
 ROPE_INTERLEAVED = 1
+INDEX_I32 = 0
+INDEX_I64 = 1
 
 ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_act_w",
                 "fp8bs_swiglu_quant_1x128",
@@ -47,6 +49,9 @@ ENTRY_POINTS = ("fp8bs_quant_act_1x128", "fp8bs_quant_w_128x128", "fp8bs_quant_a
                 "fp8bs_grouped_gemm",
                 "fp8bs_rope_table", "fp8bs_rope", "fp8bs_kv_append", "fp8bs_attn_paged",
                 "fp8bs_attn_paged_ws",
+                "fp8bs_rmsnorm_quant_1x128", "fp8bs_rmsnorm_bwd", "fp8bs_rmsnorm_bwd_ws",
+                "fp8bs_moe_sort", "fp8bs_moe_sort_ws", "fp8bs_moe_gather", "fp8bs_moe_dispatch",
+                "fp8bs_moe_combine", "fp8bs_moe_combine_bwd", "fp8bs_swiglu_bwd_quant_1x128",
                 "fp8bs_status_string", "fp8bs_version")
 
 _lib = None
@@ -76,7 +81,8 @@ def use_library(path: str) -> str:
     _lib_path, _lib = path, None
     _functions.clear()
     _addresses.clear()
-    _ws_bytes.cache_clear()
+    for sizes in (_ws_bytes, _norm_ws_bytes, _sort_ws_bytes):
+        sizes.cache_clear()
     return prev
 
 
@@ -118,6 +124,15 @@ def load() -> ctypes.CDLL:
                             I64, P, I64, I64, I64, P, P, P, P, I64, P],
         "fp8bs_attn_paged": [P, I64, P, I64, P, I64, P, P, I64, I64, I64, I64, I64, I64, P, I64, I64, I64, P, P,
                              P, P, I64, F, I, I64, P, I64, P],
+        "fp8bs_rmsnorm_quant_1x128": [P, I64, P, I64, P, I, F, I64, I64, P, I64, P, I64, P, I64, P, I64, P, P],
+        "fp8bs_rmsnorm_bwd": [P, I64, P, I64, P, I64, P, I, P, I64, I64, P, I64, P, P, I64, P],
+        "fp8bs_moe_sort": [P, I, I64, I64, I64, I64, I64, I64, P, P, P, I64, P],
+        "fp8bs_moe_gather": [I, P, I64, P, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, I64, P],
+        "fp8bs_moe_dispatch": [I, P, I64, P, I64, I64, I64, P, I, I64, I64, I64, I64, P, P, P, I64, P, I64, P, I64,
+                               I64, P, I64, P],
+        "fp8bs_moe_combine": [P, I, I64, I64, P, P, I64, I64, I64, I64, P, I64, P, I64, P],
+        "fp8bs_moe_combine_bwd": [P, I64, P, I, I64, P, P, I64, I64, I64, I64, P, I64, P, I64, P, I64, I64, P, I64, P],
+        "fp8bs_swiglu_bwd_quant_1x128": [P, I64, P, I64, P, I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -125,6 +140,10 @@ def load() -> ctypes.CDLL:
         fn.restype = ctypes.c_int
     lib.fp8bs_attn_paged_ws.argtypes = [I64] * 8
     lib.fp8bs_attn_paged_ws.restype = I64
+    lib.fp8bs_rmsnorm_bwd_ws.argtypes = [I64] * 2
+    lib.fp8bs_rmsnorm_bwd_ws.restype = I64
+    lib.fp8bs_moe_sort_ws.argtypes = [I64] * 3
+    lib.fp8bs_moe_sort_ws.restype = I64
     lib.fp8bs_status_string.argtypes = [ctypes.c_int]
     lib.fp8bs_status_string.restype = ctypes.c_char_p
     lib.fp8bs_version.argtypes = []
@@ -564,6 +583,219 @@ def fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs, s
           scale, 1 if causal else 0, window, _ptr(ws), ws_bytes, _stream(stream))
 
 
+def _row_ld(t, cols):
+    """Row stride of a checked 2-D tensor, or 0 for None (of a single row any stride will do)."""
+    if t is None:
+        return 0
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _optional(t, what, shape, dtypes):
+    if t is not None:
+        _check(t, what, shape, dtypes)
+
+
+def _dtype(t, what):
+    """OUT_BF16 or OUT_F32 by the tensor's type."""
+    name = _dtype_names[t.dtype]
+    if name not in ("bfloat16", "float32"):
+        raise ValueError(f"{what}: dtype {t.dtype}, expected bfloat16 or float32")
+    return OUT_F32 if name == "float32" else OUT_BF16
+
+
+def _vector(t, what, n, dtypes):
+    if t is None or t.shape != (n,) or _dtype_names[t.dtype] not in dtypes or not t.is_contiguous():
+        got = None if t is None else (t.dtype, tuple(t.shape))
+        raise ValueError(f"{what}: expected {n} contiguous values of {dtypes}, got {got}")
+
+
+def _workspace(ws):
+    """Bytes of a workspace tensor."""
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
+def _check_rows(q, s, y, C, rows=None):
+    """Row outputs (codes with scales, BF16): both of q and s or neither, all with
+    the same number of rows, which is returned (`rows` where there are none)."""
+    if (q is None) != (s is None):
+        raise ValueError("q and s: both or neither")
+    if rows is None:
+        rows = q.shape[0] if q is not None else y.shape[0] if y is not None else 0
+    _optional(q, "q", (rows, C), _CODES)
+    _optional(s, "s", (rows, (">=", _groups(C))), ("float32",))
+    _optional(y, "y", (rows, C), ("bfloat16",))
+    return rows
+
+
+def fp8bs_rmsnorm_quant_1x128(x, r, gamma, eps, h, q, s, y, rstd, stream=None):
+    """x (and r) bf16 [T][C], gamma bf16 or f32 [C] -> h = x + r bf16 [T][C] (with
+    r), its norm as q u8 [T][C] with s f32 [T][C/128] and/or y bf16 [T][C], and
+    rstd f32 [T] (or None)."""
+    _check(x, "x", (None, None), ("bfloat16",))
+    T, C = x.shape
+    if (r is None) != (h is None):
+        raise ValueError("r and h: both or neither")
+    _optional(r, "r", (T, C), ("bfloat16",))
+    _optional(h, "h", (T, C), ("bfloat16",))
+    _vector(gamma, "gamma", C, ("bfloat16", "float32"))
+    if q is None and y is None:
+        raise ValueError("no output")
+    _check_rows(q, s, y, C, T)
+    if rstd is not None:
+        _vector(rstd, "rstd", T, ("float32",))
+    _call("fp8bs_rmsnorm_quant_1x128", _ptr(x), _row_ld(x, C), _ptr(r), _row_ld(r, C), _ptr(gamma),
+          _dtype(gamma, "gamma"), eps, T, C, _ptr(h), _row_ld(h, C), _ptr(q), _row_ld(q, C), _ptr(s),
+          _row_ld(s, _groups(C)), _ptr(y), _row_ld(y, C), _ptr(rstd), _stream(stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_ws_bytes(T, C):
+    return load().fp8bs_rmsnorm_bwd_ws(T, C)
+
+
+def fp8bs_rmsnorm_bwd_ws(T, C):
+    """Bytes of working memory fp8bs_rmsnorm_bwd needs (-1: invalid sizes)."""
+    return _norm_ws_bytes(T, C)
+
+
+def fp8bs_rmsnorm_bwd(dn, dres, h, gamma, rstd, dx, dgamma, ws, stream=None):
+    """Gradient of the norm of h bf16 [T][C]: dn (and dres or None) bf16 [T][C] ->
+    dx bf16 [T][C] and dgamma f32 [C] (or None; with it ws uint8
+    [>= fp8bs_rmsnorm_bwd_ws(T, C)])."""
+    _check(h, "h", (None, None), ("bfloat16",))
+    T, C = h.shape
+    _check(dn, "dn", (T, C), ("bfloat16",))
+    _optional(dres, "dres", (T, C), ("bfloat16",))
+    _check(dx, "dx", (T, C), ("bfloat16",))
+    _vector(gamma, "gamma", C, ("bfloat16", "float32"))
+    _vector(rstd, "rstd", T, ("float32",))
+    if dgamma is not None:
+        _vector(dgamma, "dgamma", C, ("float32",))
+    _call("fp8bs_rmsnorm_bwd", _ptr(dn), _row_ld(dn, C), _ptr(dres), _row_ld(dres, C), _ptr(h), _row_ld(h, C),
+          _ptr(gamma), _dtype(gamma, "gamma"), _ptr(rstd), T, C, _ptr(dx), _row_ld(dx, C), _ptr(dgamma), _ptr(ws),
+          _workspace(ws), _stream(stream))
+
+
+@functools.lru_cache(maxsize=4096)
+def _sort_ws_bytes(T, k, E):
+    return load().fp8bs_moe_sort_ws(T, k, E)
+
+
+def fp8bs_moe_sort_ws(T, k, E):
+    """Bytes of working memory fp8bs_moe_sort and fp8bs_moe_dispatch need (-1: invalid sizes)."""
+    return _sort_ws_bytes(T, k, E)
+
+
+def _check_ids(ids, offsets, slot):
+    """(index type, row stride, T, k, E) of a sort."""
+    if _dtype_names[ids.dtype] not in ("int32", "int64") or ids.dim() != 2:
+        raise ValueError(f"ids: expected int32 or int64 [T][k], got {ids.dtype} {tuple(ids.shape)}")
+    T, k = ids.shape
+    row, one = ids.stride()
+    if one != 1 and k > 1:
+        raise ValueError(f"ids: rows must be contiguous, got strides {(row, one)}")
+    _check(offsets, "offsets", ((">=", 2),), ("int32",), contiguous=True)
+    _check(slot, "slot", (T, k), ("int32",), contiguous=True)
+    return (INDEX_I64 if _dtype_names[ids.dtype] == "int64" else INDEX_I32), _row_ld(ids, k), T, k, offsets.shape[0] - 1
+
+
+def fp8bs_moe_sort(ids, first, M, offsets, slot, ws, stream=None):
+    """ids i32 or i64 [T][k] -> offsets i32 [E+1] and slot i32 [T][k] of the
+    assignments to experts first .. first + E - 1; ws uint8
+    [>= fp8bs_moe_sort_ws(T, k, E)] (or None where that is 0)."""
+    it, ldi, T, k, E = _check_ids(ids, offsets, slot)
+    _call("fp8bs_moe_sort", _ptr(ids), it, ldi, T, k, first, E, M, _ptr(offsets), _ptr(slot), _ptr(ws), _workspace(ws),
+          _stream(stream))
+
+
+def _check_source(src, x, s_in):
+    """(T, C) of rows given as codes with scales or in BF16."""
+    codes = int(src) == SRC_FP8_1x128
+    _check(x, "x", (None, None), _CODES if codes else ("bfloat16",))
+    if codes:
+        _check(s_in, "s_in", (x.shape[0], (">=", _groups(x.shape[1]))), ("float32",))
+    return x.shape
+
+
+def fp8bs_moe_gather(src, x, s_in, slot, q, s, y, stream=None):
+    """Token t's row of x (bf16 [T][C], or codes with s_in f32 [T][C/128]) to the
+    rows slot i32 [T][k] of q u8 [M][C] with s f32 [M][C/128] and/or y bf16 [M][C]."""
+    T, C = _check_source(src, x, s_in)
+    _check(slot, "slot", (T, None), ("int32",), contiguous=True)
+    M = _check_rows(q, s, y, C)
+    _call("fp8bs_moe_gather", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C,
+          _ptr(slot), slot.shape[1], _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)), _ptr(y),
+          _row_ld(y, C), M, _stream(stream))
+
+
+def fp8bs_moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, stream=None):
+    """fp8bs_moe_sort of ids and fp8bs_moe_gather of x in one call."""
+    T, C = _check_source(src, x, s_in)
+    it, ldi, n, k, E = _check_ids(ids, offsets, slot)
+    if n != T:
+        raise ValueError(f"ids: {n} tokens, x has {T}")
+    M = _check_rows(q, s, y, C)
+    _call("fp8bs_moe_dispatch", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C, _ptr(ids),
+          it, ldi, k, first, E, _ptr(offsets), _ptr(slot), _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)),
+          _ptr(y), _row_ld(y, C), M, _ptr(ws), _workspace(ws), _stream(stream))
+
+
+def fp8bs_moe_combine(y, slot, w, add, out, stream=None):
+    """out bf16 [T][N] = add (or None) + the sum of w (or 1) times rows slot
+    i32 [T][k] of y bf16 or f32 [M][N]; w f32 [T][k] or None."""
+    _check(y, "y", (None, None), ("bfloat16", "float32"))
+    M, N = y.shape
+    _check(slot, "slot", (None, None), ("int32",), contiguous=True)
+    T, k = slot.shape
+    _optional(w, "w", (T, k), ("float32",))
+    _optional(add, "add", (T, N), ("bfloat16",))
+    _check(out, "out", (T, N), ("bfloat16",))
+    _call("fp8bs_moe_combine", _ptr(y), _dtype(y, "y"), _row_ld(y, N), M, _ptr(slot), _ptr(w), _row_ld(w, k), T, k, N,
+          _ptr(add), _row_ld(add, N), _ptr(out), _row_ld(out, N), _stream(stream))
+
+
+def fp8bs_moe_combine_bwd(dout, y, slot, w, q, s, dy, dw, stream=None):
+    """Gradient of fp8bs_moe_combine: dout bf16 [T][N], w f32 [T][k] -> rows slot
+    of q u8 [M][N] with s f32 [M][N/128] and/or dy bf16 [M][N], and dw f32 [T][k]
+    (or None; with it y [M][N])."""
+    _check(dout, "dout", (None, None), ("bfloat16",))
+    T, N = dout.shape
+    _check(slot, "slot", (T, None), ("int32",), contiguous=True)
+    k = slot.shape[1]
+    _check(w, "w", (T, k), ("float32",))
+    if dw is not None:
+        _check(dw, "dw", (T, k), ("float32",))
+        _check(y, "y", (None, N), ("bfloat16", "float32"))
+    elif q is None and dy is None:
+        raise ValueError("no output")
+    M = _check_rows(q, s, dy, N, None if q is not None or dy is not None else y.shape[0])
+    if dw is not None and y.shape[0] != M:
+        raise ValueError(f"y: {y.shape[0]} rows, the outputs have {M}")
+    _call("fp8bs_moe_combine_bwd", _ptr(dout), _row_ld(dout, N), _ptr(y), OUT_BF16 if y is None else _dtype(y, "y"),
+          _row_ld(y, N), _ptr(slot), _ptr(w), _row_ld(w, k), T, k, N, _ptr(q), _row_ld(q, N), _ptr(s),
+          _row_ld(s, _groups(N)), _ptr(dy), _row_ld(dy, N), M, _ptr(dw), _row_ld(dw, k), _stream(stream))
+
+
+def fp8bs_swiglu_bwd_quant_1x128(dh, g, u, q, s, d, h, stream=None):
+    """Gradient of h = silu(g) u: dh, g, u bf16 [T][I] -> dg and du side by side as
+    q u8 [T][2I] with s f32 [T][2I/128] and/or d bf16 [T][2I], and h bf16 [T][I] (or None)."""
+    _check(g, "g", (None, None), ("bfloat16",))
+    T, I = g.shape
+    _check(dh, "dh", (T, I), ("bfloat16",))
+    _check(u, "u", (T, I), ("bfloat16",))
+    _check_rows(q, s, d, 2 * I, T)
+    _optional(h, "h", (T, I), ("bfloat16",))
+    if q is None and d is None and h is None:
+        raise ValueError("no output")
+    _call("fp8bs_swiglu_bwd_quant_1x128", _ptr(dh), _row_ld(dh, I), _ptr(g), _row_ld(g, I), _ptr(u), _row_ld(u, I), T, I,
+          _ptr(q), _row_ld(q, 2 * I), _ptr(s), _row_ld(s, _groups(2 * I)), _ptr(d), _row_ld(d, 2 * I), _ptr(h),
+          _row_ld(h, I), _stream(stream))
+
+
 # ---------------------------------------------------------------------------
 # allocating helpers (torch tensors on the current device)
 # ---------------------------------------------------------------------------
@@ -814,3 +1046,128 @@ def attn_paged(q, kc, ks, vc, vs, table, kv_len, q_off=None, max_q=1, scale=None
     fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs,
                      D ** -0.5 if scale is None else scale, causal, window, ws, stream)
     return (out, lse) if with_lse else out
+
+
+def _code_rows(rows, C, device):
+    import torch
+    return (torch.empty((rows, C), dtype=torch.uint8, device=device),
+            torch.empty((rows, _groups(C)), dtype=torch.float32, device=device))
+
+
+def _ws(nbytes, device, stream):
+    """Working memory of the given stream, or None where none is needed."""
+    import torch
+    if nbytes <= 0:
+        return None
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    return _scratch(nbytes, device, stream)
+
+
+def rmsnorm_quant_1x128(x, gamma, residual=None, eps=1e-6, codes=True, with_y=False, with_rstd=False, stream=None):
+    """Root-mean-square norm of x bf16 [T][C] (plus a residual) times gamma:
+    (q, s, h, y, rstd), where codes q and scales s, the sum h, the norm y in
+    BF16 and the row factors rstd are None unless asked for (h: without a
+    residual).  Not recorded by autograd; the gradient is rmsnorm_bwd."""
+    import torch
+    T, C = x.shape
+    q, s = _code_rows(T, C, x.device) if codes else (None, None)
+    h = None if residual is None else torch.empty((T, C), dtype=torch.bfloat16, device=x.device)
+    y = torch.empty((T, C), dtype=torch.bfloat16, device=x.device) if with_y else None
+    rstd = torch.empty((T,), dtype=torch.float32, device=x.device) if with_rstd else None
+    fp8bs_rmsnorm_quant_1x128(x, residual, gamma, eps, h, q, s, y, rstd, stream)
+    return q, s, h, y, rstd
+
+
+def rmsnorm_bwd(dn, h, gamma, rstd, dres=None, with_dgamma=True, stream=None):
+    """Gradient of the norm of h (the x + residual that rmsnorm_quant_1x128
+    gave, or x): (dx, dgamma), dx that of x and of the residual, dgamma f32
+    or None.  dres: the gradient of h's other uses."""
+    import torch
+    T, C = h.shape
+    dx = torch.empty((T, C), dtype=torch.bfloat16, device=h.device)
+    dgamma = torch.empty((C,), dtype=torch.float32, device=h.device) if with_dgamma else None
+    ws = _ws(_norm_ws_bytes(T, C), h.device, stream) if with_dgamma else None
+    fp8bs_rmsnorm_bwd(dn, dres, h, gamma, rstd, dx, dgamma, ws, stream)
+    return dx, dgamma
+
+
+def moe_sort(ids, E, first=0, rows=None, stream=None):
+    """Assignments ids [T][k] (int32 or int64) to experts first .. first + E - 1
+    sorted by expert: (offsets i32 [E+1], slot i32 [T][k]).  rows: how many
+    the sorted arrays will hold (default T k)."""
+    import torch
+    T, k = ids.shape
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=ids.device)
+    slot = torch.empty((T, k), dtype=torch.int32, device=ids.device)
+    fp8bs_moe_sort(ids, first, T * k if rows is None else rows, offsets, slot,
+                   _ws(_sort_ws_bytes(T, k, E), ids.device, stream), stream)
+    return offsets, slot
+
+
+def _row_outputs(out, rows, C, codes, with_y, device):
+    """(q, s, y): those given, or new ones."""
+    import torch
+    if out is not None:
+        return out
+    q, s = _code_rows(rows, C, device) if codes else (None, None)
+    return q, s, torch.empty((rows, C), dtype=torch.bfloat16, device=device) if with_y else None
+
+
+def moe_gather(x, slot, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
+    """Tokens' rows (bf16, or codes x with scales s_in) to their places: (q, s, y)
+    with codes and scales, and BF16 rows where asked for (None otherwise).  out:
+    such a triple to write into; rows that no slot names are not written.  Its
+    gradient is moe_combine without weights."""
+    T, C = x.shape
+    q, s, y = _row_outputs(out, slot.numel() if rows is None else rows, C, codes, with_y, x.device)
+    fp8bs_moe_gather(SRC_BF16 if s_in is None else SRC_FP8_1x128, x, s_in, slot, q, s, y, stream)
+    return q, s, y
+
+
+def moe_dispatch(x, ids, E, first=0, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
+    """moe_sort and moe_gather in one call: (q, s, y, offsets, slot)."""
+    import torch
+    (T, C), k = x.shape, ids.shape[1]
+    q, s, y = _row_outputs(out, T * k if rows is None else rows, C, codes, with_y, x.device)
+    offsets = torch.empty((E + 1,), dtype=torch.int32, device=x.device)
+    slot = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    fp8bs_moe_dispatch(SRC_BF16 if s_in is None else SRC_FP8_1x128, x, s_in, ids, first, offsets, slot, q, s, y,
+                       _ws(_sort_ws_bytes(T, k, E), x.device, stream), stream)
+    return q, s, y, offsets, slot
+
+
+def moe_combine(y, slot, w=None, add=None, stream=None):
+    """Rows of y (bf16 or f32) back to their tokens, weighted by w f32 [T][k] (or
+    summed plainly: the gradient of moe_gather), onto add.  Not recorded by
+    autograd; the gradient is moe_combine_bwd (add's is the output's)."""
+    import torch
+    out = torch.empty((slot.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
+    fp8bs_moe_combine(y, slot, w, add, out, stream)
+    return out
+
+
+def moe_combine_bwd(dout, slot, w, y=None, rows=None, codes=True, with_dy=False, out=None, stream=None):
+    """Gradient of moe_combine: (q, s, dy, dw), the rows' gradient as codes with
+    scales and in BF16 where asked for, and the weights' (with y) or None.  out:
+    (q, s, dy) to write into; rows that no slot names are not written."""
+    import torch
+    if rows is None:
+        rows = slot.numel() if y is None else y.shape[0]
+    q, s, dy = _row_outputs(out, rows, dout.shape[1], codes, with_dy, dout.device)
+    dw = None if y is None else torch.empty(slot.shape, dtype=torch.float32, device=dout.device)
+    fp8bs_moe_combine_bwd(dout, y, slot, w, q, s, dy, dw, stream)
+    return q, s, dy, dw
+
+
+def swiglu_bwd_quant_1x128(dh, g, u, codes=True, with_d=False, with_h=False, stream=None):
+    """Gradient of h = silu(g) u: (q, s, d, h), the gradients of g and u side by
+    side [T][2I] as codes with scales and in BF16, and h itself, where asked for
+    (None otherwise)."""
+    import torch
+    T, I = g.shape
+    q, s = _code_rows(T, 2 * I, g.device) if codes else (None, None)
+    d = torch.empty((T, 2 * I), dtype=torch.bfloat16, device=g.device) if with_d else None
+    h = torch.empty((T, I), dtype=torch.bfloat16, device=g.device) if with_h else None
+    fp8bs_swiglu_bwd_quant_1x128(dh, g, u, q, s, d, h, stream)
+    return q, s, d, h

@@ -466,6 +466,162 @@ fp8bs_status fp8bs_attn_paged(const void *q, int64_t ldq, void *out, int64_t ldo
 int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t Hkv, int64_t D,
                             int64_t max_pages, int64_t page);
 
+/* ------------------------------------------------------------------------
+ * Around the experts' products: the norm that feeds a block, tokens sorted by
+ * expert and brought back, and the gradients of these and of SwiGLU.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Root-mean-square norm with the residual's addition, quantized in 1x128 tiles
+ * for the projections that follow ([p1] para 3: the tile's max-abs taken
+ * online; [p2] para 1 counts the HBM round trip of a separate quantization).
+ *   h = bf16(x + r), or x without r;  rstd = 1 / sqrt(mean over C of h^2 + eps);
+ *   n = h rstd gamma in FP32, of the stored h
+ *   x, r   bf16 [T][ldx], [T][ldr]  r may be NULL
+ *   h      bf16 [T][ldh]            the sum: the new residual stream; given with
+ *                                   r and NULL without; may be x or r itself
+ *                                   (with its row stride), else must not overlap them
+ *   gamma  bf16 or f32 [C] by gt
+ *   q, s   u8 [T][ldq], f32 [T][lds]  codes and scales of n (as
+ *                                   fp8bs_quant_act_1x128 quantizes FP32
+ *                                   values); both or neither
+ *   y      bf16 [T][ldy] or NULL    n rounded to BF16
+ *   rstd   f32 [T] or NULL          for fp8bs_rmsnorm_bwd
+ * At least one of q and y.  T >= 0 (0 is a no-op), C > 0, C % 128 == 0 and
+ * C <= 16384, else FP8BS_ERR_UNSUPPORTED_SHAPE; eps > 0 and finite.  gamma
+ * 16-byte aligned.  Rows whose sum of squares passes FP32's range (values near
+ * 10^19) are outside the contract.
+ */
+fp8bs_status fp8bs_rmsnorm_quant_1x128(const void *x, int64_t ldx, const void *r, int64_t ldr,
+                                       const void *gamma, fp8bs_out_dtype gt, float eps, int64_t T, int64_t C,
+                                       void *h, int64_t ldh, uint8_t *q, int64_t ldq, float *s, int64_t lds,
+                                       void *y, int64_t ldy, float *rstd, void *stream);
+
+/*
+ * Gradient of the norm.  With a = gamma dn and u = h rstd (rstd as the norm
+ * stored it):
+ *   dx = dres + rstd (a - u mean over C of a u)   the gradient of x, and of r
+ *   dgamma = sum over the T rows of dn u
+ *   dn, dres  bf16 [T][lddn], [T][lddr]  gradients of n and (or NULL) of h's
+ *                                        other uses
+ *   h         bf16 [T][ldh]      rstd f32 [T]     gamma as for the norm
+ *   dx        bf16 [T][lddx]     may be h, dn or dres itself (with its row
+ *                                stride), else must not overlap them
+ *   dgamma    f32 [C] or NULL    written, not added to; 16-byte aligned
+ *   ws        device memory of fp8bs_rmsnorm_bwd_ws(T, C) bytes, 16-byte
+ *             aligned; unused (may be NULL) without dgamma
+ * FP32 throughout, sums in a fixed order: equal calls give equal bits.  T >= 0
+ * (0: dgamma is set to zeros); C as for the norm.
+ */
+fp8bs_status fp8bs_rmsnorm_bwd(const void *dn, int64_t lddn, const void *dres, int64_t lddr, const void *h,
+                               int64_t ldh, const void *gamma, fp8bs_out_dtype gt, const float *rstd, int64_t T,
+                               int64_t C, void *dx, int64_t lddx, float *dgamma, void *ws, int64_t ws_bytes,
+                               void *stream);
+/* Bytes of working memory of fp8bs_rmsnorm_bwd with dgamma, or -1 where a size is invalid. */
+int64_t fp8bs_rmsnorm_bwd_ws(int64_t T, int64_t C);
+
+typedef enum { FP8BS_INDEX_I32 = 0, FP8BS_INDEX_I64 = 1 } fp8bs_index_type;
+
+/*
+ * Tokens sorted by expert.  An assignment (t, j) sends token t to expert
+ * ids[t][j]; those to the experts first .. first + E - 1 that are held here,
+ * ordered by expert, then t, then j, are the rows of fp8bs_grouped_gemm's
+ * operand.  Other ids (-1 for padding, experts held elsewhere) have no row.  A
+ * token may name an expert twice: two rows.
+ *   ids      i32 or i64 [T][ldi] by it, k of a token
+ *   offsets  i32 [E+1]     as fp8bs_grouped_gemm takes them: rows of expert
+ *                          first + e are offsets[e] .. offsets[e+1] - 1
+ *   slot     i32 [T][k]    the assignment's row, or -1
+ *   M        rows that the sorted arrays hold; assignments past them have no row
+ *            (slot -1, offsets cut to M).  T k rows hold every case.
+ *   ws       device memory of fp8bs_moe_sort_ws(T, k, E) bytes, 4-byte aligned
+ *            (may be NULL where that is 0)
+ * T >= 0 (0: offsets of zeros), 0 < k <= 64, 0 < E <= 1024, T k <= 2^30,
+ * else FP8BS_ERR_UNSUPPORTED_SHAPE; first >= 0, M >= 0.
+ */
+fp8bs_status fp8bs_moe_sort(const void *ids, fp8bs_index_type it, int64_t ldi, int64_t T, int64_t k, int64_t first,
+                            int64_t E, int64_t M, int32_t *offsets, int32_t *slot, void *ws, int64_t ws_bytes,
+                            void *stream);
+/* Bytes of working memory of fp8bs_moe_sort and fp8bs_moe_dispatch (0 to 2^20), or -1
+ * where a size is invalid. */
+int64_t fp8bs_moe_sort_ws(int64_t T, int64_t k, int64_t E);
+
+/*
+ * Tokens' rows to their places: row slot[t][j] of the outputs is token t's
+ * row of x, quantized (once a token, exactly as fp8bs_quant_act_1x128) or copied.
+ *   src    FP8BS_SRC_BF16: x bf16 [T][ldx], s_in ignored; outputs q with s
+ *          and/or y.  FP8BS_SRC_FP8_1x128: x u8 [T][ldx] codes with s_in f32
+ *          [T][lds_in]; outputs q with s.  Others are refused.
+ *   slot   i32 [T][k] of fp8bs_moe_sort, in device memory and not checked: rows
+ *          outside 0 .. M-1 are never followed
+ *   q, s   u8 [M][ldq], f32 [M][lds]   y bf16 [M][ldy] or NULL
+ * Rows that no slot names are left as they were.  Its gradient is
+ * fp8bs_moe_combine without weights.  T >= 0 (0 is a no-op), 0 < k <= 64, C > 0 and
+ * C % 128 == 0, T and M < 2^31.
+ */
+fp8bs_status fp8bs_moe_gather(fp8bs_requant_src src, const void *x, int64_t ldx, const float *s_in, int64_t lds_in,
+                              int64_t T, int64_t C, const int32_t *slot, int64_t k, uint8_t *q, int64_t ldq,
+                              float *s, int64_t lds, void *y, int64_t ldy, int64_t M, void *stream);
+
+/* fp8bs_moe_sort and fp8bs_moe_gather in one call, with the same results (one
+ * launch for few tokens). */
+fp8bs_status fp8bs_moe_dispatch(fp8bs_requant_src src, const void *x, int64_t ldx, const float *s_in,
+                                int64_t lds_in, int64_t T, int64_t C, const void *ids, fp8bs_index_type it,
+                                int64_t ldi, int64_t k, int64_t first, int64_t E, int32_t *offsets, int32_t *slot,
+                                uint8_t *q, int64_t ldq, float *s, int64_t lds, void *y, int64_t ldy, int64_t M,
+                                void *ws, int64_t ws_bytes, void *stream);
+
+/*
+ * Rows back to their tokens: out[t] = add[t] + sum over j of w[t][j]
+ * y[slot[t][j]], summed in FP32 in the order of j (one FMA a row), rounded once.
+ *   y     bf16 or f32 [M][ldy] by yt   the experts' outputs
+ *   slot  i32 [T][k]                   as for fp8bs_moe_gather; assignments
+ *                                      without a row add nothing, whatever
+ *                                      their weight is
+ *   w     f32 [T][ldw] or NULL         NULL: 1 (the gradient of fp8bs_moe_gather)
+ *   add   bf16 [T][ldadd] or NULL      may be out itself (with its row stride)
+ *   out   bf16 [T][ldo]                must not overlap y
+ * T >= 0 (0 is a no-op), 0 < k <= 64, N > 0 and N % 128 == 0, T and M < 2^31.
+ */
+fp8bs_status fp8bs_moe_combine(const void *y, fp8bs_out_dtype yt, int64_t ldy, int64_t M, const int32_t *slot,
+                               const float *w, int64_t ldw, int64_t T, int64_t k, int64_t N, const void *add,
+                               int64_t ldadd, void *out, int64_t ldo, void *stream);
+
+/*
+ * Gradient of fp8bs_moe_combine with weights (add's is dout itself):
+ *   dy[slot[t][j]] = w[t][j] dout[t]      dw[t][j] = dout[t] . y[slot[t][j]]
+ *   dout  bf16 [T][lddo]
+ *   q, s  u8 [M][ldq], f32 [M][lds]  dy for the input gradient's product:
+ *         dout's row quantized as fp8bs_quant_act_1x128 does, its scales times
+ *         |w| (one FP32 product) and its signs turned where w < 0; both or neither
+ *   dy    bf16 [M][lddy] or NULL     w dout, rounded once
+ *   dw    f32 [T][lddw] or NULL      FP32 sums in a fixed order; 0 without a row
+ *   y     bf16 or f32 [M][ldy] by yt; ignored (may be NULL) without dw
+ * At least one output.  Rows that no slot names are left as they were.  Sizes as for
+ * fp8bs_moe_combine.
+ */
+fp8bs_status fp8bs_moe_combine_bwd(const void *dout, int64_t lddo, const void *y, fp8bs_out_dtype yt, int64_t ldy,
+                                   const int32_t *slot, const float *w, int64_t ldw, int64_t T, int64_t k,
+                                   int64_t N, uint8_t *q, int64_t ldq, float *s, int64_t lds, void *dy,
+                                   int64_t lddy, int64_t M, float *dw, int64_t lddw, void *stream);
+
+/*
+ * Gradient of SwiGLU from the cached halves ([p1] para 4), quantized for the
+ * input gradient of the up-projection:
+ *   dg = dh u sigma (1 + g (1 - sigma)),  du = dh g sigma,  sigma = 1 / (1 + e^-g),
+ *   in FP32
+ *   dh, g, u  bf16 [T][lddh], [T][ldg], [T][ldu]   (g and u as for fp8bs_swiglu_quant_1x128)
+ *   q, s  u8 [T][ldq], f32 [T][lds]  codes and scales of the 2 I columns dg, du
+ *         (the layout of a [T][2I] up-projection output); both or neither
+ *   d     bf16 [T][ldd] or NULL      the same 2 I columns in BF16
+ *   h     bf16 [T][ldh] or NULL      silu(g) u in BF16, as fp8bs_swiglu_quant_1x128 gives it
+ * At least one output, none overlapping an input.  T >= 0 (0 is a no-op), I > 0 and
+ * I % 128 == 0.  NaN and infinite inputs are outside the contract.
+ */
+fp8bs_status fp8bs_swiglu_bwd_quant_1x128(const void *dh, int64_t lddh, const void *g, int64_t ldg, const void *u,
+                                          int64_t ldu, int64_t T, int64_t I, uint8_t *q, int64_t ldq, float *s,
+                                          int64_t lds, void *d, int64_t ldd, void *h, int64_t ldh, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *fp8bs_status_string(fp8bs_status st);
 

@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8bs.so")
-# the Python binding's short way into the attention operators (host code)
+# the Python binding's short way into the operators of small calls (host code)
 MARSHAL = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 # debug build for race checks: kernels fill their LDS with 0xFF before use
 POISON_LIB = os.path.join(PKG, "libfp8bs_poison.so")
@@ -111,7 +111,7 @@ def build(verbose: bool = False) -> str:
     except Exception as e:
         if os.path.exists(MARSHAL):
             os.remove(MARSHAL)
-        warnings.warn(f"no {os.path.basename(MARSHAL)}, the attention helpers go through ctypes: {e}")
+        warnings.warn(f"no {os.path.basename(MARSHAL)}, the short helpers go through ctypes: {e}")
     if verbose:
         print("built", ", ".join(built))
     return LIB

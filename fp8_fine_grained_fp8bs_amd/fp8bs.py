@@ -18,7 +18,7 @@ import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libfp8bs.so")
-# the compiled short way into the attention operators, of this Python
+# the compiled short way into the operators of small calls, of this Python
 MARSHAL_PATH = os.path.join(PKG, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 
 OK = 0
@@ -58,7 +58,7 @@ _lib = None
 _lib_path = LIB_PATH
 _functions = {}      # the loaded library's entry points by name
 _addresses = {}      # and their addresses
-_marshal = None      # the compiled short way into the attention operators
+_marshal = None      # the compiled short way into the operators of small calls
 
 
 class _Names(dict):
@@ -408,15 +408,17 @@ def _load_marshal():
         from . import _marshal as module
         if module.torch_version != torch.__version__:
             raise ImportError(f"built for torch {module.torch_version}, this is {torch.__version__}")
-        return {"fp8bs_" + f: getattr(module, f) for f in ("rope", "kv_append", "attn_paged")}
+        return {"fp8bs_" + f: getattr(module, f) for f in (
+            "rope", "kv_append", "attn_paged", "rmsnorm_quant_1x128", "rmsnorm_bwd", "moe_dispatch", "moe_combine",
+            "moe_combine_bwd", "swiglu_bwd_quant_1x128")}
     except (ImportError, AttributeError) as e:
         import warnings
-        warnings.warn(f"{MARSHAL_PATH}: {e}; the attention helpers go through ctypes")
+        warnings.warn(f"{MARSHAL_PATH}: {e}; the short helpers go through ctypes")
         return {}
 
 
 def _short(name, *args):
-    """The named attention operator by the compiled short way (csrc/marshal.cpp): its
+    """The named operator by the compiled short way (csrc/marshal.cpp): its
     result, or None where an argument is not as it should be (the checks below then
     say which) or there is no short way (the library is then called through ctypes)."""
     global _marshal
@@ -1069,6 +1071,10 @@ def rmsnorm_quant_1x128(x, gamma, residual=None, eps=1e-6, codes=True, with_y=Fa
     (q, s, h, y, rstd), where codes q and scales s, the sum h, the norm y in
     BF16 and the row factors rstd are None unless asked for (h: without a
     residual).  Not recorded by autograd; the gradient is rmsnorm_bwd."""
+    outputs = _short("fp8bs_rmsnorm_quant_1x128", x, gamma, residual, eps, bool(codes), bool(with_y), bool(with_rstd),
+                     _current_stream) if stream is None else None
+    if outputs is not None:
+        return outputs
     import torch
     T, C = x.shape
     q, s = _code_rows(T, C, x.device) if codes else (None, None)
@@ -1083,6 +1089,10 @@ def rmsnorm_bwd(dn, h, gamma, rstd, dres=None, with_dgamma=True, stream=None):
     """Gradient of the norm of h (the x + residual that rmsnorm_quant_1x128
     gave, or x): (dx, dgamma), dx that of x and of the residual, dgamma f32
     or None.  dres: the gradient of h's other uses."""
+    outputs = _short("fp8bs_rmsnorm_bwd", _address("fp8bs_rmsnorm_bwd_ws"), dn, h, gamma, rstd, dres, bool(with_dgamma),
+                     _current_stream) if stream is None else None
+    if outputs is not None:
+        return outputs
     import torch
     T, C = h.shape
     dx = torch.empty((T, C), dtype=torch.bfloat16, device=h.device)
@@ -1127,6 +1137,10 @@ def moe_gather(x, slot, s_in=None, rows=None, codes=True, with_y=False, out=None
 
 def moe_dispatch(x, ids, E, first=0, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
     """moe_sort and moe_gather in one call: (q, s, y, offsets, slot)."""
+    outputs = _short("fp8bs_moe_dispatch", _address("fp8bs_moe_sort_ws"), x, s_in, ids, E, first, rows, bool(codes),
+                     bool(with_y), out, _current_stream) if stream is None else None
+    if outputs is not None:
+        return outputs
     import torch
     (T, C), k = x.shape, ids.shape[1]
     q, s, y = _row_outputs(out, T * k if rows is None else rows, C, codes, with_y, x.device)
@@ -1141,6 +1155,9 @@ def moe_combine(y, slot, w=None, add=None, stream=None):
     """Rows of y (bf16 or f32) back to their tokens, weighted by w f32 [T][k] (or
     summed plainly: the gradient of moe_gather), onto add.  Not recorded by
     autograd; the gradient is moe_combine_bwd (add's is the output's)."""
+    out = _short("fp8bs_moe_combine", y, slot, w, add, _current_stream) if stream is None else None
+    if out is not None:
+        return out
     import torch
     out = torch.empty((slot.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
     fp8bs_moe_combine(y, slot, w, add, out, stream)
@@ -1151,6 +1168,10 @@ def moe_combine_bwd(dout, slot, w, y=None, rows=None, codes=True, with_dy=False,
     """Gradient of moe_combine: (q, s, dy, dw), the rows' gradient as codes with
     scales and in BF16 where asked for, and the weights' (with y) or None.  out:
     (q, s, dy) to write into; rows that no slot names are not written."""
+    outputs = _short("fp8bs_moe_combine_bwd", dout, slot, w, y, rows, bool(codes), bool(with_dy), out,
+                     _current_stream) if stream is None else None
+    if outputs is not None:
+        return outputs
     import torch
     if rows is None:
         rows = slot.numel() if y is None else y.shape[0]
@@ -1164,6 +1185,10 @@ def swiglu_bwd_quant_1x128(dh, g, u, codes=True, with_d=False, with_h=False, str
     """Gradient of h = silu(g) u: (q, s, d, h), the gradients of g and u side by
     side [T][2I] as codes with scales and in BF16, and h itself, where asked for
     (None otherwise)."""
+    outputs = _short("fp8bs_swiglu_bwd_quant_1x128", dh, g, u, bool(codes), bool(with_d), bool(with_h),
+                     _current_stream) if stream is None else None
+    if outputs is not None:
+        return outputs
     import torch
     T, I = g.shape
     q, s = _code_rows(T, 2 * I, g.device) if codes else (None, None)

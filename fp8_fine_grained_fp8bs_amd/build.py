@@ -83,7 +83,7 @@ def _build_marshal():
     for d in include:
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL + ".tmp", "-L" + cpp_extension.TORCH_LIB_PATH,
-            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for marshal.cpp:\n" + r.stderr)

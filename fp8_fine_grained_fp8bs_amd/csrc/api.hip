@@ -743,12 +743,12 @@ fp8bs_status fp8bs_rmsnorm_bwd(const void* dn, int64_t lddn, const void* dres, i
     FP8BS_TRY(check_matrix(h, C, ldh, 2));
     FP8BS_TRY(check_matrix(dx, C, lddx, 2));
     FP8BS_TRY(check_gamma(gamma, gt));
-    FP8BS_TRY(check_in_place(dx, lddx, dn, lddn));
     FP8BS_TRY(check_in_place(dx, lddx, dres, lddr));
-    FP8BS_TRY(check_in_place(dx, lddx, h, ldh));
+    if (dx == dn || dx == h) return FP8BS_ERR_INVALID_ARG;   // other workgroups may read them for dgamma
     if (rstd == nullptr) return FP8BS_ERR_INVALID_ARG;
     if (!aligned(rstd, 4)) return FP8BS_ERR_MISALIGNED;
-    if (dgamma != nullptr && (ws == nullptr || ws_bytes < fp8bs_rmsnorm_bwd_ws(T, C))) return FP8BS_ERR_INVALID_ARG;
+    const int64_t need = dgamma != nullptr ? fp8bs_rmsnorm_bwd_ws(T, C) : 0;
+    if (ws_bytes < need || (need > 0 && ws == nullptr)) return FP8BS_ERR_INVALID_ARG;
   }
   FP8BS_TRY(check_device());
   fp8bs::RmsNormBwd p;

@@ -14,6 +14,7 @@
 #include <initializer_list>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -261,7 +262,7 @@ fp8bs_out_dtype type_of(bool f32) { return f32 ? FP8BS_OUT_F32 : FP8BS_OUT_BF16;
 struct Fresh {
   at::Tensor t;
   Fresh(const at::Tensor* x, bool wanted, at::ScalarType type, at::IntArrayRef size) {
-    if (wanted) t = at::empty(size, x->options().dtype(type));
+    if (wanted) t = at::Tensor(at::detail::empty_cuda(size, type, x->device(), std::nullopt));
   }
   template <class T>
   T* data() const {

@@ -505,11 +505,12 @@ fp8bs_status fp8bs_rmsnorm_quant_1x128(const void *x, int64_t ldx, const void *r
  *   dn, dres  bf16 [T][lddn], [T][lddr]  gradients of n and (or NULL) of h's
  *                                        other uses
  *   h         bf16 [T][ldh]      rstd f32 [T]     gamma as for the norm
- *   dx        bf16 [T][lddx]     may be h, dn or dres itself (with its row
- *                                stride), else must not overlap them
+ *   dx        bf16 [T][lddx]     may be dres itself (with its row stride), else must
+ *                                not overlap the inputs
  *   dgamma    f32 [C] or NULL    written, not added to; 16-byte aligned
  *   ws        device memory of fp8bs_rmsnorm_bwd_ws(T, C) bytes, 16-byte
- *             aligned; unused (may be NULL) without dgamma
+ *             aligned (may be NULL where that is 0, and without dgamma); its contents
+ *             need no preparation
  * FP32 throughout, sums in a fixed order: equal calls give equal bits.  T >= 0
  * (0: dgamma is set to zeros); C as for the norm.
  */
@@ -517,7 +518,8 @@ fp8bs_status fp8bs_rmsnorm_bwd(const void *dn, int64_t lddn, const void *dres, i
                                int64_t ldh, const void *gamma, fp8bs_out_dtype gt, const float *rstd, int64_t T,
                                int64_t C, void *dx, int64_t lddx, float *dgamma, void *ws, int64_t ws_bytes,
                                void *stream);
-/* Bytes of working memory of fp8bs_rmsnorm_bwd with dgamma, or -1 where a size is invalid. */
+/* Bytes of working memory of fp8bs_rmsnorm_bwd with dgamma (0 for few rows, up to 2^24), or
+ * -1 where a size is invalid. */
 int64_t fp8bs_rmsnorm_bwd_ws(int64_t T, int64_t C);
 
 typedef enum { FP8BS_INDEX_I32 = 0, FP8BS_INDEX_I64 = 1 } fp8bs_index_type;

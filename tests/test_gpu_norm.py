@@ -8,8 +8,9 @@ Allowances, with U = 2^-24 and V <= 2 vectors of 8 values a lane:
 - n: two products more: 26 U |n|.
 - dx: a = gamma dn and u = h rstd carry U each, so the sum of a u carries
   (37 + 3) U of sum |a u| and the mean 2 U more; then two fused steps.
-- dgamma: a worker's chain of ceil(T / 512) rows, its parts' chains of 16 and 32,
-  u's rounding: all U of sum |dn u|.
+- dgamma: chains of rows, of workers' parts and of groups, none longer than 512 in
+  all here (T / 256 rows of a worker, 4096 / 128 parts, 16 + 8 groups; or 512 / 8
+  rows and 128 groups), u's rounding 2 more: all U of sum |dn u|.
 """
 import math
 
@@ -137,7 +138,8 @@ def bwd_want(dn, dres, h, gamma, rstd):
     return dx, (dn * u).sum(dim=0), err, (dn * u).abs().sum(dim=0)
 
 
-BWD = [(1, 128, False, "bf16"), (3, 384, True, "f32"), (131, 1280, False, "bf16"), (700, 512, True, "bf16"),
+BWD = [(1, 128, False, "bf16"), (511, 128, True, "bf16"), (512, 7168, True, "f32"), (513, 384, False, "f32"),
+       (9000, 128, False, "bf16"), (3, 384, True, "f32"), (131, 1280, False, "bf16"), (700, 512, True, "bf16"),
        (5000, 256, True, "f32"), (513, 7168, True, "f32"), (1537, 640, False, "bf16"), (8, 8192, True, "bf16"),
        (600, 8320, True, "f32"), (3, 16384, False, "bf16")]
 
@@ -152,15 +154,21 @@ def test_gradient(T, C, dres, kind):
     dx, dgamma = fp8bs.rmsnorm_bwd(pad(dn, 8), pad(h, 16), gamma.cuda(), rstd.cuda(), pad(dr, 24) if dres else None)
     want, want_g, err, size = bwd_want(dn, dr, h, gamma, rstd)
     check_bf16("dx", dx, want, err)
-    chain = math.ceil(T / 512) + 16 + 32 + 3
-    check_f32("dgamma", dgamma, want_g, chain * U * size)
-    # without dgamma, in place of each input, and twice: the same bits
+    few = T <= 512
+    chain = math.ceil(T / 8) + 128 if few else math.ceil(T / 256) + 32 + 24
+    check_f32("dgamma", dgamma, want_g, (chain + 3) * U * size)
+    # twice, without dgamma, and in place of dres: the same bits
     again = fp8bs.rmsnorm_bwd(dn.cuda(), h.cuda(), gamma.cuda(), rstd.cuda(), dr.cuda() if dres else None)
     assert torch.equal(again[0], dx) and torch.equal(again[1], dgamma)
-    for place in ("dn", "h") + (("dres",) if dres else ()):
-        t = {"dn": dn.cuda(), "h": h.cuda(), "dres": dr.cuda() if dres else None}
-        fp8bs.fp8bs_rmsnorm_bwd(t["dn"], t["dres"], t["h"], gamma.cuda(), rstd.cuda(), t[place], None, None)
-        assert torch.equal(t[place], dx), place
+    alone = fp8bs.rmsnorm_bwd(dn.cuda(), h.cuda(), gamma.cuda(), rstd.cuda(), dr.cuda() if dres else None,
+                              with_dgamma=False)
+    assert torch.equal(alone[0], dx) and alone[1] is None
+    if dres:
+        place = dr.cuda()
+        ws = torch.empty((max(1, fp8bs.fp8bs_rmsnorm_bwd_ws(T, C)),), dtype=torch.uint8, device="cuda")
+        g = torch.empty((C,), device="cuda")
+        fp8bs.fp8bs_rmsnorm_bwd(dn.cuda(), place, h.cuda(), gamma.cuda(), rstd.cuda(), place, g, ws)
+        assert torch.equal(place, dx) and torch.equal(g, dgamma)
 
 
 def test_gradient_of_nothing():

@@ -66,10 +66,10 @@ REFUSALS = [
     (norm, dict(h=A, ldh=264), INVALID), (norm, dict(h=2 * A, ldh=264), INVALID),
     (norm_bwd, dict(T=-1), INVALID), (norm_bwd, dict(C=100), SHAPE), (norm_bwd, dict(gt=-1), INVALID),
     (norm_bwd, dict(dn=NULL), INVALID), (norm_bwd, dict(h=NULL), INVALID), (norm_bwd, dict(rstd=NULL), INVALID),
-    (norm_bwd, dict(dx=NULL), INVALID), (norm_bwd, dict(ws=NULL), INVALID), (norm_bwd, dict(ws_bytes=4095), INVALID),
+    (norm_bwd, dict(dx=NULL), INVALID), (norm_bwd, dict(T=600, ws=NULL), INVALID), (norm_bwd, dict(T=600, ws_bytes=256 * 1024 - 1), INVALID),
     (norm_bwd, dict(ws=A + 8), MISALIGNED), (norm_bwd, dict(dgamma=A + 4), MISALIGNED),
-    (norm_bwd, dict(dx=A, lddx=264), INVALID), (norm_bwd, dict(dx=2 * A, lddx=264), INVALID),
-    (norm_bwd, dict(dx=3 * A, lddx=264), INVALID), (norm_bwd, dict(lddr=128), INVALID),
+    (norm_bwd, dict(dx=A), INVALID), (norm_bwd, dict(dx=3 * A), INVALID),
+    (norm_bwd, dict(dx=2 * A, lddx=264), INVALID), (norm_bwd, dict(lddr=128), INVALID),
     (sort, dict(it=2), INVALID), (sort, dict(T=-1), INVALID), (sort, dict(k=0), INVALID), (sort, dict(k=65, ldi=65), SHAPE),
     (sort, dict(E=0), INVALID), (sort, dict(E=1025), SHAPE), (sort, dict(first=-1), INVALID), (sort, dict(M=-1), INVALID),
     (sort, dict(M=1 << 31), SHAPE), (sort, dict(T=(1 << 30) // 8 + 1), SHAPE), (sort, dict(ldi=7), INVALID),
@@ -132,7 +132,9 @@ def test_working_memory():
     assert fp8bs.fp8bs_moe_sort_ws(0, 8, 16) == 0
     for bad in ((-1, 8, 16), (4, 0, 16), (4, 65, 16), (4, 8, 0), (4, 8, 1025), (1 << 28, 8, 16)):
         assert fp8bs.fp8bs_moe_sort_ws(*bad) == -1
-    assert fp8bs.fp8bs_rmsnorm_bwd_ws(3, 256) == 3 * 256 * 4
+    assert fp8bs.fp8bs_rmsnorm_bwd_ws(512, 256) == 0
+    assert fp8bs.fp8bs_rmsnorm_bwd_ws(600, 256) == 256 * 256 * 4
+    assert all(0 < fp8bs.fp8bs_rmsnorm_bwd_ws(1 << 30, 128 * g) < 1 << 25 for g in range(1, 129))
     assert fp8bs.fp8bs_rmsnorm_bwd_ws(0, 256) == 0
     for bad in ((-1, 256), (4, 0), (4, 100), (4, 16512), (1 << 31, 256)):
         assert fp8bs.fp8bs_rmsnorm_bwd_ws(*bad) == -1

@@ -190,6 +190,20 @@ __device__ __forceinline__ u32x4 quantize16(const u32x4& v0, const u32x4& v1, fl
   return u32x4{encode4_bf16(a, t, k), encode4_bf16(a + 4, t, k), encode4_bf16(b, t, k), encode4_bf16(b + 4, t, k)};
 }
 
+// 8 bf16 values to codes and their tile's scale (all 16 lanes of a tile).
+__device__ __forceinline__ uint2 quantize8(const u32x4& v, float& scale) {
+  float a[8];
+  bf16x8_unpack(v, a);
+  float am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) am = __builtin_fmaxf(am, __builtin_fabsf(a[i]));
+  am = row16_max(am);
+  const TileScale t = make_tile_scale(am);
+  const Bf16Side k = bf16_side(t.s, am);
+  scale = t.s;
+  return make_uint2(encode4_bf16(a, t, k), encode4_bf16(a + 4, t, k));
+}
+
 // 16 values of a row on their way.
 struct Unit {
   u32x4 x0, x1;   // bf16 values (x0 alone: codes)
@@ -236,6 +250,7 @@ __global__ __launch_bounds__(256) void moe_gather_kernel(MoeRows p, int chunks) 
   const int lane = threadIdx.x & 63;
   const int c = static_cast<int>(item - t * chunks) * 1024 + lane * 16;
   const int mine = lane < p.k ? p.slot[t * p.k + lane] : -1;   // lane j holds the token's slot j
+  if (__ballot(mine >= 0 && mine < p.M) == 0) return;          // no row: x is not read
   if (c >= p.C) return;
   Unit u;
   load_unit(p, t, c, u);
@@ -310,8 +325,8 @@ __global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
 
 // ---------------------------------------------------------------------
 // Rows back: out[t] = add[t] + sum over j of w[t][j] y[slot[t][j]], j
-// ascending, one FMA a row in FP32.  A wave takes 512 columns of a token, with
-// up to kAhead rows' loads in flight.
+// ascending, one FMA a row in FP32.  A wave takes 1024 columns of a token, two
+// vectors of 8 a lane, with up to kAhead rows' loads in flight.
 // ---------------------------------------------------------------------
 constexpr int kAhead = 8;
 
@@ -344,116 +359,166 @@ __device__ __forceinline__ void values8(const Values8<F32>& v, float (&f)[8]) {
   }
 }
 
+// A lane's two vectors of a row, 512 columns apart.  A lane behind the row's
+// end reads the row's first columns and leaves its outputs alone.
+struct Columns {
+  int c0, N;
+  __device__ __forceinline__ int at(int v) const { return c0 + v * 512; }
+  __device__ __forceinline__ bool in(int v) const { return at(v) < N; }
+  __device__ __forceinline__ int from(int v) const { return in(v) ? at(v) : c0 & 127; }
+};
+
+// A token's slots and weights, one a lane.
+struct Choices {
+  int slot;
+  float weight;
+  int64_t M;
+  __device__ __forceinline__ Choices(const int32_t* s, const float* w, int k, int64_t M, int lane)
+      : slot(lane < k ? s[lane] : -1), weight(w != nullptr && lane < k ? w[lane] : 1.0f), M(M) {}
+  // assignment j (any number: -1 behind the last), the same in the whole wave
+  __device__ __forceinline__ int64_t row(int j) const { return j < 64 ? __builtin_amdgcn_readlane(slot, j) : -1; }
+  __device__ __forceinline__ bool there(int64_t row) const { return row >= 0 && row < M; }
+  __device__ __forceinline__ float w(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j & 63));
+  }
+};
+
 template <bool F32>
-__global__ __launch_bounds__(256) void moe_combine_kernel(MoeCombine p, int chunks) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chunks) {
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 2 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = item <= 0xffffffffll ? static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks) : item / chunks;
   if (t >= p.T) return;
   const int lane = threadIdx.x & 63;
-  const int c = static_cast<int>(item - t * chunks) * 512 + lane * 8;
-  // lane j holds the token's slot j and its weight
-  const int mine = lane < p.k ? p.slot[t * p.k + lane] : -1;
-  const float weight = p.w != nullptr && lane < p.k ? p.w[t * p.ldw + lane] : 1.0f;
-  if (c >= p.N) return;
-  float acc[8];
-  u32x4 add{0u, 0u, 0u, 0u};
-  if (p.add != nullptr) add = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.add + t * p.ldadd + c));
-  bf16x8_unpack(add, acc);
+  const Columns c{static_cast<int>(item - t * chunks) * 1024 + lane * 8, p.N};
+  const Choices chosen(p.slot + t * p.k, p.w != nullptr ? p.w + t * p.ldw : nullptr, p.k, p.M, lane);
+  float acc[2][8];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    u32x4 add{0u, 0u, 0u, 0u};
+    if (p.add != nullptr) add = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.add + t * p.ldadd + c.from(v)));
+    bf16x8_unpack(add, acc[v]);
+  }
   for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-    Values8<F32> v[kAhead];
-    float w[kAhead];
+    Values8<F32> x[kAhead][2];
     bool there[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      const int64_t row = j0 + j < p.k ? __builtin_amdgcn_readlane(mine, (j0 + j) & 63) : -1;
-      there[j] = row >= 0 && row < p.M;   // the same in the whole wave
-      w[j] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), (j0 + j) & 63));
-      if (there[j]) v[j] = load8<F32>(p.y, row * p.ldy + c);
+      const int64_t row = chosen.row(j0 + j);
+      there[j] = chosen.there(row);
+      if (!there[j]) continue;
+#pragma unroll
+      for (int v = 0; v < 2; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (!there[j]) continue;
-      float f[8];
-      values8<F32>(v[j], f);
+      const float w = chosen.w(j0 + j);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w[j], f[i], acc[i]);
+      for (int v = 0; v < 2; ++v) {
+        float f[8];
+        values8<F32>(x[j][v], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[v][i] = __builtin_fmaf(w, f[i], acc[v][i]);
+      }
     }
   }
-  *reinterpret_cast<u32x4*>(p.out + t * p.ldo + c) = bf16x8_pack(acc);
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    if (!c.in(v)) continue;
+    u32x4* out = reinterpret_cast<u32x4*>(p.out + t * p.ldo + c.at(v));
+    const u32x4 x = bf16x8_pack(acc[v]);
+    // beside rows of FP32 the output is better kept out of their way in the
+    // caches (2048 x 8 rows of 7168: 91 us against 100); beside BF16 rows it
+    // makes no difference or costs 2% (8192 x 2: 75.1 against 73.4)
+    if (F32) __builtin_nontemporal_store(x, out);
+    else *out = x;
+  }
 }
 
 // ---------------------------------------------------------------------
 // Gradient of the way back: dy[slot] = w dout[t] as codes (dout's tile is
 // quantized once; a row's scales are those of dout times |w|, its signs those
 // of w dout) and in BF16, dw[t][j] = dout[t] . y[slot].  A workgroup a token,
-// 16 values a lane; every wave has columns in its first turn.
+// a wave 1024 columns at a time, with up to kAheadBwd rows' loads in flight;
+// every wave has columns in its first turn.
 // ---------------------------------------------------------------------
+constexpr int kAheadBwd = 4;
+
 template <bool F32>
 __global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) {
   __shared__ float part[kMaxChoices][16];
   poison_lds<sizeof(part)>(part);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int64_t t = blockIdx.x;
-  const int32_t* slot = p.slot + t * p.k;
-  const float* weight = p.w + t * p.ldw;
-  for (int c = tid * 16; c - lane * 16 < p.N; c += blockDim.x * 16) {   // whole waves
-    const bool in = c < p.N;
-    const bool opening = c == tid * 16;
-    u32x4 d0{0u, 0u, 0u, 0u}, d1{0u, 0u, 0u, 0u};
-    if (in) {
-      const u32x4* d = reinterpret_cast<const u32x4*>(p.dout + t * p.lddo + c);
-      d0 = __builtin_nontemporal_load(d);
-      d1 = __builtin_nontemporal_load(d + 1);
-    }
-    float a[8], b[8];
-    bf16x8_unpack(d0, a);
-    bf16x8_unpack(d1, b);
-    float scale = 0.0f;
-    u32x4 code{0u, 0u, 0u, 0u};
-    if (p.q != nullptr) code = quantize16(d0, d1, scale);
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t row = slot[j];
-      if (row < 0 || row >= p.M) continue;
-      const float w = weight[j];
+  const Choices chosen(p.slot + t * p.k, p.w + t * p.ldw, p.k, p.M, lane);
+  const bool any = __ballot(chosen.there(chosen.slot)) != 0;   // without rows dout is not read
+  for (int base = wave * 1024; any && base < p.N; base += waves * 1024) {
+    const Columns c{base + lane * 8, p.N};
+    u32x4 d[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      d[v] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.dout + t * p.lddo + c.from(v)));
+    uint2 code[2];
+    float scale[2];
+    for (int j0 = 0; j0 < p.k; j0 += kAheadBwd) {
+      Values8<F32> x[kAheadBwd][2];
       if (p.dw != nullptr) {
-        float dot = 0.0f;
-        if (in) {
-          float f[8], g[8];
-          values8<F32>(load8<F32>(p.y, row * p.ldy + c), f);
-          values8<F32>(load8<F32>(p.y, row * p.ldy + c + 8), g);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(a[i], f[i], dot);
+        for (int j = 0; j < kAheadBwd; ++j) {
+          const int64_t row = chosen.row(j0 + j);
+          if (!chosen.there(row)) continue;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(b[i], g[i], dot);
+          for (int v = 0; v < 2; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
         }
-        dot = wave_sum(dot);
-        if (lane == 0) part[j][wave] = opening ? dot : part[j][wave] + dot;
       }
-      if (!in) continue;
-      if (p.q != nullptr) {
-        const uint32_t turn = w < 0.0f ? 0x80808080u : 0u;
-        *reinterpret_cast<u32x4*>(p.q + row * p.ldq + c) = code ^ u32x4{turn, turn, turn, turn};
-        if ((lane & 7) == 0) p.s[row * p.lds + (c >> 7)] = __builtin_fabsf(w) * scale;
-      }
-      if (p.dy != nullptr) {
-        float f[8], g[8];
+      if (j0 == 0 && p.q != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] = w * a[i];
-          g[i] = w * b[i];
+        for (int v = 0; v < 2; ++v) code[v] = quantize8(d[v], scale[v]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAheadBwd; ++j) {
+        const int64_t row = chosen.row(j0 + j);
+        if (!chosen.there(row)) continue;
+        const float w = chosen.w(j0 + j);
+        if (p.dw != nullptr) {
+          float dot = 0.0f;
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            float f[8], a[8], s = 0.0f;
+            values8<F32>(x[j][v], f);
+            bf16x8_unpack(d[v], a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(a[i], f[i], s);
+            dot += c.in(v) ? s : 0.0f;
+          }
+          dot = wave_sum(dot);
+          if (lane == 0) part[j0 + j][wave] = base == wave * 1024 ? dot : part[j0 + j][wave] + dot;
         }
-        u32x4* y = reinterpret_cast<u32x4*>(p.dy + row * p.lddy + c);
-        y[0] = bf16x8_pack(f);
-        y[1] = bf16x8_pack(g);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          if (!c.in(v)) continue;
+          if (p.q != nullptr) {
+            const uint32_t turn = w < 0.0f ? 0x80808080u : 0u;
+            *reinterpret_cast<uint2*>(p.q + row * p.ldq + c.at(v)) = make_uint2(code[v].x ^ turn, code[v].y ^ turn);
+            if ((lane & 15) == 0) p.s[row * p.lds + (c.at(v) >> 7)] = __builtin_fabsf(w) * scale[v];
+          }
+          if (p.dy != nullptr) {
+            float a[8];
+            bf16x8_unpack(d[v], a);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] *= w;
+            *reinterpret_cast<u32x4*>(p.dy + row * p.lddy + c.at(v)) = bf16x8_pack(a);
+          }
+        }
       }
     }
   }
   if (p.dw == nullptr) return;
   __syncthreads();
   for (int j = tid; j < p.k; j += blockDim.x) {
-    const int64_t row = slot[j];
+    const int64_t row = p.slot[t * p.k + j];
     float s = 0.0f;
-    if (row >= 0 && row < p.M)
+    if (chosen.there(row))
       for (int w = 0; w < waves; ++w) s += part[j][w];
     p.dw[t * p.lddw + j] = s;
   }
@@ -509,10 +574,10 @@ hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t 
 }
 
 hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st) {
-  const int chunks = (p.N + 511) / 512;
-  const int64_t blocks = (p.T * chunks + 3) / 4;
+  const int chunks = (p.N + 1023) / 1024;
+  const int64_t blocks = (p.T * chunks + 1) / 2;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(128);
   if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true>), grid, block, 0, st, p, chunks);
   else hipLaunchKernelGGL((moe_combine_kernel<false>), grid, block, 0, st, p, chunks);
   return hipGetLastError();

@@ -189,8 +189,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
   }
   if (p.d != nullptr) {
     uint16_t* out = p.d + t * p.ldd + c;
-    *reinterpret_cast<u32x4*>(out) = bf16x8_pack(g);
-    *reinterpret_cast<u32x4*>(out + p.I) = bf16x8_pack(u);
+    __builtin_nontemporal_store(bf16x8_pack(g), reinterpret_cast<u32x4*>(out));
+    __builtin_nontemporal_store(bf16x8_pack(u), reinterpret_cast<u32x4*>(out + p.I));
   }
   if (p.h != nullptr) *reinterpret_cast<u32x4*>(p.h + t * p.ldh + c) = bf16x8_pack(h);
 }

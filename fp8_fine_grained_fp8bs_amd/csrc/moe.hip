@@ -20,42 +20,52 @@ namespace {
 // ---------------------------------------------------------------------
 // The sort: a stable counting sort by expert.
 //
-// Large batches take two kernels: workgroups count their stretch of the
-// assignments by expert, then each finds the rows before its stretch from all
-// counts (at most kMaxStretches x E numbers, from the caches) and places its
-// own.  Within a stretch the order is kept without atomics: a wave compares
-// its 64 assignments bit by bit (ballots), which gives an assignment's rank
-// among those of its expert, and counts per wave are summed over the waves.
+// Workgroups take stretches of the assignments.  An assignment's row is the
+// number of those of smaller experts, plus those of its own expert in earlier
+// stretches, plus its rank in its stretch.  The first two come from counts by
+// stretch and expert, which a kernel of its own writes (large batches) or
+// every workgroup counts for itself (middling ones: all assignments, from the
+// caches).  Within a stretch the order is kept without atomics: a wave
+// compares its 64 assignments bit by bit (ballots), which gives an
+// assignment's rank among those of its expert, and counts per wave are
+// summed over the waves.
 // ---------------------------------------------------------------------
-constexpr int kPlaceThreads = 1024;
-constexpr int kSteps = 4;                             // assignments of a lane and round
-constexpr int kRound = kPlaceThreads * kSteps;        // of a workgroup and round
-constexpr int kMaxStretches = 256;
+constexpr int kSortThreads = 512;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSteps = 2;                             // assignments of a lane and round
+constexpr int kRound = kSortThreads * kSteps;         // of a workgroup and round
+constexpr int kPerThread = kMaxExperts / kSortThreads;
+// assignments that every workgroup counts for itself: 8192 to 64 experts 11.7 us against
+// 12.8 with the counting kernel, 16384 15.4 against 12.9 (with rows of 128 columns)
+constexpr int64_t kCountHere = 8192;
 
 // Expert of assignment i among those held here, or -1.
 __device__ __forceinline__ int expert_of(const MoeIds& p, int64_t i) {
-  const int64_t t = i <= 0xffffffffll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(p.k) : i / p.k;
-  const int64_t at = t * p.ldi + (i - t * p.k);
+  int64_t at = i;
+  if (p.ldi != p.k) {
+    const int64_t t = static_cast<uint32_t>(i) / static_cast<uint32_t>(p.k);   // T k <= 2^30
+    at = t * p.ldi + (i - t * p.k);
+  }
   const int64_t id = p.wide ? static_cast<const int64_t*>(p.ids)[at] : static_cast<const int32_t*>(p.ids)[at];
   return id >= p.first && id - p.first < p.E ? static_cast<int>(id - p.first) : -1;
 }
 
-__global__ __launch_bounds__(kPlaceThreads) void moe_count_kernel(MoeIds p, int64_t n, int64_t stretch, int32_t* counts) {
+__global__ __launch_bounds__(kSortThreads) void moe_count_kernel(MoeIds p, int64_t n, int64_t stretch, int32_t* counts) {
   __shared__ int count[kMaxExperts];
   poison_lds<sizeof(count)>(count);
-  for (int e = threadIdx.x; e < p.E; e += kPlaceThreads) count[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += kSortThreads) count[e] = 0;
   __syncthreads();
   const int64_t a = blockIdx.x * stretch, b = a + stretch < n ? a + stretch : n;
-  for (int64_t i = a + threadIdx.x; i < b; i += kPlaceThreads) {
+  for (int64_t i = a + threadIdx.x; i < b; i += kSortThreads) {
     const int e = expert_of(p, i);
     if (e >= 0) atomicAdd(&count[e], 1);   // whole numbers: their order changes nothing
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kPlaceThreads) counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
+  for (int e = threadIdx.x; e < p.E; e += kSortThreads) counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
 }
 
 // Exclusive sum of every thread's v over the workgroup's threads, and the
-// whole sum in `all`.  sums: one number a wave.
+// whole sum in `all`.  sums: one number a wave, which no thread still reads.
 __device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   int s = v;
@@ -76,40 +86,79 @@ __device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
   return before + s - v;
 }
 
-// counts: of every stretch, or null with a single stretch (counted here).
-__global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeIds p, int64_t n, int64_t stretch, int stretches,
-                                                                  int bits, const int32_t* __restrict__ counts) {
-  constexpr int kWaves = kPlaceThreads / 64;
-  __shared__ int rows[kWaves][kMaxExperts];   // a wave's counts, then what the waves before it have
-  __shared__ int start[kMaxExperts];          // row of an expert's next assignment
-  __shared__ int sums[kWaves];
+// counts: of every stretch, or null (counted here).
+__global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64_t n, int64_t stretch, int stretches,
+                                                                 int bits, const int32_t* __restrict__ counts) {
+  __shared__ int rows[kSortWaves][kMaxExperts];   // a wave's counts, then what the waves before it have
+  __shared__ int total[kMaxExperts];              // assignments of an expert
+  __shared__ int start[kMaxExperts];              // those of earlier stretches, then the row of the next
+  __shared__ int sums[kSortWaves];
   poison_lds<sizeof(rows)>(rows);
+  poison_lds<sizeof(total)>(total);
   poison_lds<sizeof(start)>(start);
   poison_lds<sizeof(sums)>(sums);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const uint64_t below = (uint64_t(1) << lane) - 1;
   const int64_t a = blockIdx.x * stretch, b = a + stretch < n ? a + stretch : n;
-  static_assert(kMaxExperts <= kPlaceThreads, "a thread an expert");
-  int total = 0, before = 0;
-  if (counts != nullptr && tid < p.E) {
-#pragma unroll 8
-    for (int s = 0; s < stretches; ++s) {
-      const int c = counts[static_cast<int64_t>(s) * p.E + tid];
-      total += c;
-      before += s < static_cast<int>(blockIdx.x) ? c : 0;
+  for (int x = tid; x < p.E; x += kSortThreads) {
+    total[x] = 0;
+    start[x] = 0;
+  }
+  __syncthreads();
+  if (counts != nullptr) {
+    // as many threads an expert as there are, each some of the stretches
+    const int parts = p.E < kSortThreads ? kSortThreads / p.E : 1;
+    for (int x = tid; x < p.E * parts; x += kSortThreads) {
+      const int part = x / p.E, e = x - part * p.E;
+      int all = 0, earlier = 0;
+#pragma unroll 4
+      for (int s = part; s < stretches; s += parts) {
+        const int c = counts[static_cast<int64_t>(s) * p.E + e];
+        all += c;
+        earlier += s < static_cast<int>(blockIdx.x) ? c : 0;
+      }
+      atomicAdd(&total[e], all);
+      atomicAdd(&start[e], earlier);
+    }
+  } else {
+#pragma unroll 4
+    for (int64_t i = tid; i < n; i += kSortThreads) {
+      const int e = expert_of(p, i);
+      if (e < 0) continue;
+      atomicAdd(&total[e], 1);
+      if (i < a) atomicAdd(&start[e], 1);
     }
   }
-  int64_t round = a;
-  do {   // once where there is nothing to place: the offsets are still written
+  __syncthreads();
+  {
+    int mine[kPerThread], sum = 0, all;
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      mine[x] = tid * kPerThread + x < p.E ? total[tid * kPerThread + x] : 0;
+      sum += mine[x];
+    }
+    int first = exclusive_sum(sum, sums, all);
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      const int e = tid * kPerThread + x;
+      if (e < p.E) {
+        start[e] += first;
+        if (blockIdx.x == 0) p.offsets[e] = first < p.M ? first : static_cast<int32_t>(p.M);
+      }
+      first += mine[x];
+    }
+    if (blockIdx.x == 0 && tid == 0) p.offsets[p.E] = all < p.M ? all : static_cast<int32_t>(p.M);
+  }
+  for (int64_t round = a; round < b; round += kRound) {
     int e[kSteps], rank[kSteps];
-    for (int x = lane; x < p.E; x += 64) rows[wave][x] = 0;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int64_t i = round + (wave * kSteps + s) * 64 + lane;
       e[s] = i < b ? expert_of(p, i) : -1;
     }
+    for (int x = lane; x < p.E; x += 64) rows[wave][x] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       uint64_t same = __ballot(e[s] >= 0);
@@ -130,22 +179,17 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeIds p, int6
       rank[s] += had;
     }
     __syncthreads();
-    int mine = 0;
-    if (tid < p.E) {
-      for (int w = 0; w < kWaves; ++w) {
-        const int c = rows[w][tid];
-        rows[w][tid] = mine;
-        mine += c;
-      }
-    }
-    if (round == a) {
-      if (counts == nullptr) total = mine;   // a single round then (see the launch)
-      int all;
-      const int first = exclusive_sum(tid < p.E ? total : 0, sums, all);
-      if (tid < p.E) start[tid] = first + before;
-      if (blockIdx.x == 0) {
-        if (tid < p.E) p.offsets[tid] = first < p.M ? first : static_cast<int32_t>(p.M);
-        if (tid == 0) p.offsets[p.E] = all < p.M ? all : static_cast<int32_t>(p.M);
+    int mine[kPerThread];
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      const int expert = tid + x * kSortThreads;
+      mine[x] = 0;
+      if (expert >= p.E) continue;
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        const int c = rows[w][expert];
+        rows[w][expert] = mine[x];
+        mine[x] += c;
       }
     }
     __syncthreads();
@@ -157,38 +201,41 @@ __global__ __launch_bounds__(kPlaceThreads) void moe_place_kernel(MoeIds p, int6
       p.slot[i] = at < p.M ? at : -1;
     }
     __syncthreads();
-    if (tid < p.E) start[tid] += mine;
-    round += kRound;
-  } while (round < b);
-}
-
-// ---------------------------------------------------------------------
-// Rows to their places.  A lane has 16 values: 16-byte stores of codes, a
-// tile is 8 lanes.
-// ---------------------------------------------------------------------
-// Max over 8 lanes (a half of a DPP row) of non-negative floats.
-__device__ __forceinline__ float half8_max(float v) {
-  int x = __float_as_int(v);
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0xB1, 0xf, 0xf, false));   // quad_perm [1,0,3,2]
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x4E, 0xf, 0xf, false));   // quad_perm [2,3,0,1]
-  x = max(x, __builtin_amdgcn_update_dpp(x, x, 0x141, 0xf, 0xf, false));  // row_half_mirror
-  return __int_as_float(x);
-}
-
-// 16 bf16 values to codes and their tile's scale (all lanes of a tile).
-__device__ __forceinline__ u32x4 quantize16(const u32x4& v0, const u32x4& v1, float& scale) {
-  float a[8], b[8];
-  bf16x8_unpack(v0, a);
-  bf16x8_unpack(v1, b);
-  float am = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) am = __builtin_fmaxf(am, __builtin_fmaxf(__builtin_fabsf(a[i]), __builtin_fabsf(b[i])));
-  am = half8_max(am);
-  const TileScale t = make_tile_scale(am);
-  const Bf16Side k = bf16_side(t.s, am);
-  scale = t.s;
-  return u32x4{encode4_bf16(a, t, k), encode4_bf16(a + 4, t, k), encode4_bf16(b, t, k), encode4_bf16(b + 4, t, k)};
+    for (int x = 0; x < kPerThread; ++x)
+      if (tid + x * kSortThreads < p.E) start[tid + x * kSortThreads] += mine[x];
+  }
 }
+
+// ---------------------------------------------------------------------
+// Rows to their places.  A workgroup a token, so that a row's scales, written
+// a few at a time, meet in one L2; a wave takes 1024 columns at a time, two
+// vectors of 8 a lane.
+// ---------------------------------------------------------------------
+// A lane's two vectors of a row, 512 columns apart.  A lane behind the row's
+// end reads the row's first columns and leaves its outputs alone.
+struct Columns {
+  int c0, N;
+  __device__ __forceinline__ int at(int v) const { return c0 + v * 512; }
+  __device__ __forceinline__ bool in(int v) const { return at(v) < N; }
+  __device__ __forceinline__ int from(int v) const { return in(v) ? at(v) : c0 & 127; }
+};
+
+// A token's slots and weights, one a lane.
+struct Choices {
+  int slot;
+  float weight;
+  int64_t M;
+  __device__ __forceinline__ Choices(const int32_t* s, const float* w, int k, int64_t M, int lane)
+      : slot(lane < k ? s[lane] : -1), weight(w != nullptr && lane < k ? w[lane] : 1.0f), M(M) {}
+  // assignment j (any number: -1 behind the last), the same in the whole wave
+  __device__ __forceinline__ int64_t row(int j) const { return j < 64 ? __builtin_amdgcn_readlane(slot, j) : -1; }
+  __device__ __forceinline__ bool there(int64_t row) const { return row >= 0 && row < M; }
+  __device__ __forceinline__ bool any() const { return __ballot(there(slot)) != 0; }
+  __device__ __forceinline__ float w(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j & 63));
+  }
+};
 
 // 8 bf16 values to codes and their tile's scale (all 16 lanes of a tile).
 __device__ __forceinline__ uint2 quantize8(const u32x4& v, float& scale) {
@@ -204,80 +251,94 @@ __device__ __forceinline__ uint2 quantize8(const u32x4& v, float& scale) {
   return make_uint2(encode4_bf16(a, t, k), encode4_bf16(a + 4, t, k));
 }
 
-// 16 values of a row on their way.
+// A lane's part of a row on its way: values in BF16, or codes with scales.
 struct Unit {
-  u32x4 x0, x1;   // bf16 values (x0 alone: codes)
-  float s;        // the tile's scale of a row of codes
+  u32x4 x[2];
+  uint2 code[2];
+  float scale[2];
 };
 
-__device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, int c, Unit& u) {
-  if (p.codes_in) {
-    u.x0 = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c));
-    u.s = p.s_in[t * p.lds_in + (c >> 7)];
-  } else {
-    const u32x4* x = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + t * p.ldx + c);
-    u.x0 = __builtin_nontemporal_load(x);
-    u.x1 = __builtin_nontemporal_load(x + 1);
+template <bool CODES>
+__device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, const Columns& c, Unit& u) {
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    if (CODES) {
+      const u32x2 q = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c.from(v)));
+      u.code[v] = make_uint2(q[0], q[1]);
+      u.scale[v] = p.s_in[t * p.lds_in + (c.from(v) >> 7)];
+    } else {
+      u.x[v] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + t * p.ldx + c.from(v)));
+    }
   }
 }
 
-// A unit to the rows that row(0 .. k - 1) gives.  Called by whole tiles.
-template <class Row>
-__device__ __forceinline__ void store_unit(const MoeRows& p, int c, const Unit& u, Row row_of) {
-  u32x4 code = u.x0;
-  float scale = u.s;
-  if (p.q != nullptr && !p.codes_in) code = quantize16(u.x0, u.x1, scale);
+// A unit to the rows chosen.  Called by whole waves.
+template <bool CODES>
+__device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, Unit& u, const Choices& chosen, int lane) {
+  if (!CODES && p.q != nullptr) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) u.code[v] = quantize8(u.x[v], u.scale[v]);
+  }
   for (int j = 0; j < p.k; ++j) {
-    const int64_t row = row_of(j);
-    if (row < 0 || row >= p.M) continue;
-    if (p.q != nullptr) {
-      *reinterpret_cast<u32x4*>(p.q + row * p.ldq + c) = code;
-      if ((threadIdx.x & 7) == 0) p.s[row * p.lds + (c >> 7)] = scale;
-    }
-    if (p.y != nullptr) {
-      u32x4* y = reinterpret_cast<u32x4*>(p.y + row * p.ldy + c);
-      y[0] = u.x0;
-      y[1] = u.x1;
+    const int64_t row = chosen.row(j);
+    if (!chosen.there(row)) continue;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      if (!c.in(v)) continue;
+      if (CODES || p.q != nullptr) {
+        // plain stores: past the caches they were 7 us faster by themselves at 8192
+        // x 2 rows of 7168, and cost the product that reads them 8
+        *reinterpret_cast<uint2*>(p.q + row * p.ldq + c.at(v)) = u.code[v];
+        if ((lane & 15) == 0) p.s[row * p.lds + (c.at(v) >> 7)] = u.scale[v];
+      }
+      if (!CODES && p.y != nullptr) *reinterpret_cast<u32x4*>(p.y + row * p.ldy + c.at(v)) = u.x[v];
     }
   }
 }
 
-// A wave takes 1024 columns of a token.
-__global__ __launch_bounds__(256) void moe_gather_kernel(MoeRows p, int chunks) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t = item <= 0xffffffffll ? static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks) : item / chunks;
-  if (t >= p.T) return;
+// CODES: x holds codes with scales
+template <bool CODES>
+__global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
   const int lane = threadIdx.x & 63;
-  const int c = static_cast<int>(item - t * chunks) * 1024 + lane * 16;
-  const int mine = lane < p.k ? p.slot[t * p.k + lane] : -1;   // lane j holds the token's slot j
-  if (__ballot(mine >= 0 && mine < p.M) == 0) return;          // no row: x is not read
-  if (c >= p.C) return;
-  Unit u;
-  load_unit(p, t, c, u);
-  store_unit(p, c, u, [mine](int j) { return __builtin_amdgcn_readlane(mine, j); });
+  const int64_t t = blockIdx.x;
+  const Choices chosen(p.slot + t * p.k, nullptr, p.k, p.M, lane);
+  if (!chosen.any()) return;   // no row: x is not read
+  for (int base = (threadIdx.x >> 6) * 1024; base < p.C; base += (blockDim.x >> 6) * 1024) {
+    const Columns c{base + lane * 8, p.C};
+    Unit u;
+    load_unit<CODES>(p, t, c, u);
+    store_unit<CODES>(p, c, u, chosen, lane);
+  }
 }
 
-// Few assignments: sort and rows in one launch.  A workgroup a token counts
-// the assignments before each of its own, (e', i') < (e, i), by itself: n
-// comparisons of a wave for an assignment, from the caches.  One more
-// workgroup counts the experts' offsets.
-constexpr int64_t kFew = 2048;
-__device__ __forceinline__ uint32_t order_key(int e, int64_t i) {
+// Few assignments: sort and rows in one launch.  A workgroup a token holds all
+// assignments as keys (expert, number) in LDS and counts the smaller ones for
+// each of its own, which is that one's row: 256 comparisons of a wave a step.
+// One more workgroup counts the experts' offsets.  256 tokens to 8 experts: 9.5 us
+// against 12.8 in two launches, 1024 to 2 7.1 against 9.9, 2048 to 1 level; 4096
+// assignments 12.7 and more against 12.5 and less (but for rows of 7168).
+constexpr int kFew = 2048;
+__device__ __forceinline__ uint32_t order_key(int e, int i) {
   return e >= 0 ? (static_cast<uint32_t>(e) << 20) | static_cast<uint32_t>(i) : 0xffffffffu;
 }
-static_assert(kMaxExperts <= 2048 && kFew <= (1 << 20), "a key's 32 bits");
+static_assert(kMaxExperts <= 2048 && kFew <= (1 << 20) && kFew % 256 == 0, "a key's 32 bits, whole steps");
+static_assert(kMaxExperts <= kFew, "counts in the keys' place");
 
+template <bool CODES>
 __global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
+  __shared__ uint4 keys[kFew / 4];
   __shared__ int32_t slot[kMaxChoices];
-  __shared__ int count[kMaxExperts];
   __shared__ int sums[16];
+  poison_lds<sizeof(keys)>(keys);
   poison_lds<sizeof(slot)>(slot);
-  poison_lds<sizeof(count)>(count);
   poison_lds<sizeof(sums)>(sums);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int n = static_cast<int>(ids.T) * ids.k;
   const int64_t t = blockIdx.x;
   if (t == ids.T) {
+    int* count = reinterpret_cast<int*>(keys);   // kMaxExperts at most
     for (int e = tid; e < ids.E; e += blockDim.x) count[e] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += blockDim.x) {
@@ -297,29 +358,36 @@ __global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
     if (tid == 0) ids.offsets[ids.E] = done < ids.M ? done : static_cast<int32_t>(ids.M);
     return;
   }
-  const int c0 = tid * 16;
+  // the first columns are on their way while the slots are counted
+  const Columns first{wave * 1024 + lane * 8, p.C};
   Unit u;
-  if (c0 < p.C) load_unit(p, t, c0, u);
+  if (wave * 1024 < p.C) load_unit<CODES>(p, t, first, u);
+  uint32_t* key = reinterpret_cast<uint32_t*>(keys);
+  const int steps = (n + 255) / 256;
+  for (int i = tid; i < steps * 256; i += blockDim.x) key[i] = i < n ? order_key(expert_of(ids, i), i) : 0xffffffffu;
+  __syncthreads();
   for (int j = wave; j < ids.k; j += waves) {
-    const int64_t i = t * ids.k + j;
-    const uint32_t key = order_key(expert_of(ids, i), i);
+    const int i = static_cast<int>(t) * ids.k + j;
+    const uint32_t own = __builtin_amdgcn_readfirstlane(key[i]);
     int before = 0;
-    for (int o = 0; o < n; o += 64) {
-      const int other = o + lane;
-      before += __popcll(__ballot(other < n && order_key(expert_of(ids, other < n ? other : 0), other) < key));
+    for (int o = 0; o < steps; ++o) {
+      const uint4 x = keys[o * 64 + lane];
+      before += __popcll(__ballot(x.x < own)) + __popcll(__ballot(x.y < own)) + __popcll(__ballot(x.z < own)) +
+                __popcll(__ballot(x.w < own));
     }
-    const int at = key != 0xffffffffu && before < ids.M ? before : -1;
+    const int at = own != 0xffffffffu && before < ids.M ? before : -1;
     if (lane == 0) {
       slot[j] = at;
       ids.slot[i] = at;
     }
   }
   __syncthreads();
-  const auto row_of = [](int j) { return __builtin_amdgcn_readfirstlane(slot[j]); };
-  if (c0 < p.C) store_unit(p, c0, u, row_of);
-  for (int c = c0 + blockDim.x * 16; c < p.C; c += blockDim.x * 16) {
-    load_unit(p, t, c, u);
-    store_unit(p, c, u, row_of);
+  const Choices chosen(slot, nullptr, ids.k, p.M, lane);
+  if (wave * 1024 < p.C) store_unit<CODES>(p, first, u, chosen, lane);
+  for (int base = (wave + waves) * 1024; base < p.C; base += waves * 1024) {
+    const Columns c{base + lane * 8, p.C};
+    load_unit<CODES>(p, t, c, u);
+    store_unit<CODES>(p, c, u, chosen, lane);
   }
 }
 
@@ -358,30 +426,6 @@ __device__ __forceinline__ void values8(const Values8<F32>& v, float (&f)[8]) {
     bf16x8_unpack(v.a, f);
   }
 }
-
-// A lane's two vectors of a row, 512 columns apart.  A lane behind the row's
-// end reads the row's first columns and leaves its outputs alone.
-struct Columns {
-  int c0, N;
-  __device__ __forceinline__ int at(int v) const { return c0 + v * 512; }
-  __device__ __forceinline__ bool in(int v) const { return at(v) < N; }
-  __device__ __forceinline__ int from(int v) const { return in(v) ? at(v) : c0 & 127; }
-};
-
-// A token's slots and weights, one a lane.
-struct Choices {
-  int slot;
-  float weight;
-  int64_t M;
-  __device__ __forceinline__ Choices(const int32_t* s, const float* w, int k, int64_t M, int lane)
-      : slot(lane < k ? s[lane] : -1), weight(w != nullptr && lane < k ? w[lane] : 1.0f), M(M) {}
-  // assignment j (any number: -1 behind the last), the same in the whole wave
-  __device__ __forceinline__ int64_t row(int j) const { return j < 64 ? __builtin_amdgcn_readlane(slot, j) : -1; }
-  __device__ __forceinline__ bool there(int64_t row) const { return row >= 0 && row < M; }
-  __device__ __forceinline__ float w(int j) const {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j & 63));
-  }
-};
 
 template <bool F32>
 __global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chunks) {
@@ -451,7 +495,7 @@ __global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int64_t t = blockIdx.x;
   const Choices chosen(p.slot + t * p.k, p.w + t * p.ldw, p.k, p.M, lane);
-  const bool any = __ballot(chosen.there(chosen.slot)) != 0;   // without rows dout is not read
+  const bool any = chosen.any();   // without rows dout is not read
   for (int base = wave * 1024; any && base < p.N; base += waves * 1024) {
     const Columns c{base + lane * 8, p.N};
     u32x4 d[2];
@@ -524,41 +568,47 @@ __global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) 
   }
 }
 
-// Stretches of the sort and their length (whole rounds).
-int64_t stretch_of(int64_t n) {
-  const int64_t rounds = n > 0 ? (n + kRound - 1) / kRound : 1;
-  return (rounds + kMaxStretches - 1) / kMaxStretches * kRound;
+// Stretches of the sort and their length (whole rounds).  Every workgroup reads
+// the counts of all stretches, so many experts get fewer.
+struct Stretches {
+  int64_t length;
+  int count;
+};
+Stretches stretches_of(int64_t n, int E) {
+  const int64_t rounds = (n + kRound - 1) / kRound, most = E <= 64 ? 256 : E <= 128 ? 128 : 64;
+  const int64_t each = rounds > most ? (rounds + most - 1) / most : 1;
+  // one where there is nothing to place: the offsets are still written
+  return {each * kRound, n > 0 ? static_cast<int>((rounds + each - 1) / each) : 1};
 }
 
 }  // namespace
 
 int64_t moe_sort_ws(int64_t T, int k, int E) {
-  const int64_t n = T * k, stretch = stretch_of(n), stretches = (n + stretch - 1) / stretch;
-  return stretches > 1 ? stretches * E * static_cast<int64_t>(sizeof(int32_t)) : 0;
+  const int64_t n = T * k;
+  return n > kCountHere ? stretches_of(n, E).count * E * static_cast<int64_t>(sizeof(int32_t)) : 0;
 }
 
 hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st) {
-  const int64_t n = p.T * p.k, stretch = stretch_of(n);
-  const int stretches = n > 0 ? static_cast<int>((n + stretch - 1) / stretch) : 1;
+  const int64_t n = p.T * p.k;
+  const Stretches s = stretches_of(n, p.E);
   int bits = 0;
   while ((p.E - 1) >> bits) ++bits;
   int32_t* counts = nullptr;
-  if (stretches > 1) {
+  if (n > kCountHere) {
     counts = p.ws;
-    hipLaunchKernelGGL(moe_count_kernel, dim3(stretches), dim3(kPlaceThreads), 0, st, p, n, stretch, counts);
+    hipLaunchKernelGGL(moe_count_kernel, dim3(s.count), dim3(kSortThreads), 0, st, p, n, s.length, counts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(moe_place_kernel, dim3(stretches), dim3(kPlaceThreads), 0, st, p, n, stretch, stretches, bits,
-                     counts);
+  hipLaunchKernelGGL(moe_place_kernel, dim3(s.count), dim3(kSortThreads), 0, st, p, n, s.length, s.count, bits, counts);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
-  const int chunks = (p.C + 1023) / 1024;
-  const int64_t blocks = (p.T * chunks + 3) / 4;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(moe_gather_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, chunks);
+  const int waves = (p.C + 1023) / 1024;
+  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * (waves > 16 ? 16 : waves));
+  if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((moe_gather_kernel<false>), grid, block, 0, st, p);
   return hipGetLastError();
 }
 
@@ -566,7 +616,9 @@ hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t 
   if (ids.T * ids.k <= kFew) {
     int waves = (p.C + 1023) / 1024;
     waves = waves < 4 ? 4 : waves > 16 ? 16 : waves;
-    hipLaunchKernelGGL(moe_few_kernel, dim3(static_cast<unsigned>(ids.T + 1)), dim3(64 * waves), 0, st, ids, p);
+    const dim3 grid(static_cast<unsigned>(ids.T + 1)), block(64 * waves);
+    if (p.codes_in) hipLaunchKernelGGL((moe_few_kernel<true>), grid, block, 0, st, ids, p);
+    else hipLaunchKernelGGL((moe_few_kernel<false>), grid, block, 0, st, ids, p);
     return hipGetLastError();
   }
   const hipError_t e = launch_moe_sort(ids, st);

@@ -544,7 +544,7 @@ typedef enum { FP8BS_INDEX_I32 = 0, FP8BS_INDEX_I64 = 1 } fp8bs_index_type;
 fp8bs_status fp8bs_moe_sort(const void *ids, fp8bs_index_type it, int64_t ldi, int64_t T, int64_t k, int64_t first,
                             int64_t E, int64_t M, int32_t *offsets, int32_t *slot, void *ws, int64_t ws_bytes,
                             void *stream);
-/* Bytes of working memory of fp8bs_moe_sort and fp8bs_moe_dispatch (0 to 2^20), or -1
+/* Bytes of working memory of fp8bs_moe_sort and fp8bs_moe_dispatch (0 to 2^18), or -1
  * where a size is invalid. */
 int64_t fp8bs_moe_sort_ws(int64_t T, int64_t k, int64_t E);
 

@@ -32,7 +32,7 @@ def choices(T, k, of, seed, out_of_range=0.1):
 SORTS = [(1, 1, 1, 1, 0, None), (1, 8, 256, 256, 0, None), (5, 2, 8, 8, 0, None), (37, 6, 60, 13, 20, None),
          (700, 8, 64, 64, 0, None), (512, 8, 16, 16, 0, None), (4097, 1, 1024, 1024, 0, None),
          (3000, 8, 256, 32, 96, 2000), (900, 7, 40, 40, 0, 11), (33, 64, 9, 5, 2, None), (20000, 3, 7, 7, 0, None),
-         (64, 8, 8, 8, 0, 0)]
+         (64, 8, 8, 8, 0, 0), (1024, 8, 100, 70, 3, None), (1025, 8, 600, 600, 0, None), (40000, 8, 300, 300, 0, None)]
 
 
 @pytest.mark.parametrize("wide", [False, True])
@@ -55,7 +55,7 @@ def test_sort(T, k, of, E, first, rows, wide):
 def test_sort_of_many():
     """More rounds than stretches: workgroups of several rounds."""
     native_loaded()
-    T, k, E = 170001, 8, 100
+    T, k, E = 170001, 8, 100   # 1329 rounds, 128 stretches of 11
     announce(f"sort {T}x{k}")
     ids = torch.randint(-3, 130, (T, k), generator=torch.Generator().manual_seed(1))
     offsets, slot = fp8bs.moe_sort(ids.cuda(), E, first=5)
@@ -96,11 +96,13 @@ def codes_of(x):
     return torch.from_numpy(q), torch.from_numpy(s)
 
 
-# around the largest count of one launch (2048), widths around a wave's and a workgroup's columns
+# around the largest counts of one launch (2048) and of two (8192), widths around a wave's and a
+# workgroup's columns
 DISPATCHES = [(1, 1, 128, 1, 1, None), (1, 8, 7168, 64, 64, None), (16, 8, 7168, 64, 64, None), (3, 5, 1152, 9, 4, None),
               (256, 8, 256, 32, 32, None), (257, 8, 256, 32, 32, None), (683, 3, 384, 16, 16, 900),
               (2, 64, 640, 16, 16, None), (9, 2, 16512, 4, 4, None), (1500, 2, 1024, 8, 8, None),
-              (700, 6, 16512, 160, 20, None), (40, 8, 128, 1024, 1024, None)]
+              (700, 6, 16512, 160, 20, None), (40, 8, 128, 1024, 1024, None),
+              (1025, 8, 128, 256, 256, None)]
 
 
 @pytest.mark.parametrize("T,k,C,of,E,rows", DISPATCHES)

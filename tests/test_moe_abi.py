@@ -75,7 +75,7 @@ REFUSALS = [
     (sort, dict(M=1 << 31), SHAPE), (sort, dict(T=(1 << 30) // 8 + 1), SHAPE), (sort, dict(ldi=7), INVALID),
     (sort, dict(ids=NULL), INVALID), (sort, dict(offsets=NULL), INVALID), (sort, dict(slot=NULL), INVALID),
     (sort, dict(ids=A + 4), MISALIGNED), (sort, dict(it=0, ids=A + 2), MISALIGNED), (sort, dict(slot=A + 1), MISALIGNED),
-    (sort, dict(T=5000), INVALID), (sort, dict(T=5000, ws=A, ws_bytes=10 * 16 * 4 - 1), INVALID),
+    (sort, dict(T=5000), INVALID), (sort, dict(T=5000, ws=A, ws_bytes=40 * 16 * 4 - 1), INVALID),
     (gather, dict(src=2), INVALID), (gather, dict(src=0), INVALID), (gather, dict(src=0, y=NULL, s_in=NULL), INVALID),
     (gather, dict(q=NULL, s=NULL, y=NULL), INVALID), (gather, dict(q=NULL), INVALID), (gather, dict(x=NULL), INVALID),
     (gather, dict(slot=NULL), INVALID), (gather, dict(C=100), SHAPE), (gather, dict(C=-128), INVALID),
@@ -126,9 +126,10 @@ def test_nothing_to_do(call, args):
 
 
 def test_working_memory():
-    assert fp8bs.fp8bs_moe_sort_ws(512, 8, 256) == 0
-    assert fp8bs.fp8bs_moe_sort_ws(513, 8, 256) == 2 * 256 * 4
-    assert fp8bs.fp8bs_moe_sort_ws(1 << 27, 8, 1024) <= 1 << 20
+    assert fp8bs.fp8bs_moe_sort_ws(1024, 8, 256) == 0
+    assert fp8bs.fp8bs_moe_sort_ws(1025, 8, 256) == 9 * 256 * 4
+    assert all(0 < fp8bs.fp8bs_moe_sort_ws(t, 8, e) <= 1 << 18 for t in (1 << 13, 1 << 20, 1 << 27)
+               for e in (1, 64, 65, 256, 257, 1024))
     assert fp8bs.fp8bs_moe_sort_ws(0, 8, 16) == 0
     for bad in ((-1, 8, 16), (4, 0, 16), (4, 65, 16), (4, 8, 0), (4, 8, 1025), (1 << 28, 8, 16)):
         assert fp8bs.fp8bs_moe_sort_ws(*bad) == -1

@@ -76,14 +76,15 @@ def _build_marshal():
 
     import torch
     from torch.utils import cpp_extension
-    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]
+    rocm = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))), "include")
+    include = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], rocm]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f'-DFP8BS_TORCH_VERSION="{torch.__version__}"',
+           "-D__HIP_PLATFORM_AMD__", f'-DFP8BS_TORCH_VERSION="{torch.__version__}"',
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
     for d in include:
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "marshal.cpp"), "-o", MARSHAL + ".tmp", "-L" + cpp_extension.TORCH_LIB_PATH,
-            "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10"]
+            "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10_hip", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for marshal.cpp:\n" + r.stderr)

@@ -15,6 +15,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -119,12 +120,18 @@ struct Numbers {
     ok = ok && PyFloat_Check(o);
     return ok ? static_cast<float>(PyFloat_AS_DOUBLE(o)) : 0.0f;
   }
+  bool flag(PyObject* o) {
+    ok = ok && PyBool_Check(o);
+    return o == Py_True;
+  }
   float real(PyObject* o) {
     ok = ok && PyFloat_Check(o);
     return ok ? static_cast<float>(PyFloat_AS_DOUBLE(o)) : 0.0f;
   }
-  // A handle, or a function that gives one: asked last, when all else is there.
+  // A handle, a function that gives one (asked last, when all else is there), or None:
+  // the current device's current stream.
   void* stream(PyObject* o) {
+    if (o == Py_None) return c10::hip::getCurrentHIPStream().stream();
     if (!ok || PyLong_Check(o)) return address(o);
     PyObject* x = PyObject_CallNoArgs(o);
     if (x == nullptr) {
@@ -341,11 +348,11 @@ PyObject* rmsnorm_quant_1x128(PyObject*, PyObject* const* o, Py_ssize_t n) {
     Py_RETURN_NONE;
   const auto entry = reinterpret_cast<decltype(&fp8bs_rmsnorm_quant_1x128)>(a.address(o[0]));
   const float eps = a.real(o[4]);
-  const bool with_q = o[5] == Py_True, with_y = o[6] == Py_True;
+  const bool with_q = a.flag(o[5]), with_y = a.flag(o[6]), with_rstd = a.flag(o[7]);
   void* stream = a.stream(o[8]);
   if (!a.ok || (!with_q && !with_y)) Py_RETURN_NONE;
   const Rows out(x.t, with_q, with_y, x.rows, x.cols);
-  const Fresh h(x.t, r.t != nullptr, at::kBFloat16, {x.rows, x.cols}), rstd(x.t, o[7] == Py_True, at::kFloat, {x.rows});
+  const Fresh h(x.t, r.t != nullptr, at::kBFloat16, {x.rows, x.cols}), rstd(x.t, with_rstd, at::kFloat, {x.rows});
   return answers(entry(data<void>(x.t), x.ld, data<void>(r.t), r.ld, data<void>(gamma), gt, eps, x.rows, x.cols,
                        h.data<void>(), x.cols, out.pq(), out.ldq(), out.ps(), out.lds(), out.py(), out.ldy(),
                        rstd.data<float>(), stream),
@@ -367,7 +374,7 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
     Py_RETURN_NONE;
   const auto entry = reinterpret_cast<decltype(&fp8bs_rmsnorm_bwd)>(a.address(o[0]));
   const auto size = reinterpret_cast<decltype(&fp8bs_rmsnorm_bwd_ws)>(a.address(o[1]));
-  const bool with = o[7] == Py_True;
+  const bool with = a.flag(o[7]);
   void* stream = a.stream(o[8]);
   if (!a.ok) Py_RETURN_NONE;
   const int64_t need = with ? std::max<int64_t>(size(h.rows, h.cols), 0) : 0;
@@ -397,10 +404,10 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const auto size = reinterpret_cast<decltype(&fp8bs_moe_sort_ws)>(a.address(o[1]));
   const int64_t E = a.whole(o[5]), first = a.whole(o[6]), k = ids.cols;
   const int64_t rows = o[7] == Py_None ? x.rows * k : a.whole(o[7]);
+  const bool with_q = a.flag(o[8]), with_y = a.flag(o[9]), made = o[10] == Py_None;
   void* stream = a.stream(o[11]);
-  const bool made = o[10] == Py_None;
   if (!a.ok || E <= 0 || E > (1 << 20) || rows < 0) Py_RETURN_NONE;
-  Rows out(x.t, made && o[8] == Py_True, made && o[9] == Py_True, rows, x.cols);
+  Rows out(x.t, made && with_q, made && with_y, rows, x.cols);
   if (!made && !out.take(o[10])) Py_RETURN_NONE;
   const int64_t need = std::max<int64_t>(size(x.rows, k, E), 0);
   const Fresh offsets(x.t, true, at::kInt, {E + 1}), slot(x.t, true, at::kInt, {x.rows, k}),
@@ -452,10 +459,10 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (o[4] != Py_None && (!values(o[4], y, f32) || y.cols != N)) Py_RETURN_NONE;
   const auto entry = reinterpret_cast<decltype(&fp8bs_moe_combine_bwd)>(a.address(o[0]));
   const int64_t rows = o[5] != Py_None ? a.whole(o[5]) : y.t != nullptr ? y.rows : T * k;
+  const bool with_q = a.flag(o[6]), with_dy = a.flag(o[7]), made = o[8] == Py_None;
   void* stream = a.stream(o[9]);
-  const bool made = o[8] == Py_None;
   if (!a.ok || rows < 0) Py_RETURN_NONE;
-  Rows out(dout.t, made && o[6] == Py_True, made && o[7] == Py_True, rows, N);
+  Rows out(dout.t, made && with_q, made && with_dy, rows, N);
   if (!made && !out.take(o[8])) Py_RETURN_NONE;
   if (y.t != nullptr && y.rows != out.M) Py_RETURN_NONE;
   const Fresh dw(dout.t, y.t != nullptr, at::kFloat, {T, k});
@@ -476,10 +483,11 @@ PyObject* swiglu_bwd_quant_1x128(PyObject*, PyObject* const* o, Py_ssize_t n) {
       !matrix(o[3], at::kBFloat16, g.rows, g.cols, u))
     Py_RETURN_NONE;
   const auto entry = reinterpret_cast<decltype(&fp8bs_swiglu_bwd_quant_1x128)>(a.address(o[0]));
+  const bool with_q = a.flag(o[4]), with_d = a.flag(o[5]), with_h = a.flag(o[6]);
   void* stream = a.stream(o[7]);
   if (!a.ok) Py_RETURN_NONE;
-  const Rows out(g.t, o[4] == Py_True, o[5] == Py_True, g.rows, 2 * g.cols);
-  const Fresh h(g.t, o[6] == Py_True, at::kBFloat16, {g.rows, g.cols});
+  const Rows out(g.t, with_q, with_d, g.rows, 2 * g.cols);
+  const Fresh h(g.t, with_h, at::kBFloat16, {g.rows, g.cols});
   return answers(entry(data<void>(dh.t), dh.ld, data<void>(g.t), g.ld, data<void>(u.t), u.ld, g.rows, g.cols, out.pq(),
                        out.ldq(), out.ps(), out.lds(), out.py(), out.ldy(), h.data<void>(), g.cols, stream),
                  {out.q, out.s, out.y, h});

@@ -209,10 +209,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64
 
 // ---------------------------------------------------------------------
 // Rows to their places.  A workgroup a token, so that a row's scales, written
-// a few at a time, meet in one L2; a wave takes 1024 columns at a time, two
-// vectors of 8 a lane.
+// a few at a time, meet in one L2; a lane has V vectors of 8 values at a time.
 // ---------------------------------------------------------------------
-// A lane's two vectors of a row, 512 columns apart.  A lane behind the row's
+// A lane's vectors of a row, 512 columns apart.  A lane behind the row's
 // end reads the row's first columns and leaves its outputs alone.
 struct Columns {
   int c0, N;
@@ -252,16 +251,17 @@ __device__ __forceinline__ uint2 quantize8(const u32x4& v, float& scale) {
 }
 
 // A lane's part of a row on its way: values in BF16, or codes with scales.
+template <int V>
 struct Unit {
-  u32x4 x[2];
-  uint2 code[2];
-  float scale[2];
+  u32x4 x[V];
+  uint2 code[V];
+  float scale[V];
 };
 
-template <bool CODES>
-__device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, const Columns& c, Unit& u) {
+template <bool CODES, int V>
+__device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, const Columns& c, Unit<V>& u) {
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
+  for (int v = 0; v < V; ++v) {
     if (CODES) {
       const u32x2 q = __builtin_nontemporal_load(
           reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(p.x) + t * p.ldx + c.from(v)));
@@ -275,17 +275,17 @@ __device__ __forceinline__ void load_unit(const MoeRows& p, int64_t t, const Col
 }
 
 // A unit to the rows chosen.  Called by whole waves.
-template <bool CODES>
-__device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, Unit& u, const Choices& chosen, int lane) {
+template <bool CODES, int V>
+__device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, Unit<V>& u, const Choices& chosen, int lane) {
   if (!CODES && p.q != nullptr) {
 #pragma unroll
-    for (int v = 0; v < 2; ++v) u.code[v] = quantize8(u.x[v], u.scale[v]);
+    for (int v = 0; v < V; ++v) u.code[v] = quantize8(u.x[v], u.scale[v]);
   }
   for (int j = 0; j < p.k; ++j) {
     const int64_t row = chosen.row(j);
     if (!chosen.there(row)) continue;
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
+    for (int v = 0; v < V; ++v) {
       if (!c.in(v)) continue;
       if (CODES || p.q != nullptr) {
         // plain stores: past the caches they were 7 us faster by themselves at 8192
@@ -299,17 +299,17 @@ __device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, U
 }
 
 // CODES: x holds codes with scales
-template <bool CODES>
+template <bool CODES, int V>
 __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
   const int lane = threadIdx.x & 63;
   const int64_t t = blockIdx.x;
   const Choices chosen(p.slot + t * p.k, nullptr, p.k, p.M, lane);
   if (!chosen.any()) return;   // no row: x is not read
-  for (int base = (threadIdx.x >> 6) * 1024; base < p.C; base += (blockDim.x >> 6) * 1024) {
+  for (int base = (threadIdx.x >> 6) * (512 * V); base < p.C; base += (blockDim.x >> 6) * (512 * V)) {
     const Columns c{base + lane * 8, p.C};
-    Unit u;
-    load_unit<CODES>(p, t, c, u);
-    store_unit<CODES>(p, c, u, chosen, lane);
+    Unit<V> u;
+    load_unit<CODES, V>(p, t, c, u);
+    store_unit<CODES, V>(p, c, u, chosen, lane);
   }
 }
 
@@ -360,8 +360,8 @@ __global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
   }
   // the first columns are on their way while the slots are counted
   const Columns first{wave * 1024 + lane * 8, p.C};
-  Unit u;
-  if (wave * 1024 < p.C) load_unit<CODES>(p, t, first, u);
+  Unit<2> u;
+  if (wave * 1024 < p.C) load_unit<CODES, 2>(p, t, first, u);
   uint32_t* key = reinterpret_cast<uint32_t*>(keys);
   const int steps = (n + 255) / 256;
   for (int i = tid; i < steps * 256; i += blockDim.x) key[i] = i < n ? order_key(expert_of(ids, i), i) : 0xffffffffu;
@@ -383,11 +383,11 @@ __global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
   }
   __syncthreads();
   const Choices chosen(slot, nullptr, ids.k, p.M, lane);
-  if (wave * 1024 < p.C) store_unit<CODES>(p, first, u, chosen, lane);
+  if (wave * 1024 < p.C) store_unit<CODES, 2>(p, first, u, chosen, lane);
   for (int base = (wave + waves) * 1024; base < p.C; base += waves * 1024) {
     const Columns c{base + lane * 8, p.C};
-    load_unit<CODES>(p, t, c, u);
-    store_unit<CODES>(p, c, u, chosen, lane);
+    load_unit<CODES, 2>(p, t, c, u);
+    store_unit<CODES, 2>(p, c, u, chosen, lane);
   }
 }
 
@@ -483,41 +483,39 @@ __global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chun
 // Gradient of the way back: dy[slot] = w dout[t] as codes (dout's tile is
 // quantized once; a row's scales are those of dout times |w|, its signs those
 // of w dout) and in BF16, dw[t][j] = dout[t] . y[slot].  A workgroup a token,
-// a wave 1024 columns at a time, with up to kAheadBwd rows' loads in flight;
 // every wave has columns in its first turn.
 // ---------------------------------------------------------------------
-constexpr int kAheadBwd = 4;
-
-template <bool F32>
-__global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) {
+template <bool F32, int V>
+__global__ __launch_bounds__(V == 2 ? 1024 : 512) void moe_combine_bwd_kernel(MoeCombineBwd p) {
   __shared__ float part[kMaxChoices][16];
   poison_lds<sizeof(part)>(part);
+  constexpr int kAheadBwd = 8 / V, kStep = 512 * V;   // rows whose loads are in flight, columns of a wave
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
   const int64_t t = blockIdx.x;
   const Choices chosen(p.slot + t * p.k, p.w + t * p.ldw, p.k, p.M, lane);
   const bool any = chosen.any();   // without rows dout is not read
-  for (int base = wave * 1024; any && base < p.N; base += waves * 1024) {
+  for (int base = wave * kStep; any && base < p.N; base += waves * kStep) {
     const Columns c{base + lane * 8, p.N};
-    u32x4 d[2];
+    u32x4 d[V];
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
+    for (int v = 0; v < V; ++v)
       d[v] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.dout + t * p.lddo + c.from(v)));
-    uint2 code[2];
-    float scale[2];
+    uint2 code[V];
+    float scale[V];
     for (int j0 = 0; j0 < p.k; j0 += kAheadBwd) {
-      Values8<F32> x[kAheadBwd][2];
+      Values8<F32> x[kAheadBwd][V];
       if (p.dw != nullptr) {
 #pragma unroll
         for (int j = 0; j < kAheadBwd; ++j) {
           const int64_t row = chosen.row(j0 + j);
           if (!chosen.there(row)) continue;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
+          for (int v = 0; v < V; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
         }
       }
       if (j0 == 0 && p.q != nullptr) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) code[v] = quantize8(d[v], scale[v]);
+        for (int v = 0; v < V; ++v) code[v] = quantize8(d[v], scale[v]);
       }
 #pragma unroll
       for (int j = 0; j < kAheadBwd; ++j) {
@@ -527,7 +525,7 @@ __global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) 
         if (p.dw != nullptr) {
           float dot = 0.0f;
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
+          for (int v = 0; v < V; ++v) {
             float f[8], a[8], s = 0.0f;
             values8<F32>(x[j][v], f);
             bf16x8_unpack(d[v], a);
@@ -536,10 +534,10 @@ __global__ __launch_bounds__(1024) void moe_combine_bwd_kernel(MoeCombineBwd p) 
             dot += c.in(v) ? s : 0.0f;
           }
           dot = wave_sum(dot);
-          if (lane == 0) part[j0 + j][wave] = base == wave * 1024 ? dot : part[j0 + j][wave] + dot;
+          if (lane == 0) part[j0 + j][wave] = base == wave * kStep ? dot : part[j0 + j][wave] + dot;
         }
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
+        for (int v = 0; v < V; ++v) {
           if (!c.in(v)) continue;
           if (p.q != nullptr) {
             const uint32_t turn = w < 0.0f ? 0x80808080u : 0u;
@@ -605,10 +603,15 @@ hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st) {
 }
 
 hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
-  const int waves = (p.C + 1023) / 1024;
+  // four vectors a lane for wide rows in BF16 (8192 tokens of 7168 to 32 of 256 experts
+  // 28.9 us against 31.8, all of them to 2 of 8 level), two for narrow ones and for
+  // codes, whose lanes have nothing to compute (4096 x 8 rows of 7168: 70.5 us against 73.8)
+  const bool wide = !p.codes_in && p.C >= 2048;
+  const int step = wide ? 2048 : 1024, waves = (p.C + step - 1) / step;
   const dim3 grid(static_cast<unsigned>(p.T)), block(64 * (waves > 16 ? 16 : waves));
-  if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((moe_gather_kernel<false>), grid, block, 0, st, p);
+  if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true, 2>), grid, block, 0, st, p);
+  else if (wide) hipLaunchKernelGGL((moe_gather_kernel<false, 4>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((moe_gather_kernel<false, 2>), grid, block, 0, st, p);
   return hipGetLastError();
 }
 
@@ -637,11 +640,15 @@ hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st) {
 
 hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st) {
   if (p.T > 0x7fffffff) return hipErrorInvalidValue;
-  int waves = (p.N + 1023) / 1024;
-  waves = waves > 16 ? 16 : waves;
-  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * waves);
-  if (p.y_f32) hipLaunchKernelGGL((moe_combine_bwd_kernel<true>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((moe_combine_bwd_kernel<false>), grid, block, 0, st, p);
+  // four vectors a lane where there are tokens enough (1024 x 8 rows of 7168: 33.7 us
+  // against 37.9, 8191 x 2 90.7 against 91.8), two for few (16 x 8: 8.1 against 9.0)
+  const bool many = p.T >= 512;
+  const int step = many ? 2048 : 1024, most = many ? 8 : 16, waves = (p.N + step - 1) / step;
+  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * (waves > most ? most : waves));
+  if (p.y_f32 && many) hipLaunchKernelGGL((moe_combine_bwd_kernel<true, 4>), grid, block, 0, st, p);
+  else if (p.y_f32) hipLaunchKernelGGL((moe_combine_bwd_kernel<true, 2>), grid, block, 0, st, p);
+  else if (many) hipLaunchKernelGGL((moe_combine_bwd_kernel<false, 4>), grid, block, 0, st, p);
+  else hipLaunchKernelGGL((moe_combine_bwd_kernel<false, 2>), grid, block, 0, st, p);
   return hipGetLastError();
 }
 

@@ -59,6 +59,7 @@ _lib_path = LIB_PATH
 _functions = {}      # the loaded library's entry points by name
 _addresses = {}      # and their addresses
 _marshal = None      # the compiled short way into the operators of small calls
+_ways = {}           # its functions with the loaded library's entry points
 
 
 class _Names(dict):
@@ -81,6 +82,7 @@ def use_library(path: str) -> str:
     _lib_path, _lib = path, None
     _functions.clear()
     _addresses.clear()
+    _ways.clear()
     for sizes in (_ws_bytes, _norm_ws_bytes, _sort_ws_bytes):
         sizes.cache_clear()
     return prev
@@ -431,6 +433,23 @@ def _short(name, *args):
     if type(result) is int:
         raise Fp8bsError(result, name)
     return result
+
+
+def _way(name, *sizes):
+    """The named operator by the compiled short way, as a function of what follows its
+    entry points (the operator's and those of the sizes it needs): like _short for
+    helpers whose own time counts, a status is left to them."""
+    global _marshal
+    if _marshal is None:
+        _marshal = _load_marshal()
+    way = _marshal.get(name)
+    way = _no_way if way is None else functools.partial(way, *map(_address, (name,) + sizes))
+    _ways[name] = way
+    return way
+
+
+def _no_way(*args):
+    return None
 
 
 def _address(name):
@@ -1071,10 +1090,13 @@ def rmsnorm_quant_1x128(x, gamma, residual=None, eps=1e-6, codes=True, with_y=Fa
     (q, s, h, y, rstd), where codes q and scales s, the sum h, the norm y in
     BF16 and the row factors rstd are None unless asked for (h: without a
     residual).  Not recorded by autograd; the gradient is rmsnorm_bwd."""
-    outputs = _short("fp8bs_rmsnorm_quant_1x128", x, gamma, residual, eps, bool(codes), bool(with_y), bool(with_rstd),
-                     _current_stream) if stream is None else None
-    if outputs is not None:
-        return outputs
+    if stream is None:
+        way = _ways.get("fp8bs_rmsnorm_quant_1x128") or _way("fp8bs_rmsnorm_quant_1x128")
+        outputs = way(x, gamma, residual, eps, codes, with_y, with_rstd, None)
+        if outputs.__class__ is tuple:
+            return outputs
+        if outputs is not None:
+            raise Fp8bsError(outputs, "fp8bs_rmsnorm_quant_1x128")
     import torch
     T, C = x.shape
     q, s = _code_rows(T, C, x.device) if codes else (None, None)
@@ -1089,10 +1111,13 @@ def rmsnorm_bwd(dn, h, gamma, rstd, dres=None, with_dgamma=True, stream=None):
     """Gradient of the norm of h (the x + residual that rmsnorm_quant_1x128
     gave, or x): (dx, dgamma), dx that of x and of the residual, dgamma f32
     or None.  dres: the gradient of h's other uses."""
-    outputs = _short("fp8bs_rmsnorm_bwd", _address("fp8bs_rmsnorm_bwd_ws"), dn, h, gamma, rstd, dres, bool(with_dgamma),
-                     _current_stream) if stream is None else None
-    if outputs is not None:
-        return outputs
+    if stream is None:
+        way = _ways.get("fp8bs_rmsnorm_bwd") or _way("fp8bs_rmsnorm_bwd", "fp8bs_rmsnorm_bwd_ws")
+        outputs = way(dn, h, gamma, rstd, dres, with_dgamma, None)
+        if outputs.__class__ is tuple:
+            return outputs
+        if outputs is not None:
+            raise Fp8bsError(outputs, "fp8bs_rmsnorm_bwd")
     import torch
     T, C = h.shape
     dx = torch.empty((T, C), dtype=torch.bfloat16, device=h.device)
@@ -1137,10 +1162,13 @@ def moe_gather(x, slot, s_in=None, rows=None, codes=True, with_y=False, out=None
 
 def moe_dispatch(x, ids, E, first=0, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
     """moe_sort and moe_gather in one call: (q, s, y, offsets, slot)."""
-    outputs = _short("fp8bs_moe_dispatch", _address("fp8bs_moe_sort_ws"), x, s_in, ids, E, first, rows, bool(codes),
-                     bool(with_y), out, _current_stream) if stream is None else None
-    if outputs is not None:
-        return outputs
+    if stream is None:
+        way = _ways.get("fp8bs_moe_dispatch") or _way("fp8bs_moe_dispatch", "fp8bs_moe_sort_ws")
+        outputs = way(x, s_in, ids, E, first, rows, codes, with_y, out, None)
+        if outputs.__class__ is tuple:
+            return outputs
+        if outputs is not None:
+            raise Fp8bsError(outputs, "fp8bs_moe_dispatch")
     import torch
     (T, C), k = x.shape, ids.shape[1]
     q, s, y = _row_outputs(out, T * k if rows is None else rows, C, codes, with_y, x.device)
@@ -1155,9 +1183,13 @@ def moe_combine(y, slot, w=None, add=None, stream=None):
     """Rows of y (bf16 or f32) back to their tokens, weighted by w f32 [T][k] (or
     summed plainly: the gradient of moe_gather), onto add.  Not recorded by
     autograd; the gradient is moe_combine_bwd (add's is the output's)."""
-    out = _short("fp8bs_moe_combine", y, slot, w, add, _current_stream) if stream is None else None
-    if out is not None:
-        return out
+    if stream is None:
+        way = _ways.get("fp8bs_moe_combine") or _way("fp8bs_moe_combine")
+        out = way(y, slot, w, add, None)
+        if out.__class__ is int:
+            raise Fp8bsError(out, "fp8bs_moe_combine")
+        if out is not None:
+            return out
     import torch
     out = torch.empty((slot.shape[0], y.shape[1]), dtype=torch.bfloat16, device=y.device)
     fp8bs_moe_combine(y, slot, w, add, out, stream)
@@ -1168,10 +1200,13 @@ def moe_combine_bwd(dout, slot, w, y=None, rows=None, codes=True, with_dy=False,
     """Gradient of moe_combine: (q, s, dy, dw), the rows' gradient as codes with
     scales and in BF16 where asked for, and the weights' (with y) or None.  out:
     (q, s, dy) to write into; rows that no slot names are not written."""
-    outputs = _short("fp8bs_moe_combine_bwd", dout, slot, w, y, rows, bool(codes), bool(with_dy), out,
-                     _current_stream) if stream is None else None
-    if outputs is not None:
-        return outputs
+    if stream is None:
+        way = _ways.get("fp8bs_moe_combine_bwd") or _way("fp8bs_moe_combine_bwd")
+        outputs = way(dout, slot, w, y, rows, codes, with_dy, out, None)
+        if outputs.__class__ is tuple:
+            return outputs
+        if outputs is not None:
+            raise Fp8bsError(outputs, "fp8bs_moe_combine_bwd")
     import torch
     if rows is None:
         rows = slot.numel() if y is None else y.shape[0]
@@ -1185,10 +1220,13 @@ def swiglu_bwd_quant_1x128(dh, g, u, codes=True, with_d=False, with_h=False, str
     """Gradient of h = silu(g) u: (q, s, d, h), the gradients of g and u side by
     side [T][2I] as codes with scales and in BF16, and h itself, where asked for
     (None otherwise)."""
-    outputs = _short("fp8bs_swiglu_bwd_quant_1x128", dh, g, u, bool(codes), bool(with_d), bool(with_h),
-                     _current_stream) if stream is None else None
-    if outputs is not None:
-        return outputs
+    if stream is None:
+        way = _ways.get("fp8bs_swiglu_bwd_quant_1x128") or _way("fp8bs_swiglu_bwd_quant_1x128")
+        outputs = way(dh, g, u, codes, with_d, with_h, None)
+        if outputs.__class__ is tuple:
+            return outputs
+        if outputs is not None:
+            raise Fp8bsError(outputs, "fp8bs_swiglu_bwd_quant_1x128")
     import torch
     T, I = g.shape
     q, s = _code_rows(T, 2 * I, g.device) if codes else (None, None)

@@ -15,6 +15,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -265,6 +266,14 @@ bool gamma_of(PyObject* o, int64_t C, const at::Tensor*& t, fp8bs_out_dtype& typ
 }
 fp8bs_out_dtype type_of(bool f32) { return f32 ? FP8BS_OUT_F32 : FP8BS_OUT_BF16; }
 
+// Whether all of them (null: not given) are on the current device, on which the kernels run.
+bool here(std::initializer_list<const at::Tensor*> tensors) {
+  const auto device = c10::hip::current_device();
+  for (const at::Tensor* t : tensors)
+    if (t != nullptr && t->device().index() != device) return false;
+  return true;
+}
+
 // A new [rows][cols] on x's device where wanted, and its pointer.
 struct Fresh {
   at::Tensor t;
@@ -350,7 +359,7 @@ PyObject* rmsnorm_quant_1x128(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const float eps = a.real(o[4]);
   const bool with_q = a.flag(o[5]), with_y = a.flag(o[6]), with_rstd = a.flag(o[7]);
   void* stream = a.stream(o[8]);
-  if (!a.ok || (!with_q && !with_y)) Py_RETURN_NONE;
+  if (!a.ok || (!with_q && !with_y) || !here({x.t, r.t, gamma})) Py_RETURN_NONE;
   const Rows out(x.t, with_q, with_y, x.rows, x.cols);
   const Fresh h(x.t, r.t != nullptr, at::kBFloat16, {x.rows, x.cols}), rstd(x.t, with_rstd, at::kFloat, {x.rows});
   return answers(entry(data<void>(x.t), x.ld, data<void>(r.t), r.ld, data<void>(gamma), gt, eps, x.rows, x.cols,
@@ -376,7 +385,7 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const auto size = reinterpret_cast<decltype(&fp8bs_rmsnorm_bwd_ws)>(a.address(o[1]));
   const bool with = a.flag(o[7]);
   void* stream = a.stream(o[8]);
-  if (!a.ok) Py_RETURN_NONE;
+  if (!a.ok || !here({dn.t, h.t, dres.t, gamma, rstd})) Py_RETURN_NONE;
   const int64_t need = with ? std::max<int64_t>(size(h.rows, h.cols), 0) : 0;
   const Fresh dx(h.t, true, at::kBFloat16, {h.rows, h.cols}), dgamma(h.t, with, at::kFloat, {h.cols}),
       ws(h.t, need > 0, at::kByte, {need});
@@ -409,6 +418,7 @@ PyObject* moe_dispatch(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (!a.ok || E <= 0 || E > (1 << 20) || rows < 0) Py_RETURN_NONE;
   Rows out(x.t, made && with_q, made && with_y, rows, x.cols);
   if (!made && !out.take(o[10])) Py_RETURN_NONE;
+  if (!here({x.t, s_in.t, ids.t, out.mq.t, out.ms.t, out.my.t})) Py_RETURN_NONE;
   const int64_t need = std::max<int64_t>(size(x.rows, k, E), 0);
   const Fresh offsets(x.t, true, at::kInt, {E + 1}), slot(x.t, true, at::kInt, {x.rows, k}),
       ws(x.t, need > 0, at::kByte, {need});
@@ -437,7 +447,7 @@ PyObject* moe_combine(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (!optional(o[3], at::kFloat, T, k, w) || !optional(o[4], at::kBFloat16, T, y.cols, add)) Py_RETURN_NONE;
   const auto entry = reinterpret_cast<decltype(&fp8bs_moe_combine)>(a.address(o[0]));
   void* stream = a.stream(o[5]);
-  if (!a.ok) Py_RETURN_NONE;
+  if (!a.ok || !here({y.t, slot, w.t, add.t})) Py_RETURN_NONE;
   const Fresh out(y.t, true, at::kBFloat16, {T, y.cols});
   return answer(entry(data<void>(y.t), type_of(f32), y.ld, y.rows, data<int32_t>(slot), data<float>(w.t), w.ld, T, k, y.cols,
                       data<void>(add.t), add.ld, out.data<void>(), y.cols, stream),
@@ -464,6 +474,7 @@ PyObject* moe_combine_bwd(PyObject*, PyObject* const* o, Py_ssize_t n) {
   if (!a.ok || rows < 0) Py_RETURN_NONE;
   Rows out(dout.t, made && with_q, made && with_dy, rows, N);
   if (!made && !out.take(o[8])) Py_RETURN_NONE;
+  if (!here({dout.t, slot, w.t, y.t, out.mq.t, out.ms.t, out.my.t})) Py_RETURN_NONE;
   if (y.t != nullptr && y.rows != out.M) Py_RETURN_NONE;
   const Fresh dw(dout.t, y.t != nullptr, at::kFloat, {T, k});
   return answers(entry(data<void>(dout.t), dout.ld, data<void>(y.t), type_of(f32), y.ld, data<int32_t>(slot),
@@ -485,7 +496,7 @@ PyObject* swiglu_bwd_quant_1x128(PyObject*, PyObject* const* o, Py_ssize_t n) {
   const auto entry = reinterpret_cast<decltype(&fp8bs_swiglu_bwd_quant_1x128)>(a.address(o[0]));
   const bool with_q = a.flag(o[4]), with_d = a.flag(o[5]), with_h = a.flag(o[6]);
   void* stream = a.stream(o[7]);
-  if (!a.ok) Py_RETURN_NONE;
+  if (!a.ok || !here({dh.t, g.t, u.t})) Py_RETURN_NONE;
   const Rows out(g.t, with_q, with_d, g.rows, 2 * g.cols);
   const Fresh h(g.t, with_h, at::kBFloat16, {g.rows, g.cols});
   return answers(entry(data<void>(dh.t), dh.ld, data<void>(g.t), g.ld, data<void>(u.t), u.ld, g.rows, g.cols, out.pq(),

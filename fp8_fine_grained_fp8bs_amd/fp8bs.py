@@ -630,6 +630,20 @@ def _vector(t, what, n, dtypes):
         raise ValueError(f"{what}: expected {n} contiguous values of {dtypes}, got {got}")
 
 
+def _here(*tensors):
+    """Refuse tensors that are not on the current device, on which the kernels run."""
+    import torch
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        _ptr(t)
+        if device is None:
+            device = torch.cuda.current_device()
+        if t.get_device() != device:
+            raise ValueError(f"tensors have to be on the current device {device}; got one on {t.device}")
+
+
 def _workspace(ws):
     """Bytes of a workspace tensor."""
     if ws is None:
@@ -668,6 +682,7 @@ def fp8bs_rmsnorm_quant_1x128(x, r, gamma, eps, h, q, s, y, rstd, stream=None):
     _check_rows(q, s, y, C, T)
     if rstd is not None:
         _vector(rstd, "rstd", T, ("float32",))
+    _here(x, r, gamma, h, q, s, y, rstd)
     _call("fp8bs_rmsnorm_quant_1x128", _ptr(x), _row_ld(x, C), _ptr(r), _row_ld(r, C), _ptr(gamma),
           _dtype(gamma, "gamma"), eps, T, C, _ptr(h), _row_ld(h, C), _ptr(q), _row_ld(q, C), _ptr(s),
           _row_ld(s, _groups(C)), _ptr(y), _row_ld(y, C), _ptr(rstd), _stream(stream))
@@ -696,6 +711,7 @@ def fp8bs_rmsnorm_bwd(dn, dres, h, gamma, rstd, dx, dgamma, ws, stream=None):
     _vector(rstd, "rstd", T, ("float32",))
     if dgamma is not None:
         _vector(dgamma, "dgamma", C, ("float32",))
+    _here(dn, dres, h, gamma, rstd, dx, dgamma, ws)
     _call("fp8bs_rmsnorm_bwd", _ptr(dn), _row_ld(dn, C), _ptr(dres), _row_ld(dres, C), _ptr(h), _row_ld(h, C),
           _ptr(gamma), _dtype(gamma, "gamma"), _ptr(rstd), T, C, _ptr(dx), _row_ld(dx, C), _ptr(dgamma), _ptr(ws),
           _workspace(ws), _stream(stream))
@@ -729,6 +745,7 @@ def fp8bs_moe_sort(ids, first, M, offsets, slot, ws, stream=None):
     assignments to experts first .. first + E - 1; ws uint8
     [>= fp8bs_moe_sort_ws(T, k, E)] (or None where that is 0)."""
     it, ldi, T, k, E = _check_ids(ids, offsets, slot)
+    _here(ids, offsets, slot, ws)
     _call("fp8bs_moe_sort", _ptr(ids), it, ldi, T, k, first, E, M, _ptr(offsets), _ptr(slot), _ptr(ws), _workspace(ws),
           _stream(stream))
 
@@ -748,6 +765,7 @@ def fp8bs_moe_gather(src, x, s_in, slot, q, s, y, stream=None):
     T, C = _check_source(src, x, s_in)
     _check(slot, "slot", (T, None), ("int32",), contiguous=True)
     M = _check_rows(q, s, y, C)
+    _here(x, s_in, slot, q, s, y)
     _call("fp8bs_moe_gather", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C,
           _ptr(slot), slot.shape[1], _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)), _ptr(y),
           _row_ld(y, C), M, _stream(stream))
@@ -760,6 +778,7 @@ def fp8bs_moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, str
     if n != T:
         raise ValueError(f"ids: {n} tokens, x has {T}")
     M = _check_rows(q, s, y, C)
+    _here(x, s_in, ids, offsets, slot, q, s, y, ws)
     _call("fp8bs_moe_dispatch", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C, _ptr(ids),
           it, ldi, k, first, E, _ptr(offsets), _ptr(slot), _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)),
           _ptr(y), _row_ld(y, C), M, _ptr(ws), _workspace(ws), _stream(stream))
@@ -775,6 +794,7 @@ def fp8bs_moe_combine(y, slot, w, add, out, stream=None):
     _optional(w, "w", (T, k), ("float32",))
     _optional(add, "add", (T, N), ("bfloat16",))
     _check(out, "out", (T, N), ("bfloat16",))
+    _here(y, slot, w, add, out)
     _call("fp8bs_moe_combine", _ptr(y), _dtype(y, "y"), _row_ld(y, N), M, _ptr(slot), _ptr(w), _row_ld(w, k), T, k, N,
           _ptr(add), _row_ld(add, N), _ptr(out), _row_ld(out, N), _stream(stream))
 
@@ -796,6 +816,7 @@ def fp8bs_moe_combine_bwd(dout, y, slot, w, q, s, dy, dw, stream=None):
     M = _check_rows(q, s, dy, N, None if q is not None or dy is not None else y.shape[0])
     if dw is not None and y.shape[0] != M:
         raise ValueError(f"y: {y.shape[0]} rows, the outputs have {M}")
+    _here(dout, y, slot, w, q, s, dy, dw)
     _call("fp8bs_moe_combine_bwd", _ptr(dout), _row_ld(dout, N), _ptr(y), OUT_BF16 if y is None else _dtype(y, "y"),
           _row_ld(y, N), _ptr(slot), _ptr(w), _row_ld(w, k), T, k, N, _ptr(q), _row_ld(q, N), _ptr(s),
           _row_ld(s, _groups(N)), _ptr(dy), _row_ld(dy, N), M, _ptr(dw), _row_ld(dw, k), _stream(stream))
@@ -812,6 +833,7 @@ def fp8bs_swiglu_bwd_quant_1x128(dh, g, u, q, s, d, h, stream=None):
     _optional(h, "h", (T, I), ("bfloat16",))
     if q is None and d is None and h is None:
         raise ValueError("no output")
+    _here(dh, g, u, q, s, d, h)
     _call("fp8bs_swiglu_bwd_quant_1x128", _ptr(dh), _row_ld(dh, I), _ptr(g), _row_ld(g, I), _ptr(u), _row_ld(u, I), T, I,
           _ptr(q), _row_ld(q, 2 * I), _ptr(s), _row_ld(s, _groups(2 * I)), _ptr(d), _row_ld(d, 2 * I), _ptr(h),
           _row_ld(h, I), _stream(stream))

@@ -204,3 +204,25 @@ BINDING = [
 def test_binding_refuses(call):
     with pytest.raises(ValueError):
         call()
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """The kernels run on the current device; a tensor of another one is refused."""
+    class On:
+        is_cuda = True
+
+        def __init__(self, index):
+            self.device = self.index = index
+
+        def data_ptr(self):
+            return A
+
+        def get_device(self):
+            return self.index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    B._here(On(1), None, On(1))
+    B._here(None)
+    for tensors in ((On(0),), (On(1), None, On(2))):
+        with pytest.raises(ValueError, match="current device"):
+            B._here(*tensors)

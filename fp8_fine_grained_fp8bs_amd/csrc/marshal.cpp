@@ -236,7 +236,7 @@ bool matrix(PyObject* o, at::ScalarType type, Matrix& m) {
   if (m.t == nullptr || m.t->stride(1) != 1) return false;
   m.rows = m.t->size(0);
   m.cols = m.t->size(1);
-  m.ld = m.rows > 1 ? m.t->stride(0) : std::max(m.t->stride(0), m.cols);
+  m.ld = m.rows > 1 ? m.t->stride(0) : m.cols;   // a single row's stride does not matter
   return true;
 }
 bool matrix(PyObject* o, at::ScalarType type, int64_t rows, int64_t cols, Matrix& m) {

@@ -605,10 +605,10 @@ def fp8bs_attn_paged(q, out, lse, q_off, kv_len, max_q, table, kc, ks, vc, vs, s
 
 
 def _row_ld(t, cols):
-    """Row stride of a checked 2-D tensor, or 0 for None (of a single row any stride will do)."""
+    """Row stride of a checked 2-D tensor (a single row's does not matter), or 0 for None."""
     if t is None:
         return 0
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    return t.stride(0) if t.shape[0] > 1 else cols
 
 
 def _optional(t, what, shape, dtypes):

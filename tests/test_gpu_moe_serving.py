@@ -159,7 +159,18 @@ def test_statuses_of_the_short_way():
             call()
 
 
-MISFITS = ("norm", "norm gradient", "dispatch", "combine", "combine gradient", "swiglu gradient")
+def test_a_single_row_of_any_stride():
+    """One token as a slice of rows whose stride breaks the alignment rules."""
+    announce("single rows")
+    C = 256
+    wide = randn(3, C + 3, seed=1).bfloat16().cuda()
+    x = torch.cat([wide[:, :C].flatten(), wide.flatten()]).as_strided((1, C), (C + 3, 1))
+    gamma, ids = torch.ones(C, device="cuda"), torch.zeros((1, 1), dtype=torch.int64, device="cuda")
+    dense = x.contiguous()
+    same(fp8bs.rmsnorm_quant_1x128(x, gamma, x), fp8bs.rmsnorm_quant_1x128(dense, gamma, dense), "norm")
+    same(fp8bs.moe_dispatch(x, ids, 1), fp8bs.moe_dispatch(dense, ids, 1), "dispatch")
+    same(fp8bs.moe_gather(x, ids.int()), fp8bs.moe_gather(dense, ids.int()), "gather")
+    same(fp8bs.swiglu_bwd_quant_1x128(x, x, x), fp8bs.swiglu_bwd_quant_1x128(dense, dense, dense), "swiglu gradient")
 
 
 def test_misfits_are_turned_back():

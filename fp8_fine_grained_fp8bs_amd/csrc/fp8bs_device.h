@@ -348,6 +348,17 @@ __device__ __forceinline__ u32x4 bf16x8_pack(const float (&f)[8]) {
                pack_bf16x2_rne(f[6], f[7])};
 }
 
+// A workgroup's number among those of its grid, permuted so that 32 neighbours
+// are on one of the 8 XCDs, which take workgroups in turn.  Rows next to each
+// other, whose scales share lines, are then mostly written through one L2:
+// 4096 x 8 rows of 7168 dispatched 71.7 us against 73.5 in plain order, gradients of 8191
+// x 2 rows 89.2 against 90.5, the norm of 4096 rows 43.7 against 44.3.
+__device__ __forceinline__ int64_t neighbours_on_an_xcd() {
+  constexpr unsigned kRow = 32, kXcds = 8, kTurn = kRow * kXcds;
+  const unsigned b = blockIdx.x, i = b / kXcds;
+  return b < gridDim.x / kTurn * kTurn ? i / kRow * kTurn + b % kXcds * kRow + i % kRow : b;
+}
+
 // Debug builds with FP8BS_POISON_LDS fill a kernel's LDS with 0xFF bytes
 // (NaN as FP32, and the NaN code as E4M3) before its first use, so that a
 // read of LDS that the kernel never wrote changes its results.  Called at

@@ -302,7 +302,7 @@ __device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, U
 template <bool CODES, int V>
 __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
   const int lane = threadIdx.x & 63;
-  const int64_t t = blockIdx.x;
+  const int64_t t = neighbours_on_an_xcd();
   const Choices chosen(p.slot + t * p.k, nullptr, p.k, p.M, lane);
   if (!chosen.any()) return;   // no row: x is not read
   for (int base = (threadIdx.x >> 6) * (512 * V); base < p.C; base += (blockDim.x >> 6) * (512 * V)) {
@@ -491,7 +491,7 @@ __global__ __launch_bounds__(V == 2 ? 1024 : 512) void moe_combine_bwd_kernel(Mo
   poison_lds<sizeof(part)>(part);
   constexpr int kAheadBwd = 8 / V, kStep = 512 * V;   // rows whose loads are in flight, columns of a wave
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int64_t t = blockIdx.x;
+  const int64_t t = neighbours_on_an_xcd();
   const Choices chosen(p.slot + t * p.k, p.w + t * p.ldw, p.k, p.M, lane);
   const bool any = chosen.any();   // without rows dout is not read
   for (int base = wave * kStep; any && base < p.N; base += waves * kStep) {

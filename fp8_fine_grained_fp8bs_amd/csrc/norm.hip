@@ -73,7 +73,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_kernel(RmsNorm p, int waves) {
   __shared__ float4 part[2][kMaxWaves / 4];
   poison_lds<sizeof(part)>(part);
   const int w = threadIdx.x >> 6;
-  const int64_t row = waves == 1 ? static_cast<int64_t>(blockIdx.x) * 4 + w : blockIdx.x;
+  const int64_t group = neighbours_on_an_xcd(), row = waves == 1 ? group * 4 + w : group;
   if (row >= p.T) return;
   const Lane at{waves, waves == 1 ? 0 : w, static_cast<int>(threadIdx.x) & 63, p.C};
   if (waves > 1) clear_tail(part, at);

@@ -298,14 +298,19 @@ __device__ __forceinline__ void store_unit(const MoeRows& p, const Columns& c, U
   }
 }
 
-// CODES: x holds codes with scales
+// Narrow rows (V == 1: up to 512 columns) are a wave's; four such tokens are a
+// workgroup.
+constexpr int kTogether = 4;
+
+// CODES: x holds codes with scales.
 template <bool CODES, int V>
 __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = neighbours_on_an_xcd();
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wave = V == 1 ? 0 : w, waves = V == 1 ? 1 : blockDim.x >> 6;
+  const int64_t t = V == 1 ? neighbours_on_an_xcd() * kTogether + w : neighbours_on_an_xcd();
+  if (t >= p.T) return;
   const Choices chosen(p.slot + t * p.k, nullptr, p.k, p.M, lane);
   if (!chosen.any()) return;   // no row: x is not read
-  for (int base = (threadIdx.x >> 6) * (512 * V); base < p.C; base += (blockDim.x >> 6) * (512 * V)) {
+  for (int base = wave * (512 * V); base < p.C; base += waves * (512 * V)) {
     const Columns c{base + lane * 8, p.C};
     Unit<V> u;
     load_unit<CODES, V>(p, t, c, u);
@@ -313,87 +318,90 @@ __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
   }
 }
 
-// Few assignments: sort and rows in one launch.  A workgroup a token holds all
-// assignments as keys (expert, number) in LDS and counts the smaller ones for
-// each of its own, which is that one's row: 256 comparisons of a wave a step.
-// One more workgroup counts the experts' offsets.  256 tokens to 8 experts: 9.5 us
-// against 12.8 in two launches, 1024 to 2 7.1 against 9.9, 2048 to 1 level; 4096
-// assignments 12.7 and more against 12.5 and less (but for rows of 7168).
-constexpr int kFew = 2048;
-__device__ __forceinline__ uint32_t order_key(int e, int i) {
-  return e >= 0 ? (static_cast<uint32_t>(e) << 20) | static_cast<uint32_t>(i) : 0xffffffffu;
-}
-static_assert(kMaxExperts <= 2048 && kFew <= (1 << 20) && kFew % 256 == 0, "a key's 32 bits, whole steps");
-static_assert(kMaxExperts <= kFew, "counts in the keys' place");
+// Up to kOneLaunch assignments: sort and rows in one launch.  A workgroup takes
+// a few tokens, with at most 64 assignments, and counts all assignments by
+// expert for itself (those before its own apart), which gives its own rows as
+// in the sort above; their ranks are one wave's ballots.
+constexpr int kOneLaunch = 8192;
 
 template <bool CODES>
-__global__ __launch_bounds__(1024) void moe_few_kernel(MoeIds ids, MoeRows p) {
-  __shared__ uint4 keys[kFew / 4];
-  __shared__ int32_t slot[kMaxChoices];
-  __shared__ int sums[16];
-  poison_lds<sizeof(keys)>(keys);
-  poison_lds<sizeof(slot)>(slot);
+__global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, MoeRows p, int tokens, int bits) {
+  __shared__ int total[kMaxExperts];
+  __shared__ int start[kMaxExperts];
+  __shared__ int sums[kSortWaves];
+  __shared__ int32_t slots[64];
+  poison_lds<sizeof(total)>(total);
+  poison_lds<sizeof(start)>(start);
   poison_lds<sizeof(sums)>(sums);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int n = static_cast<int>(ids.T) * ids.k;
-  const int64_t t = blockIdx.x;
-  if (t == ids.T) {
-    int* count = reinterpret_cast<int*>(keys);   // kMaxExperts at most
-    for (int e = tid; e < ids.E; e += blockDim.x) count[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += blockDim.x) {
-      const int e = expert_of(ids, i);
-      if (e >= 0) atomicAdd(&count[e], 1);
-    }
-    __syncthreads();
-    int done = 0;
-    for (int e0 = 0; e0 < ids.E; e0 += blockDim.x) {
-      const int e = e0 + tid;
-      int all;
-      const int first = done + exclusive_sum(e < ids.E ? count[e] : 0, sums, all);
-      if (e < ids.E) ids.offsets[e] = first < ids.M ? first : static_cast<int32_t>(ids.M);
-      done += all;
-      __syncthreads();
-    }
-    if (tid == 0) ids.offsets[ids.E] = done < ids.M ? done : static_cast<int32_t>(ids.M);
-    return;
-  }
-  // the first columns are on their way while the slots are counted
-  const Columns first{wave * 1024 + lane * 8, p.C};
+  poison_lds<sizeof(slots)>(slots);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int T = static_cast<int>(ids.T), n = T * ids.k;
+  const int t0 = blockIdx.x * tokens, here = T - t0 < tokens ? T - t0 : tokens;
+  const int a = t0 * ids.k, b = a + here * ids.k;
+  const int chunks = (p.C + 1023) / 1024, items = here * chunks;
+  // the first columns are on their way while the rows are counted
   Unit<2> u;
-  if (wave * 1024 < p.C) load_unit<CODES, 2>(p, t, first, u);
-  uint32_t* key = reinterpret_cast<uint32_t*>(keys);
-  const int steps = (n + 255) / 256;
-  for (int i = tid; i < steps * 256; i += blockDim.x) key[i] = i < n ? order_key(expert_of(ids, i), i) : 0xffffffffu;
-  __syncthreads();
-  for (int j = wave; j < ids.k; j += waves) {
-    const int i = static_cast<int>(t) * ids.k + j;
-    const uint32_t own = __builtin_amdgcn_readfirstlane(key[i]);
-    int before = 0;
-    for (int o = 0; o < steps; ++o) {
-      const uint4 x = keys[o * 64 + lane];
-      before += __popcll(__ballot(x.x < own)) + __popcll(__ballot(x.y < own)) + __popcll(__ballot(x.z < own)) +
-                __popcll(__ballot(x.w < own));
-    }
-    const int at = own != 0xffffffffu && before < ids.M ? before : -1;
-    if (lane == 0) {
-      slot[j] = at;
-      ids.slot[i] = at;
-    }
+  if (wave < items) load_unit<CODES, 2>(p, t0 + wave / chunks, Columns{wave % chunks * 1024 + lane * 8, p.C}, u);
+  for (int e = tid; e < ids.E; e += kSortThreads) {
+    total[e] = 0;
+    start[e] = 0;
   }
   __syncthreads();
-  const Choices chosen(slot, nullptr, ids.k, p.M, lane);
-  if (wave * 1024 < p.C) store_unit<CODES, 2>(p, first, u, chosen, lane);
-  for (int base = (wave + waves) * 1024; base < p.C; base += waves * 1024) {
-    const Columns c{base + lane * 8, p.C};
-    load_unit<CODES, 2>(p, t, c, u);
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSortThreads) {
+    const int e = expert_of(ids, i);
+    if (e >= 0) atomicAdd(i < a ? &start[e] : &total[e], 1);
+  }
+  __syncthreads();
+  {
+    int mine[kPerThread], sum = 0, all;
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      const int e = tid * kPerThread + x;
+      mine[x] = e < ids.E ? total[e] + start[e] : 0;
+      sum += mine[x];
+    }
+    int first = exclusive_sum(sum, sums, all);
+#pragma unroll
+    for (int x = 0; x < kPerThread; ++x) {
+      const int e = tid * kPerThread + x;
+      if (e < ids.E) {
+        start[e] += first;
+        if (blockIdx.x == 0) ids.offsets[e] = first < ids.M ? first : static_cast<int32_t>(ids.M);
+      }
+      first += mine[x];
+    }
+    if (blockIdx.x == 0 && tid == 0) ids.offsets[ids.E] = all < ids.M ? all : static_cast<int32_t>(ids.M);
+  }
+  __syncthreads();
+  if (wave == 0) {
+    const int e = a + lane < b ? expert_of(ids, a + lane) : -1;
+    uint64_t same = __ballot(e >= 0);
+    for (int bit = 0; bit < bits; ++bit) {
+      const uint64_t ones = __ballot((e >> bit) & 1);
+      same &= (e >> bit) & 1 ? ones : ~ones;
+    }
+    const int row = e >= 0 ? start[e] + __popcll(same & ((uint64_t(1) << lane) - 1)) : -1;
+    const int at = row < ids.M ? row : -1;
+    slots[lane] = at;
+    if (a + lane < b) ids.slot[a + lane] = at;
+  }
+  __syncthreads();
+  for (int item = wave; item < items; item += kSortWaves) {
+    const int token = item / chunks;
+    const Columns c{(item - token * chunks) * 1024 + lane * 8, p.C};
+    const Choices chosen(slots + token * ids.k, nullptr, ids.k, p.M, lane);
+    if (item != wave) {
+      if (!chosen.any()) continue;   // no row: x is not read
+      load_unit<CODES, 2>(p, t0 + token, c, u);
+    }
     store_unit<CODES, 2>(p, c, u, chosen, lane);
   }
 }
 
 // ---------------------------------------------------------------------
 // Rows back: out[t] = add[t] + sum over j of w[t][j] y[slot[t][j]], j
-// ascending, one FMA a row in FP32.  A wave takes 1024 columns of a token, two
+// ascending, one FMA a row in FP32.  A wave takes 512 V columns of a token, V
 // vectors of 8 a lane, with up to kAhead rows' loads in flight.
 // ---------------------------------------------------------------------
 constexpr int kAhead = 8;
@@ -427,23 +435,23 @@ __device__ __forceinline__ void values8(const Values8<F32>& v, float (&f)[8]) {
   }
 }
 
-template <bool F32>
-__global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chunks) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 2 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <bool F32, int V>
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeCombine p, int chunks) {
+  const int64_t item = neighbours_on_an_xcd() * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = item <= 0xffffffffll ? static_cast<uint32_t>(item) / static_cast<uint32_t>(chunks) : item / chunks;
   if (t >= p.T) return;
   const int lane = threadIdx.x & 63;
-  const Columns c{static_cast<int>(item - t * chunks) * 1024 + lane * 8, p.N};
+  const Columns c{static_cast<int>(item - t * chunks) * (512 * V) + lane * 8, p.N};
   const Choices chosen(p.slot + t * p.k, p.w != nullptr ? p.w + t * p.ldw : nullptr, p.k, p.M, lane);
-  float acc[2][8];
+  float acc[V][8];
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
+  for (int v = 0; v < V; ++v) {
     u32x4 add{0u, 0u, 0u, 0u};
     if (p.add != nullptr) add = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p.add + t * p.ldadd + c.from(v)));
     bf16x8_unpack(add, acc[v]);
   }
   for (int j0 = 0; j0 < p.k; j0 += kAhead) {
-    Values8<F32> x[kAhead][2];
+    Values8<F32> x[kAhead][V];
     bool there[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -451,14 +459,14 @@ __global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chun
       there[j] = chosen.there(row);
       if (!there[j]) continue;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
+      for (int v = 0; v < V; ++v) x[j][v] = load8<F32>(p.y, row * p.ldy + c.from(v));
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (!there[j]) continue;
       const float w = chosen.w(j0 + j);
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
+      for (int v = 0; v < V; ++v) {
         float f[8];
         values8<F32>(x[j][v], f);
 #pragma unroll
@@ -467,7 +475,7 @@ __global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chun
     }
   }
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
+  for (int v = 0; v < V; ++v) {
     if (!c.in(v)) continue;
     u32x4* out = reinterpret_cast<u32x4*>(p.out + t * p.ldo + c.at(v));
     const u32x4 x = bf16x8_pack(acc[v]);
@@ -483,15 +491,17 @@ __global__ __launch_bounds__(128) void moe_combine_kernel(MoeCombine p, int chun
 // Gradient of the way back: dy[slot] = w dout[t] as codes (dout's tile is
 // quantized once; a row's scales are those of dout times |w|, its signs those
 // of w dout) and in BF16, dw[t][j] = dout[t] . y[slot].  A workgroup a token,
-// every wave has columns in its first turn.
+// whose waves all have columns in their first turn, or four tokens of a wave
+// each, whose row is then one turn.
 // ---------------------------------------------------------------------
 template <bool F32, int V>
-__global__ __launch_bounds__(V == 2 ? 1024 : 512) void moe_combine_bwd_kernel(MoeCombineBwd p) {
+__global__ __launch_bounds__(V == 4 ? 512 : 1024) void moe_combine_bwd_kernel(MoeCombineBwd p) {
   __shared__ float part[kMaxChoices][16];
   poison_lds<sizeof(part)>(part);
   constexpr int kAheadBwd = 8 / V, kStep = 512 * V;   // rows whose loads are in flight, columns of a wave
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
-  const int64_t t = neighbours_on_an_xcd();
+  const int tid = threadIdx.x, lane = tid & 63, w0 = tid >> 6, wave = V == 1 ? 0 : w0, waves = V == 1 ? 1 : blockDim.x >> 6;
+  const int64_t t = V == 1 ? neighbours_on_an_xcd() * kTogether + w0 : neighbours_on_an_xcd();
+  if (t >= p.T) return;
   const Choices chosen(p.slot + t * p.k, p.w + t * p.ldw, p.k, p.M, lane);
   const bool any = chosen.any();   // without rows dout is not read
   for (int base = wave * kStep; any && base < p.N; base += waves * kStep) {
@@ -534,7 +544,11 @@ __global__ __launch_bounds__(V == 2 ? 1024 : 512) void moe_combine_bwd_kernel(Mo
             dot += c.in(v) ? s : 0.0f;
           }
           dot = wave_sum(dot);
-          if (lane == 0) part[j0 + j][wave] = base == wave * kStep ? dot : part[j0 + j][wave] + dot;
+          if (V == 1) {
+            if (lane == 0) p.dw[t * p.lddw + j0 + j] = dot;
+          } else if (lane == 0) {
+            part[j0 + j][wave] = base == wave * kStep ? dot : part[j0 + j][wave] + dot;
+          }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -556,6 +570,10 @@ __global__ __launch_bounds__(V == 2 ? 1024 : 512) void moe_combine_bwd_kernel(Mo
     }
   }
   if (p.dw == nullptr) return;
+  if (V == 1) {
+    if (lane < p.k && !chosen.there(chosen.slot)) p.dw[t * p.lddw + lane] = 0.0f;
+    return;
+  }
   __syncthreads();
   for (int j = tid; j < p.k; j += blockDim.x) {
     const int64_t row = p.slot[t * p.k + j];
@@ -579,6 +597,23 @@ Stretches stretches_of(int64_t n, int E) {
   return {each * kRound, n > 0 ? static_cast<int>((rounds + each - 1) / each) : 1};
 }
 
+// A launch by token, V vectors a lane and at most so many waves.
+struct Tokens {
+  dim3 grid, block;
+};
+Tokens tokens_of(int64_t T, int columns, int V, int most) {
+  if (V == 1) return {dim3(static_cast<unsigned>((T + kTogether - 1) / kTogether)), dim3(64 * kTogether)};
+  const int waves = (columns + 512 * V - 1) / (512 * V);
+  return {dim3(static_cast<unsigned>(T)), dim3(64 * (waves > most ? most : waves))};
+}
+
+// Bits of an expert's number.
+int id_bits(int E) {
+  int bits = 0;
+  while ((E - 1) >> bits) ++bits;
+  return bits;
+}
+
 }  // namespace
 
 int64_t moe_sort_ws(int64_t T, int k, int E) {
@@ -589,8 +624,6 @@ int64_t moe_sort_ws(int64_t T, int k, int E) {
 hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st) {
   const int64_t n = p.T * p.k;
   const Stretches s = stretches_of(n, p.E);
-  int bits = 0;
-  while ((p.E - 1) >> bits) ++bits;
   int32_t* counts = nullptr;
   if (n > kCountHere) {
     counts = p.ws;
@@ -598,30 +631,34 @@ hipError_t launch_moe_sort(const MoeIds& p, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(moe_place_kernel, dim3(s.count), dim3(kSortThreads), 0, st, p, n, s.length, s.count, bits, counts);
+  hipLaunchKernelGGL(moe_place_kernel, dim3(s.count), dim3(kSortThreads), 0, st, p, n, s.length, s.count, id_bits(p.E),
+                     counts);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
   // four vectors a lane for wide rows in BF16 (8192 tokens of 7168 to 32 of 256 experts
-  // 28.9 us against 31.8, all of them to 2 of 8 level), two for narrow ones and for
-  // codes, whose lanes have nothing to compute (4096 x 8 rows of 7168: 70.5 us against 73.8)
-  const bool wide = !p.codes_in && p.C >= 2048;
-  const int step = wide ? 2048 : 1024, waves = (p.C + step - 1) / step;
-  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * (waves > 16 ? 16 : waves));
-  if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true, 2>), grid, block, 0, st, p);
-  else if (wide) hipLaunchKernelGGL((moe_gather_kernel<false, 4>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((moe_gather_kernel<false, 2>), grid, block, 0, st, p);
+  // 28.9 us against 31.8, all of them to 2 of 8 level), two for narrower ones and for
+  // codes, whose lanes have nothing to compute (4096 x 8 rows of 7168: 70.5 us against
+  // 73.8); one where a row has no more
+  const int V = p.C <= 512 ? 1 : p.codes_in || p.C < 2048 ? 2 : 4;
+  const Tokens g = tokens_of(p.T, p.C, V, 16);
+  if (p.codes_in && V == 1) hipLaunchKernelGGL((moe_gather_kernel<true, 1>), g.grid, g.block, 0, st, p);
+  else if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true, 2>), g.grid, g.block, 0, st, p);
+  else if (V == 1) hipLaunchKernelGGL((moe_gather_kernel<false, 1>), g.grid, g.block, 0, st, p);
+  else if (V == 2) hipLaunchKernelGGL((moe_gather_kernel<false, 2>), g.grid, g.block, 0, st, p);
+  else hipLaunchKernelGGL((moe_gather_kernel<false, 4>), g.grid, g.block, 0, st, p);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st) {
-  if (ids.T * ids.k <= kFew) {
-    int waves = (p.C + 1023) / 1024;
-    waves = waves < 4 ? 4 : waves > 16 ? 16 : waves;
-    const dim3 grid(static_cast<unsigned>(ids.T + 1)), block(64 * waves);
-    if (p.codes_in) hipLaunchKernelGGL((moe_few_kernel<true>), grid, block, 0, st, ids, p);
-    else hipLaunchKernelGGL((moe_few_kernel<false>), grid, block, 0, st, ids, p);
+  if (ids.T * ids.k <= kOneLaunch) {
+    // enough workgroups for the compute units
+    const int T = static_cast<int>(ids.T), most = 64 / ids.k;
+    const int each = (T + 511) / 512, tokens = each < most ? each : most;
+    const dim3 grid((T + tokens - 1) / tokens), block(kSortThreads);
+    if (p.codes_in) hipLaunchKernelGGL((moe_dispatch_kernel<true>), grid, block, 0, st, ids, p, tokens, id_bits(ids.E));
+    else hipLaunchKernelGGL((moe_dispatch_kernel<false>), grid, block, 0, st, ids, p, tokens, id_bits(ids.E));
     return hipGetLastError();
   }
   const hipError_t e = launch_moe_sort(ids, st);
@@ -629,26 +666,37 @@ hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t 
 }
 
 hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st) {
-  const int chunks = (p.N + 1023) / 1024;
-  const int64_t blocks = (p.T * chunks + 1) / 2;
+  const bool narrow = p.N <= 512;
+  const int chunks = narrow ? 1 : (p.N + 1023) / 1024;
+  const int64_t blocks = (p.T * chunks + 3) / 4;
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(128);
-  if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true>), grid, block, 0, st, p, chunks);
-  else hipLaunchKernelGGL((moe_combine_kernel<false>), grid, block, 0, st, p, chunks);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
+  if (p.y_f32 && narrow) hipLaunchKernelGGL((moe_combine_kernel<true, 1>), grid, block, 0, st, p, chunks);
+  else if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, 2>), grid, block, 0, st, p, chunks);
+  else if (narrow) hipLaunchKernelGGL((moe_combine_kernel<false, 1>), grid, block, 0, st, p, chunks);
+  else hipLaunchKernelGGL((moe_combine_kernel<false, 2>), grid, block, 0, st, p, chunks);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st) {
   if (p.T > 0x7fffffff) return hipErrorInvalidValue;
   // four vectors a lane where there are tokens enough (1024 x 8 rows of 7168: 33.7 us
-  // against 37.9, 8191 x 2 90.7 against 91.8), two for few (16 x 8: 8.1 against 9.0)
-  const bool many = p.T >= 512;
-  const int step = many ? 2048 : 1024, most = many ? 8 : 16, waves = (p.N + step - 1) / step;
-  const dim3 grid(static_cast<unsigned>(p.T)), block(64 * (waves > most ? most : waves));
-  if (p.y_f32 && many) hipLaunchKernelGGL((moe_combine_bwd_kernel<true, 4>), grid, block, 0, st, p);
-  else if (p.y_f32) hipLaunchKernelGGL((moe_combine_bwd_kernel<true, 2>), grid, block, 0, st, p);
-  else if (many) hipLaunchKernelGGL((moe_combine_bwd_kernel<false, 4>), grid, block, 0, st, p);
-  else hipLaunchKernelGGL((moe_combine_bwd_kernel<false, 2>), grid, block, 0, st, p);
+  // against 37.9, 8191 x 2 90.7 against 91.8), two for few (16 x 8: 8.1 against 9.0);
+  // one where a row has no more
+  const int V = p.N <= 512 ? 1 : p.T >= 512 && p.N > 1024 ? 4 : 2;
+  const Tokens g = tokens_of(p.T, p.N, V, V == 4 ? 8 : 16);
+#define FP8BS_COMBINE(F32, V) \
+  hipLaunchKernelGGL((moe_combine_bwd_kernel<F32, V>), g.grid, g.block, 0, st, p)
+  if (p.y_f32) {
+    if (V == 1) FP8BS_COMBINE(true, 1);
+    else if (V == 2) FP8BS_COMBINE(true, 2);
+    else FP8BS_COMBINE(true, 4);
+  } else {
+    if (V == 1) FP8BS_COMBINE(false, 1);
+    else if (V == 2) FP8BS_COMBINE(false, 2);
+    else FP8BS_COMBINE(false, 4);
+  }
+#undef FP8BS_COMBINE
   return hipGetLastError();
 }
 

@@ -96,13 +96,14 @@ def codes_of(x):
     return torch.from_numpy(q), torch.from_numpy(s)
 
 
-# around the largest counts of one launch (2048) and of two (8192), widths around a wave's and a
-# workgroup's columns
+# around the largest count of one launch (8192), several tokens a workgroup with a short last one,
+# widths around a lane's vectors, a wave's and a workgroup's columns
 DISPATCHES = [(1, 1, 128, 1, 1, None), (1, 8, 7168, 64, 64, None), (16, 8, 7168, 64, 64, None), (3, 5, 1152, 9, 4, None),
               (256, 8, 256, 32, 32, None), (257, 8, 256, 32, 32, None), (683, 3, 384, 16, 16, 900),
               (2, 64, 640, 16, 16, None), (9, 2, 16512, 4, 4, None), (1500, 2, 1024, 8, 8, None),
               (700, 6, 16512, 160, 20, None), (40, 8, 128, 1024, 1024, None),
-              (1025, 8, 128, 256, 256, None)]
+              (1025, 8, 128, 256, 256, None), (1024, 8, 512, 256, 256, None), (521, 15, 640, 20, 20, None),
+              (1200, 7, 512, 16, 16, None), (3000, 3, 1024, 8, 8, None), (900, 9, 2048, 8, 2, None)]
 
 
 @pytest.mark.parametrize("T,k,C,of,E,rows", DISPATCHES)
@@ -148,7 +149,7 @@ def test_dispatch(T, k, C, of, E, rows):
     assert torch.equal(out[0].cpu(), want_q) and torch.equal(out[1].cpu(), want_s)
 
 
-COMBINES = [(1, 1, 128, 1, 1), (16, 8, 7168, 64, 64), (5, 3, 640, 8, 3), (300, 2, 1152, 8, 8), (33, 64, 256, 16, 16),
+COMBINES = [(1, 1, 128, 1, 1), (50, 3, 512, 8, 8), (600, 9, 128, 8, 8), (16, 8, 7168, 64, 64), (5, 3, 640, 8, 3), (300, 2, 1152, 8, 8), (33, 64, 256, 16, 16),
             (7, 9, 384, 20, 20), (1030, 8, 512, 60, 30)]
 
 
@@ -189,7 +190,7 @@ def test_combine(T, k, N, of, E, kind):
                 assert (wide[T] == 4).all() and (wide[:, N:] == 4).all()
 
 
-GRADIENTS = [(1, 1, 128, 1, 1), (77, 4, 1152, 16, 16), (16, 8, 7168, 64, 40), (5, 64, 640, 8, 8), (9, 2, 16512, 4, 4),
+GRADIENTS = [(1, 1, 128, 1, 1), (50, 9, 512, 8, 8), (600, 17, 128, 8, 8), (520, 3, 2176, 8, 8), (512, 2, 16512, 4, 4), (77, 4, 1152, 16, 16), (16, 8, 7168, 64, 40), (5, 64, 640, 8, 8), (9, 2, 16512, 4, 4),
              (700, 3, 1024, 8, 8), (3, 5, 2048, 8, 2)]
 
 

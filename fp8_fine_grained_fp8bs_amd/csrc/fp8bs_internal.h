@@ -127,6 +127,9 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st);
 // Working memory of launch_attn_paged: a function of the sizes alone.
 int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page);
 
+// A grid's threads are numbered in 32 bits.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= 0xffffffffll / threads; }
+
 // Arguments of fp8bs_rmsnorm_quant_1x128 (r, q, y, rstd may be null; q with s, r with h).
 struct RmsNorm {
   const uint16_t* x;

@@ -9,7 +9,13 @@
 // With a = gamma dn and u = h rstd the gradient is
 //   dx = dres + rstd (a - u mean(a u)),   dgamma = sum over the rows of dn u.
 // Both move a few bytes a value for about ten operations: HBM-bound.  A row is
-// read once and stays in registers between its sum and its output.
+// read once and stays in registers between its sum and its output.  Measured,
+// per call in a stream of calls:
+//   4096 x 7168 with residual, codes, BF16 norm and row factors: 265 MB, 43.8 us,
+//     6.1 TB/s (a kernel that only moves as many bytes in this mix: 44.5);
+//     5 rows 6.5 us, 4.0 in the kernel
+//   gradient of 8191 x 7168 with dres: 470 MB, 79.0 us, 76 in the kernel (moving alone:
+//     75 to 78) and 4.7 in the sum of dgamma's parts; 131 x 1280 5.5 us, one launch
 #include <hip/hip_runtime.h>
 
 #include "fp8bs_device.h"
@@ -333,7 +339,9 @@ hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t st) {
   const bool narrow = p.C <= 512;
   const int waves = row_waves(p.C, narrow ? 1 : 2);
   const int64_t blocks = waves == 1 ? (p.T + 3) / 4 : p.T;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(waves == 1 ? 256 : 64 * waves);
+  const int threads = waves == 1 ? 256 : 64 * waves;
+  if (!grid_fits(blocks, threads)) return hipErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
 #define FP8BS_NORM(V, RES) hipLaunchKernelGGL((rmsnorm_kernel<V, RES>), grid, block, 0, st, p, waves)
   if (narrow && p.r != nullptr) FP8BS_NORM(1, true);
   else if (narrow) FP8BS_NORM(1, false);

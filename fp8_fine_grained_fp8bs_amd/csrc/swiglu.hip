@@ -147,6 +147,8 @@ __global__ __launch_bounds__(256) void swiglu_quant_kernel(const uint16_t* __res
 // as codes with 1x128 scales (the input gradient's operand) and in BF16 (the
 // weight gradient's source), and optionally h again.  A DPP row takes one tile
 // of dh, g and u, 8 values a lane, and gives one tile of dg and one of du.
+// HBM-bound: 16384 x 2048 with codes, BF16 gradients and h, 472 MB, 68.9 us, 6.8
+// TB/s; 33 rows 6.0 us, 3.1 in the kernel.
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
   const int sub = threadIdx.x & 15;
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
@@ -189,6 +191,9 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
   }
   if (p.d != nullptr) {
     uint16_t* out = p.d + t * p.ldd + c;
+    // past the caches: what reads them next, the weights' gradient, comes after the
+    // input gradient's product (69.0 us against 79.7 with plain stores; with that
+    // product and the re-quantization behind it 573 against 580)
     __builtin_nontemporal_store(bf16x8_pack(g), reinterpret_cast<u32x4*>(out));
     __builtin_nontemporal_store(bf16x8_pack(u), reinterpret_cast<u32x4*>(out + p.I));
   }
@@ -200,7 +205,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
 hipError_t launch_swiglu_bwd(const SwigluBwd& p, hipStream_t st) {
   const int G = static_cast<int>(p.I / 128);
   const int64_t blocks = (p.T * G + 15) / 16;
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+  if (!grid_fits(blocks, 256)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, G);
   return hipGetLastError();
 }

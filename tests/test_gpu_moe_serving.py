@@ -217,3 +217,50 @@ def test_poisoned_lds():
         finally:
             fp8bs.use_library(prev)
     ts.test_edge_gates()
+
+
+def wide(t, extra, value):
+    """The tensor as a part of wider rows."""
+    w = torch.full((t.shape[0], t.shape[1] + extra), value, dtype=t.dtype, device="cuda")
+    w[:, :t.shape[1]] = t
+    return w[:, :t.shape[1]]
+
+
+def test_every_input_in_wider_rows():
+    announce("inputs in wider rows")
+    T, k, C, E = 130, 3, 640, 7
+    x, dout = tm.tokens(T, C, 1).cuda(), tm.tokens(T, C, 2).cuda()
+    ids, w = tm.choices(T, k, E, 1).cuda(), torch.rand((T, k), device="cuda")
+    offsets, slot = fp8bs.moe_sort(wide(ids, 5, 3), E)
+    same((offsets, slot), fp8bs.moe_sort(ids, E), "sort")
+    n = int(offsets[-1])
+    y = randn(T * k, C, seed=3).cuda()
+    cut = lambda out: tuple(t if t is None or t.shape[0] != T * k else t[:n] for t in out)  # noqa: E731
+    q, s, _ = fp8bs.moe_gather(x, slot)
+    q, s = q[:T].clone(), s[:T].clone()
+    same(cut(fp8bs.moe_gather(wide(q, 32, 1), slot, s_in=wide(s, 3, 9.0))), cut(fp8bs.moe_gather(q, slot, s_in=s)), "gather")
+    same(cut(fp8bs.moe_dispatch(wide(q, 32, 1), ids, E, s_in=wide(s, 3, 9.0))), cut(fp8bs.moe_dispatch(q, ids, E, s_in=s)),
+         "dispatch")
+    for rows in (y, y.bfloat16()):
+        same(fp8bs.moe_combine(wide(rows, 8, 1.0), slot, wide(w, 5, 7.0), wide(x, 24, 1.0)),
+             fp8bs.moe_combine(rows, slot, w, x), "combine")
+        same(cut(fp8bs.moe_combine_bwd(wide(dout, 8, 1.0), slot, wide(w, 1, 7.0), wide(rows, 16, 1.0), with_dy=True)),
+             cut(fp8bs.moe_combine_bwd(dout, slot, w, rows, with_dy=True)), "combine gradient")
+    same(fp8bs.swiglu_bwd_quant_1x128(wide(dout, 40, 1.0), wide(x, 8, 1.0), wide(y.bfloat16()[:T], 16, 1.0), with_d=True),
+         fp8bs.swiglu_bwd_quant_1x128(dout, x, y.bfloat16()[:T], with_d=True), "swiglu gradient")
+
+
+@pytest.mark.parametrize("T", [3, 400, 1500])
+def test_more_rows_than_assignments(T):
+    """Buffers larger than every case needs: the rows behind the last stay."""
+    announce(f"more rows than assignments, T {T}")
+    k, C, E = 4, 256, 9
+    x, ids = tm.tokens(T, C, 1).cuda(), tm.choices(T, k, E, 2).cuda()
+    few = fp8bs.moe_dispatch(x, ids, E)
+    n = int(few[3][-1])
+    out = (torch.full((T * k + 50, C), 0x5A, dtype=torch.uint8, device="cuda"), torch.full((T * k + 50, C // 128), -1.0, device="cuda"),
+           None)
+    q, s, _, offsets, slot = fp8bs.moe_dispatch(x, ids, E, out=out)
+    assert torch.equal(offsets, few[3]) and torch.equal(slot, few[4])
+    assert torch.equal(q[:n], few[0][:n]) and torch.equal(s[:n], few[1][:n])
+    assert (q[n:] == 0x5A).all() and (s[n:] == -1).all()

@@ -92,6 +92,20 @@ def test_norm_edges():
     assert (s[0] == 0).all() and (s[1, 1:] == 0).all() and (q[0] & 127 == 0).all()
 
 
+def test_norm_of_tiny_weights():
+    """Scales below 2^-100 (the encoder's slow path) and outputs down to FP32's
+    subnormals, whose products are off by up to 2^-149 each."""
+    native_loaded()
+    T, C = 9, 512
+    announce("norm, tiny weights")
+    x = rows_of(T, C, 1)
+    gamma = gamma_of(C, "f32", 2) * torch.tensor([2.0 ** -60, 2.0 ** -110, 2.0 ** -125, 2.0 ** -138]).repeat_interleave(128)
+    q, s, _, y, _ = fp8bs.rmsnorm_quant_1x128(x.cuda(), gamma.cuda(), with_y=True)
+    n, _ = norm(x, gamma, 1e-6)
+    check_bf16("y", y, n, 26 * U * n.abs() + 2.0 ** -149)
+    check_tiles("codes", q, s, n, 26 * U * n.abs() + 2.0 ** -149)
+
+
 @pytest.mark.parametrize("which", ["x", "r"])
 @pytest.mark.parametrize("T,C", [(6, 384), (300, 4096)])
 def test_norm_in_place(which, T, C):

@@ -78,6 +78,20 @@ def test_edge_gates():
     assert (s[7] == 0).all() and (s[6, :2] == 0).all()
 
 
+def test_tiny_gradients():
+    """Scales below 2^-100: the encoder's slow path."""
+    native_loaded()
+    announce("swiglu gradient, tiny")
+    T, I = 5, 256
+    up, dh = halves(T, I, 1), (randn(T, I, seed=2) * 2.0 ** -112).bfloat16()
+    q, s, d, _ = fp8bs.swiglu_bwd_quant_1x128(dh.cuda(), up[:, :I].cuda(), up[:, I:].cuda(), with_d=True)
+    dg, du, _ = swiglu_grads(dh, up[:, :I], up[:, I:])
+    eg, eu, _ = (e + 2.0 ** -149 for e in allowances(dh, up[:, :I], up[:, I:]))
+    check_bf16("dg", d[:, :I], dg, eg)
+    check_bf16("du", d[:, I:], du, eu)
+    check_tiles("codes", q, s, torch.cat([dg, du], 1), torch.cat([eg, eu], 1))
+
+
 def test_against_differences():
     """Central differences of the binary64 SwiGLU along a direction: steps of
     1e-5 leave under 1e-8 of the magnitudes, the outputs' rounding 2^-8."""

@@ -487,8 +487,8 @@ int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int
  *                                   values); both or neither
  *   y      bf16 [T][ldy] or NULL    n rounded to BF16
  *   rstd   f32 [T] or NULL          for fp8bs_rmsnorm_bwd
- * At least one of q and y.  T >= 0 (0 is a no-op), C > 0, C % 128 == 0 and
- * C <= 16384, else FP8BS_ERR_UNSUPPORTED_SHAPE; eps > 0 and finite.  gamma
+ * At least one of q and y; q, s, y and rstd must not overlap the inputs.
+ * T >= 0 (0 is a no-op), C > 0, C % 128 == 0 and C <= 16384, else FP8BS_ERR_UNSUPPORTED_SHAPE; eps > 0 and finite.  gamma
  * 16-byte aligned.  Rows whose sum of squares passes FP32's range (values near
  * 10^19) are outside the contract.
  */
@@ -557,8 +557,8 @@ int64_t fp8bs_moe_sort_ws(int64_t T, int64_t k, int64_t E);
  *   slot   i32 [T][k] of fp8bs_moe_sort, in device memory and not checked: rows
  *          outside 0 .. M-1 are never followed
  *   q, s   u8 [M][ldq], f32 [M][lds]   y bf16 [M][ldy] or NULL
- * Rows that no slot names are left as they were.  Its gradient is
- * fp8bs_moe_combine without weights.  T >= 0 (0 is a no-op), 0 < k <= 64, C > 0 and
+ * Outputs must not overlap inputs.  Rows that no slot names are left as they
+ * were.  Its gradient is fp8bs_moe_combine without weights.  T >= 0 (0 is a no-op), 0 < k <= 64, C > 0 and
  * C % 128 == 0, T and M < 2^31.
  */
 fp8bs_status fp8bs_moe_gather(fp8bs_requant_src src, const void *x, int64_t ldx, const float *s_in, int64_t lds_in,
@@ -599,8 +599,8 @@ fp8bs_status fp8bs_moe_combine(const void *y, fp8bs_out_dtype yt, int64_t ldy, i
  *   dy    bf16 [M][lddy] or NULL     w dout, rounded once
  *   dw    f32 [T][lddw] or NULL      FP32 sums in a fixed order; 0 without a row
  *   y     bf16 or f32 [M][ldy] by yt; ignored (may be NULL) without dw
- * At least one output.  Rows that no slot names are left as they were.  Sizes as for
- * fp8bs_moe_combine.
+ * At least one output, none overlapping an input.  Rows that no slot names are left as
+ * they were.  Sizes as for fp8bs_moe_combine.
  */
 fp8bs_status fp8bs_moe_combine_bwd(const void *dout, int64_t lddo, const void *y, fp8bs_out_dtype yt, int64_t ldy,
                                    const int32_t *slot, const float *w, int64_t ldw, int64_t T, int64_t k,

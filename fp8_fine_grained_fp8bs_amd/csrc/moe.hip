@@ -43,8 +43,9 @@ constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSteps = 2;                             // assignments of a lane and round
 constexpr int kRound = kSortThreads * kSteps;         // of a workgroup and round
 constexpr int kPerThread = kMaxExperts / kSortThreads;
-// assignments that every workgroup counts for itself: 8192 to 64 experts 11.7 us against
-// 12.8 with the counting kernel, 16384 15.4 against 12.9 (with rows of 128 columns)
+// assignments that every workgroup counts for itself (with the rows in a launch of
+// their own): 8192 to 64 experts with rows of 128 columns 9.7 us against 12.7 with the
+// counting kernel, of 2048 15.0 and 15.6; 16384 with rows of 2048 20.0 against 18.1
 constexpr int64_t kCountHere = 8192;
 
 // Expert of assignment i among those held here, or -1.
@@ -94,6 +95,28 @@ __device__ __forceinline__ int exclusive_sum(int v, int* sums, int& all) {
   return before + s - v;
 }
 
+// All n assignments counted by expert: those before a in `start`, the others in
+// `total`.  Bound by the loads' latency: four of a thread are in flight, with
+// indices cut to the last assignment in place of branches.  Dispatch of 8192 with rows
+// of 2048 10.9 us (12.2 with a branch at each load); of 512 with rows of 7168 6.8, with
+// eight in flight 7.3 and with sixteen 8.2, whose surplus loads wait for nothing.
+__device__ __forceinline__ void count_all(const MoeIds& p, int n, int a, int* start, int* total) {
+  constexpr int kLoads = 4;
+  for (int base = threadIdx.x; base < n; base += kLoads * kSortThreads) {
+    int e[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = base + u * kSortThreads;
+      e[u] = expert_of(p, i < n ? i : n - 1);
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int i = base + u * kSortThreads;
+      if (i < n && e[u] >= 0) atomicAdd(i < a ? &start[e[u]] : &total[e[u]], 1);
+    }
+  }
+}
+
 // counts: of every stretch, or null (counted here).
 __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64_t n, int64_t stretch, int stretches,
                                                                  int bits, const int32_t* __restrict__ counts) {
@@ -129,13 +152,9 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64
       atomicAdd(&start[e], earlier);
     }
   } else {
-#pragma unroll 4
-    for (int64_t i = tid; i < n; i += kSortThreads) {
-      const int e = expert_of(p, i);
-      if (e < 0) continue;
-      atomicAdd(&total[e], 1);
-      if (i < a) atomicAdd(&start[e], 1);
-    }
+    count_all(p, static_cast<int>(n), static_cast<int>(a), start, total);
+    __syncthreads();
+    for (int x = tid; x < p.E; x += kSortThreads) total[x] += start[x];
   }
   __syncthreads();
   {
@@ -332,9 +351,9 @@ __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
 // a few tokens, with at most 64 assignments, and counts all assignments by
 // expert for itself (those before its own apart), which gives its own rows as
 // in the sort above; their ranks are one wave's ballots.  Against sort and rows in
-// launches of their own: 256 tokens of 7168 to 8 experts 8.9 us and 12.8, 512 12.9 and
-// 16.2, 1024 of 1024 columns 10.4 and 12.5, of 7168 24.9 and 23.8; 2048 to 8
-// (16384 assignments) 20.9 and 17.9.
+// launches of their own: 256 tokens of 7168 to 8 experts 8.4 us and 12.1, 512 11.6 and
+// 15.3, 1024 of 1024 columns 9.5 and 11.3, of 7168 22.4 and 21.0; 2048 of 7168 to 8
+// (16384 assignments) 43.2 and 40.4.
 constexpr int kOneLaunch = 8192;
 
 template <bool CODES>
@@ -360,11 +379,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, 
     start[e] = 0;
   }
   __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < n; i += kSortThreads) {
-    const int e = expert_of(ids, i);
-    if (e >= 0) atomicAdd(i < a ? &start[e] : &total[e], 1);
-  }
+  count_all(ids, n, a, start, total);
   __syncthreads();
   {
     int mine[kPerThread], sum = 0, all;

@@ -31,7 +31,7 @@ namespace {
 // number of those of smaller experts, plus those of its own expert in earlier
 // stretches, plus its rank in its stretch.  The first two come from counts by
 // stretch and expert, which a kernel of its own writes (large batches) or
-// every workgroup counts for itself (middling ones: all assignments, from the
+// every workgroup counts for itself (small ones: all assignments, from the
 // caches).  Within a stretch the order is kept without atomics: a wave
 // compares its 64 assignments bit by bit (ballots), which gives an
 // assignment's rank among those of its expert, and counts per wave are
@@ -117,6 +117,25 @@ __device__ __forceinline__ void count_all(const MoeIds& p, int n, int a, int* st
   }
 }
 
+// The stretches' counts summed by expert: of those before stretch `mine` to `start`,
+// of all to `total`.  As many threads an expert as there are, each some of the stretches.
+__device__ __forceinline__ void add_counts(const int32_t* __restrict__ counts, int E, int stretches, int mine,
+                                           int* start, int* total) {
+  const int parts = E < kSortThreads ? kSortThreads / E : 1;
+  for (int x = threadIdx.x; x < E * parts; x += kSortThreads) {
+    const int part = x / E, e = x - part * E;
+    int all = 0, earlier = 0;
+#pragma unroll 4
+    for (int s = part; s < stretches; s += parts) {
+      const int c = counts[static_cast<int64_t>(s) * E + e];
+      all += c;
+      earlier += s < mine ? c : 0;
+    }
+    atomicAdd(&total[e], all);
+    atomicAdd(&start[e], earlier);
+  }
+}
+
 // counts: of every stretch, or null (counted here).
 __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64_t n, int64_t stretch, int stretches,
                                                                  int bits, const int32_t* __restrict__ counts) {
@@ -137,20 +156,7 @@ __global__ __launch_bounds__(kSortThreads) void moe_place_kernel(MoeIds p, int64
   }
   __syncthreads();
   if (counts != nullptr) {
-    // as many threads an expert as there are, each some of the stretches
-    const int parts = p.E < kSortThreads ? kSortThreads / p.E : 1;
-    for (int x = tid; x < p.E * parts; x += kSortThreads) {
-      const int part = x / p.E, e = x - part * p.E;
-      int all = 0, earlier = 0;
-#pragma unroll 4
-      for (int s = part; s < stretches; s += parts) {
-        const int c = counts[static_cast<int64_t>(s) * p.E + e];
-        all += c;
-        earlier += s < static_cast<int>(blockIdx.x) ? c : 0;
-      }
-      atomicAdd(&total[e], all);
-      atomicAdd(&start[e], earlier);
-    }
+    add_counts(counts, p.E, stretches, blockIdx.x, start, total);
   } else {
     count_all(p, static_cast<int>(n), static_cast<int>(a), start, total);
     __syncthreads();
@@ -347,17 +353,34 @@ __global__ __launch_bounds__(1024) void moe_gather_kernel(MoeRows p) {
   }
 }
 
-// Up to kOneLaunch assignments: sort and rows in one launch.  A workgroup takes
-// a few tokens, with at most 64 assignments, and counts all assignments by
-// expert for itself (those before its own apart), which gives its own rows as
-// in the sort above; their ranks are one wave's ballots.  Against sort and rows in
-// launches of their own: 256 tokens of 7168 to 8 experts 8.4 us and 12.1, 512 11.6 and
-// 15.3, 1024 of 1024 columns 9.5 and 11.3, of 7168 22.4 and 21.0; 2048 of 7168 to 8
-// (16384 assignments) 43.2 and 40.4.
+// Sort and rows in one launch (up to kOneLaunch assignments), or in one behind the
+// counting kernel (COUNTED).  A workgroup takes a few tokens, with at most 64
+// assignments, and counts those before its own by expert for itself, all of them or
+// those of its stretch, which gives its own rows as in the sort above; their ranks
+// are one wave's ballots.  A wave's next loads go out before its rows are stored: 1024
+// tokens of 7168 to 8 of 64 experts 20.2 us (22.5 without).  Against sort and rows
+// in launches of their own: 256 such tokens 8.5 us and 12.1, 512 11.5 and 15.3, 1024 of
+// 1024 columns 9.5 and 11.3, of 7168 20.2 and 21.0; 8192 tokens to one expert each 38.1 and
+// 37.5.
 constexpr int kOneLaunch = 8192;
+static_assert(kOneLaunch >= kCountHere, "more assignments have a workspace for their counts");
 
-template <bool CODES>
-__global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, MoeRows p, int tokens, int bits) {
+// Whether a batch of more assignments is COUNTED, or has the sort's two kernels and
+// the rows' own.  That kernel has fewer, longer workgroups, which pays as long as the
+// launch that it spares is a good part of the whole: 2048 tokens of 2048 to 8 of 64
+// experts 14.7 us against 18.0, 4096 to 8 of 8 22.8 and 22.6, 2048 of 7168 38.7
+// and 39.5, 4096 of 4096 43.7 and 43.9, 16384 of 1024 to 2 20.0 and 21.9.  Past these
+// limits: 16384 of 1024 to 4 28.8 and 28.7, 2048 of 7168 to 16 73.3 and 68.9,
+// 8192 of 7168 to 2 59.2 and 54.3 and, held elsewhere for the most part, to 8 of 256 40.8 and
+// 28.8; of narrow rows 16384 of 256 to 2 15.8 and 15.0, 32768 of 512 23.8 and 21.3.
+inline bool counted_rows(int64_t T, int k, int64_t C) {
+  return T <= (C < 1024 ? 8192 : 16384) && T * k <= 32768 && T * C <= 1 << 24 && T * k * C <= 1 << 27;
+}
+
+template <bool CODES, bool COUNTED>
+__global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, MoeRows p, int tokens, int bits,
+                                                                    int stretch, int stretches,
+                                                                    const int32_t* __restrict__ counts) {
   __shared__ int total[kMaxExperts];
   __shared__ int start[kMaxExperts];
   __shared__ int sums[kSortWaves];
@@ -368,25 +391,36 @@ __global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, 
   poison_lds<sizeof(slots)>(slots);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int T = static_cast<int>(ids.T), n = T * ids.k;
-  const int t0 = blockIdx.x * tokens, here = T - t0 < tokens ? T - t0 : tokens;
+  const int t0 = static_cast<int>(neighbours_on_an_xcd()) * tokens, here = T - t0 < tokens ? T - t0 : tokens;
   const int a = t0 * ids.k, b = a + here * ids.k;
   const int chunks = (p.C + 1023) / 1024, items = here * chunks;
+  const int step = kSortWaves / chunks, rest = kSortWaves - step * chunks;   // from a wave's item to its next
+  int token = wave / chunks, chunk = wave - token * chunks;
   // the first columns are on their way while the rows are counted
   Unit<2> u;
-  if (wave < items) load_unit<CODES, 2>(p, t0 + wave / chunks, Columns{wave % chunks * 1024 + lane * 8, p.C}, u);
+  if (wave < items) load_unit<CODES, 2>(p, t0 + token, Columns{chunk * 1024 + lane * 8, p.C}, u);
   for (int e = tid; e < ids.E; e += kSortThreads) {
     total[e] = 0;
     start[e] = 0;
   }
   __syncthreads();
-  count_all(ids, n, a, start, total);
+  if (COUNTED) {
+    const int s = a / stretch;
+    for (int i = s * stretch + tid; i < a; i += kSortThreads) {
+      const int e = expert_of(ids, i);
+      if (e >= 0) atomicAdd(&start[e], 1);
+    }
+    add_counts(counts, ids.E, stretches, s, start, total);
+  } else {
+    count_all(ids, n, a, start, total);
+  }
   __syncthreads();
   {
     int mine[kPerThread], sum = 0, all;
 #pragma unroll
     for (int x = 0; x < kPerThread; ++x) {
       const int e = tid * kPerThread + x;
-      mine[x] = e < ids.E ? total[e] + start[e] : 0;
+      mine[x] = e >= ids.E ? 0 : COUNTED ? total[e] : total[e] + start[e];
       sum += mine[x];
     }
     int first = exclusive_sum(sum, sums, all);
@@ -415,15 +449,26 @@ __global__ __launch_bounds__(kSortThreads) void moe_dispatch_kernel(MoeIds ids, 
     if (a + lane < b) ids.slot[a + lane] = at;
   }
   __syncthreads();
+  if (wave >= items) return;
+  Choices chosen(slots + token * ids.k, nullptr, ids.k, p.M, lane);
   for (int item = wave; item < items; item += kSortWaves) {
-    const int token = item / chunks;
-    const Columns c{(item - token * chunks) * 1024 + lane * 8, p.C};
-    const Choices chosen(slots + token * ids.k, nullptr, ids.k, p.M, lane);
-    if (item != wave) {
-      if (!chosen.any()) continue;   // no row: x is not read
-      load_unit<CODES, 2>(p, t0 + token, c, u);
+    const Columns c{chunk * 1024 + lane * 8, p.C};
+    token += step;
+    chunk += rest;
+    if (chunk >= chunks) {
+      chunk -= chunks;
+      ++token;
     }
-    store_unit<CODES, 2>(p, c, u, chosen, lane);
+    Choices next = chosen;
+    Unit<2> ahead{};
+    if (item + kSortWaves < items) {
+      next = Choices(slots + token * ids.k, nullptr, ids.k, p.M, lane);
+      if (next.any())   // no row: x is not read
+        load_unit<CODES, 2>(p, t0 + token, Columns{chunk * 1024 + lane * 8, p.C}, ahead);
+    }
+    if (chosen.any()) store_unit<CODES, 2>(p, c, u, chosen, lane);
+    u = ahead;
+    chosen = next;
   }
 }
 
@@ -683,13 +728,24 @@ hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
 }
 
 hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st) {
-  if (ids.T * ids.k <= kOneLaunch) {
+  const int64_t n = ids.T * ids.k;
+  const Stretches s = stretches_of(n, ids.E);
+  if (n <= kOneLaunch || counted_rows(ids.T, ids.k, p.C)) {
+    const bool counted = n > kOneLaunch;
+    if (counted) {
+      hipLaunchKernelGGL(moe_count_kernel, dim3(s.count), dim3(kSortThreads), 0, st, ids, n, s.length, ids.ws);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     // enough workgroups for the compute units
     const int T = static_cast<int>(ids.T), most = 64 / ids.k;
     const int each = (T + 511) / 512, tokens = each < most ? each : most;
     const dim3 grid((T + tokens - 1) / tokens), block(kSortThreads);
-    if (p.codes_in) hipLaunchKernelGGL((moe_dispatch_kernel<true>), grid, block, 0, st, ids, p, tokens, id_bits(ids.E));
-    else hipLaunchKernelGGL((moe_dispatch_kernel<false>), grid, block, 0, st, ids, p, tokens, id_bits(ids.E));
+    const auto kernel = p.codes_in ? counted ? moe_dispatch_kernel<true, true> : moe_dispatch_kernel<true, false>
+                        : counted  ? moe_dispatch_kernel<false, true>
+                                   : moe_dispatch_kernel<false, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, ids, p, tokens, id_bits(ids.E), static_cast<int>(s.length), s.count,
+                       ids.ws);
     return hipGetLastError();
   }
   const hipError_t e = launch_moe_sort(ids, st);

@@ -149,6 +149,45 @@ def test_dispatch(T, k, C, of, E, rows):
     assert torch.equal(out[0].cpu(), want_q) and torch.equal(out[1].cpu(), want_s)
 
 
+# larger ones on both sides of each limit between the ways there are: assignments, tokens (of narrow
+# and of wide rows), values in and out; most experts, most choices, stretches that end inside a token
+LARGER = [(2731, 3, 256, 8, 8, None), (4096, 8, 128, 1024, 1024, None), (4097, 8, 128, 64, 64, None),
+          (512, 64, 256, 16, 16, None), (513, 64, 128, 16, 5, None), (8192, 2, 512, 64, 9, 3000), (8193, 2, 512, 64, 9, 3000),
+          (16384, 1, 1024, 32, 32, None), (16385, 1, 1024, 32, 32, None), (1100, 8, 15232, 300, 3, 99),
+          (1102, 8, 15232, 300, 3, 99), (4369, 7, 640, 20, 20, None), (2000, 15, 1152, 48, 6, None)]
+
+
+@pytest.mark.parametrize("T,k,C,of,E,rows", LARGER)
+def test_dispatch_of_larger_batches(T, k, C, of, E, rows):
+    test_dispatch(T, k, C, of, E, rows)
+
+
+def test_dispatch_of_a_larger_batch_captured():
+    native_loaded()
+    announce("dispatch 1500x8, two captured graphs")
+    T, k, C, E = 1500, 8, 256, 16
+    graphs = []
+    for seed in (1, 2):
+        ids, x = choices(T, k, E, seed).cuda(), tokens(T, C, seed).cuda()
+        fp8bs.moe_dispatch(x, ids, E)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            made = fp8bs.moe_dispatch(x, ids, E)
+        graphs.append((g, ids, x, made))
+    for turn in range(4):
+        for i, (g, ids, x, made) in enumerate(graphs):
+            ids.copy_(choices(T, k, E, 10 + 2 * turn + i).cuda())
+            x.copy_(tokens(T, C, 20 + 2 * turn + i).cuda())
+        for g, ids, x, made in graphs:
+            g.replay()
+        for g, ids, x, made in graphs:
+            want = fp8bs.moe_dispatch(x, ids, E)
+            rows = int(want[3][-1])
+            assert torch.equal(made[3], want[3]) and torch.equal(made[4], want[4])
+            assert torch.equal(made[0][:rows], want[0][:rows]) and torch.equal(made[1][:rows], want[1][:rows])
+
+
 COMBINES = [(1, 1, 128, 1, 1), (50, 3, 512, 8, 8), (600, 9, 128, 8, 8), (16, 8, 7168, 64, 64), (5, 3, 640, 8, 3), (300, 2, 1152, 8, 8), (33, 64, 256, 16, 16),
             (7, 9, 384, 20, 20), (1030, 8, 512, 60, 30)]
 

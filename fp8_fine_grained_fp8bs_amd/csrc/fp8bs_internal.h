@@ -127,8 +127,25 @@ hipError_t launch_attn_paged(const AttnPaged& p, hipStream_t st);
 // Working memory of launch_attn_paged: a function of the sizes alone.
 int64_t attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, int64_t max_pages, int page);
 
-// A grid's threads are numbered in 32 bits.
-inline bool grid_fits(int64_t blocks, int threads) { return blocks <= 0xffffffffll / threads; }
+// Workgroups of a launch: a grid's threads are numbered in 32 bits.
+constexpr int64_t most_blocks(int threads) { return 0xffffffffll / threads; }
+
+// Launches for all of p's tokens, at most so many a launch.  launch(part) takes the
+// arguments of some of them; p.part(t, n) gives those of tokens t .. t + n - 1.
+template <class P, class Launch>
+hipError_t by_tokens(const P& p, int64_t most, Launch launch) {
+  if (p.T <= most) return launch(p);
+  for (int64_t t = 0; t < p.T; t += most) {
+    const hipError_t e = launch(p.part(t, p.T - t < most ? p.T - t : most));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+// An optional buffer n elements further.
+template <class T>
+T* further(T* p, int64_t n) {
+  return p != nullptr ? p + n : nullptr;
+}
 
 // Arguments of fp8bs_rmsnorm_quant_1x128 (r, q, y, rstd may be null; q with s, r with h).
 struct RmsNorm {
@@ -150,6 +167,18 @@ struct RmsNorm {
   uint16_t* y;
   int64_t ldy;
   float* rstd;
+  RmsNorm part(int64_t t, int64_t n) const {
+    RmsNorm p = *this;
+    p.T = n;
+    p.x += t * ldx;
+    p.r = further(r, t * ldr);
+    p.h = further(h, t * ldh);
+    p.q = further(q, t * ldq);
+    p.s = further(s, t * lds);
+    p.y = further(y, t * ldy);
+    p.rstd = further(rstd, t);
+    return p;
+  }
 };
 hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t st);
 
@@ -209,6 +238,15 @@ struct MoeRows {
   int64_t lds;
   uint16_t* y;
   int64_t ldy, M;
+  // the outputs' rows go by slot
+  MoeRows part(int64_t t, int64_t n) const {
+    MoeRows p = *this;
+    p.T = n;
+    p.x = static_cast<const uint8_t*>(x) + t * ldx * (codes_in ? 1 : 2);
+    p.s_in = further(s_in, t * lds_in);
+    p.slot += t * k;
+    return p;
+  }
 };
 hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st);
 hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st);
@@ -225,6 +263,15 @@ struct MoeCombine {
   int64_t ldadd;
   uint16_t* out;
   int64_t ldo;
+  MoeCombine part(int64_t t, int64_t n) const {
+    MoeCombine p = *this;
+    p.T = n;
+    p.slot += t * k;
+    p.w = further(w, t * ldw);
+    p.add = further(add, t * ldadd);
+    p.out += t * ldo;
+    return p;
+  }
 };
 hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st);
 
@@ -246,6 +293,15 @@ struct MoeCombineBwd {
   int64_t lddy, M;
   float* dw;   // may be null
   int64_t lddw;
+  MoeCombineBwd part(int64_t t, int64_t n) const {
+    MoeCombineBwd p = *this;
+    p.T = n;
+    p.dout += t * lddo;
+    p.slot += t * k;
+    p.w += t * ldw;
+    p.dw = further(dw, t * lddw);
+    return p;
+  }
 };
 hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st);
 
@@ -265,6 +321,18 @@ struct SwigluBwd {
   int64_t ldd;
   uint16_t* h;
   int64_t ldh;
+  SwigluBwd part(int64_t t, int64_t n) const {
+    SwigluBwd p = *this;
+    p.T = n;
+    p.dh += t * lddh;
+    p.g += t * ldg;
+    p.u += t * ldu;
+    p.q = further(q, t * ldq);
+    p.s = further(s, t * lds);
+    p.d = further(d, t * ldd);
+    p.h = further(h, t * ldh);
+    return p;
+  }
 };
 hipError_t launch_swiglu_bwd(const SwigluBwd& p, hipStream_t st);
 

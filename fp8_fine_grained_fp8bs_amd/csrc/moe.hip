@@ -670,16 +670,17 @@ Stretches stretches_of(int64_t n, int E) {
   return {each * kRound, n > 0 ? static_cast<int>((rounds + each - 1) / each) : 1};
 }
 
-// A launch by token, V vectors a lane and at most so many waves.
+// Launches by token, V vectors a lane and at most so many waves: a workgroup's threads
+// and tokens.
 struct Tokens {
-  dim3 grid, block;
-  bool fits;
+  int threads, each;
+  int64_t most() const { return most_blocks(threads) * each; }
+  dim3 grid(int64_t T) const { return dim3(static_cast<unsigned>((T + each - 1) / each)); }
 };
-Tokens tokens_of(int64_t T, int columns, int V, int most) {
-  int waves = (columns + 512 * V - 1) / (512 * V);
-  waves = V == 1 ? kTogether : waves > most ? most : waves;
-  const int64_t blocks = V == 1 ? (T + kTogether - 1) / kTogether : T;
-  return {dim3(static_cast<unsigned>(blocks)), dim3(64 * waves), grid_fits(blocks, 64 * waves)};
+Tokens tokens_of(int columns, int V, int most) {
+  if (V == 1) return {64 * kTogether, kTogether};
+  const int waves = (columns + 512 * V - 1) / (512 * V);
+  return {64 * (waves > most ? most : waves), 1};
 }
 
 // Bits of an expert's number.
@@ -717,14 +718,16 @@ hipError_t launch_moe_gather(const MoeRows& p, hipStream_t st) {
   // codes, whose lanes have nothing to compute (4096 x 8 rows of 7168: 70.5 us against
   // 73.8); one where a row has no more
   const int V = p.C <= 512 ? 1 : p.codes_in || p.C < 2048 ? 2 : 4;
-  const Tokens g = tokens_of(p.T, p.C, V, 16);
-  if (!g.fits) return hipErrorInvalidValue;
-  if (p.codes_in && V == 1) hipLaunchKernelGGL((moe_gather_kernel<true, 1>), g.grid, g.block, 0, st, p);
-  else if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true, 2>), g.grid, g.block, 0, st, p);
-  else if (V == 1) hipLaunchKernelGGL((moe_gather_kernel<false, 1>), g.grid, g.block, 0, st, p);
-  else if (V == 2) hipLaunchKernelGGL((moe_gather_kernel<false, 2>), g.grid, g.block, 0, st, p);
-  else hipLaunchKernelGGL((moe_gather_kernel<false, 4>), g.grid, g.block, 0, st, p);
-  return hipGetLastError();
+  const Tokens g = tokens_of(p.C, V, 16);
+  return by_tokens(p, g.most(), [&](const MoeRows& p) {
+    const dim3 grid = g.grid(p.T), block(g.threads);
+    if (p.codes_in && V == 1) hipLaunchKernelGGL((moe_gather_kernel<true, 1>), grid, block, 0, st, p);
+    else if (p.codes_in) hipLaunchKernelGGL((moe_gather_kernel<true, 2>), grid, block, 0, st, p);
+    else if (V == 1) hipLaunchKernelGGL((moe_gather_kernel<false, 1>), grid, block, 0, st, p);
+    else if (V == 2) hipLaunchKernelGGL((moe_gather_kernel<false, 2>), grid, block, 0, st, p);
+    else hipLaunchKernelGGL((moe_gather_kernel<false, 4>), grid, block, 0, st, p);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_moe_dispatch(const MoeIds& ids, const MoeRows& p, hipStream_t st) {
@@ -757,14 +760,14 @@ hipError_t launch_moe_combine(const MoeCombine& p, hipStream_t st) {
   // 10.4 with two, 16384 x 8 FP32 rows of 512 53.9 against 63.0)
   const bool narrow = p.N <= 512;
   const int chunks = narrow ? 1 : (p.N + 1023) / 1024;
-  const int64_t blocks = (p.T * chunks + 3) / 4;
-  if (!grid_fits(blocks, 256)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
-  if (p.y_f32 && narrow) hipLaunchKernelGGL((moe_combine_kernel<true, 1>), grid, block, 0, st, p, chunks);
-  else if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, 2>), grid, block, 0, st, p, chunks);
-  else if (narrow) hipLaunchKernelGGL((moe_combine_kernel<false, 1>), grid, block, 0, st, p, chunks);
-  else hipLaunchKernelGGL((moe_combine_kernel<false, 2>), grid, block, 0, st, p, chunks);
-  return hipGetLastError();
+  return by_tokens(p, most_blocks(256) * 4 / chunks, [&](const MoeCombine& p) {
+    const dim3 grid(static_cast<unsigned>((p.T * chunks + 3) / 4)), block(256);
+    if (p.y_f32 && narrow) hipLaunchKernelGGL((moe_combine_kernel<true, 1>), grid, block, 0, st, p, chunks);
+    else if (p.y_f32) hipLaunchKernelGGL((moe_combine_kernel<true, 2>), grid, block, 0, st, p, chunks);
+    else if (narrow) hipLaunchKernelGGL((moe_combine_kernel<false, 1>), grid, block, 0, st, p, chunks);
+    else hipLaunchKernelGGL((moe_combine_kernel<false, 2>), grid, block, 0, st, p, chunks);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st) {
@@ -772,21 +775,22 @@ hipError_t launch_moe_combine_bwd(const MoeCombineBwd& p, hipStream_t st) {
   // against 37.9, 8191 x 2 90.7 against 91.8), two for few (16 x 8: 8.1 against 9.0);
   // one where a row has no more
   const int V = p.N <= 512 ? 1 : p.T >= 512 && p.N > 1024 ? 4 : 2;
-  const Tokens g = tokens_of(p.T, p.N, V, V == 4 ? 8 : 16);
-  if (!g.fits) return hipErrorInvalidValue;
-#define FP8BS_COMBINE(F32, V) \
-  hipLaunchKernelGGL((moe_combine_bwd_kernel<F32, V>), g.grid, g.block, 0, st, p)
-  if (p.y_f32) {
-    if (V == 1) FP8BS_COMBINE(true, 1);
-    else if (V == 2) FP8BS_COMBINE(true, 2);
-    else FP8BS_COMBINE(true, 4);
-  } else {
-    if (V == 1) FP8BS_COMBINE(false, 1);
-    else if (V == 2) FP8BS_COMBINE(false, 2);
-    else FP8BS_COMBINE(false, 4);
-  }
+  const Tokens g = tokens_of(p.N, V, V == 4 ? 8 : 16);
+  return by_tokens(p, g.most(), [&](const MoeCombineBwd& p) {
+    const dim3 grid = g.grid(p.T), block(g.threads);
+#define FP8BS_COMBINE(F32, V) hipLaunchKernelGGL((moe_combine_bwd_kernel<F32, V>), grid, block, 0, st, p)
+    if (p.y_f32) {
+      if (V == 1) FP8BS_COMBINE(true, 1);
+      else if (V == 2) FP8BS_COMBINE(true, 2);
+      else FP8BS_COMBINE(true, 4);
+    } else {
+      if (V == 1) FP8BS_COMBINE(false, 1);
+      else if (V == 2) FP8BS_COMBINE(false, 2);
+      else FP8BS_COMBINE(false, 4);
+    }
 #undef FP8BS_COMBINE
-  return hipGetLastError();
+    return hipGetLastError();
+  });
 }
 
 }  // namespace fp8bs

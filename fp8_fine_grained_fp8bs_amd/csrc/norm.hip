@@ -338,17 +338,17 @@ hipError_t launch_rmsnorm(const RmsNorm& p, hipStream_t st) {
   // columns (44.2 us against 44.7 and 44.5)
   const bool narrow = p.C <= 512;
   const int waves = row_waves(p.C, narrow ? 1 : 2);
-  const int64_t blocks = waves == 1 ? (p.T + 3) / 4 : p.T;
-  const int threads = waves == 1 ? 256 : 64 * waves;
-  if (!grid_fits(blocks, threads)) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(threads);
+  const int threads = waves == 1 ? 256 : 64 * waves, together = waves == 1 ? 4 : 1;
+  return by_tokens(p, most_blocks(threads) * together, [&](const RmsNorm& p) {
+    const dim3 grid(static_cast<unsigned>((p.T + together - 1) / together)), block(threads);
 #define FP8BS_NORM(V, RES) hipLaunchKernelGGL((rmsnorm_kernel<V, RES>), grid, block, 0, st, p, waves)
-  if (narrow && p.r != nullptr) FP8BS_NORM(1, true);
-  else if (narrow) FP8BS_NORM(1, false);
-  else if (p.r != nullptr) FP8BS_NORM(2, true);
-  else FP8BS_NORM(2, false);
+    if (narrow && p.r != nullptr) FP8BS_NORM(1, true);
+    else if (narrow) FP8BS_NORM(1, false);
+    else if (p.r != nullptr) FP8BS_NORM(2, true);
+    else FP8BS_NORM(2, false);
 #undef FP8BS_NORM
-  return hipGetLastError();
+    return hipGetLastError();
+  });
 }
 
 int64_t rmsnorm_bwd_ws(int64_t T, int C) {

@@ -204,10 +204,10 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
 
 hipError_t launch_swiglu_bwd(const SwigluBwd& p, hipStream_t st) {
   const int G = static_cast<int>(p.I / 128);
-  const int64_t blocks = (p.T * G + 15) / 16;
-  if (!grid_fits(blocks, 256)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, p, G);
-  return hipGetLastError();
+  return by_tokens(p, most_blocks(256) * 16 / G, [&](const SwigluBwd& p) {
+    hipLaunchKernelGGL(swiglu_bwd_kernel, dim3(static_cast<unsigned>((p.T * G + 15) / 16)), dim3(256), 0, st, p, G);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_swiglu_quant_1x128(const uint16_t* g, int64_t ldg, const uint16_t* u, int64_t ldu,

@@ -727,7 +727,17 @@ def fp8bs_moe_sort_ws(T, k, E):
     return _sort_ws_bytes(T, k, E)
 
 
-def _check_ids(ids, offsets, slot):
+def _overlap(rows, flat):
+    """Whether a contiguous tensor (or None) lies on values of a 2-D tensor with contiguous rows."""
+    if flat is None or flat.numel() == 0 or rows.numel() == 0:
+        return False
+    item, at, begin = rows.element_size(), rows.data_ptr(), flat.data_ptr()
+    T, width, step = rows.shape[0], rows.shape[1] * item, max(rows.stride(0), 1) * item
+    first = max(0, (begin - at - width) // step + 1)     # of the rows that end behind flat's start
+    return first < T and at + first * step < begin + flat.numel() * flat.element_size()
+
+
+def _check_ids(ids, offsets, slot, ws):
     """(index type, row stride, T, k, E) of a sort."""
     if _dtype_names[ids.dtype] not in ("int32", "int64") or ids.dim() != 2:
         raise ValueError(f"ids: expected int32 or int64 [T][k], got {ids.dtype} {tuple(ids.shape)}")
@@ -737,6 +747,9 @@ def _check_ids(ids, offsets, slot):
         raise ValueError(f"ids: rows must be contiguous, got strides {(row, one)}")
     _check(offsets, "offsets", ((">=", 2),), ("int32",), contiguous=True)
     _check(slot, "slot", (T, k), ("int32",), contiguous=True)
+    for name, t in (("offsets", offsets), ("slot", slot), ("ws", ws)):
+        if _overlap(ids, t):
+            raise ValueError(f"{name}: must not overlap ids")
     return (INDEX_I64 if _dtype_names[ids.dtype] == "int64" else INDEX_I32), _row_ld(ids, k), T, k, offsets.shape[0] - 1
 
 
@@ -744,7 +757,7 @@ def fp8bs_moe_sort(ids, first, M, offsets, slot, ws, stream=None):
     """ids i32 or i64 [T][k] -> offsets i32 [E+1] and slot i32 [T][k] of the
     assignments to experts first .. first + E - 1; ws uint8
     [>= fp8bs_moe_sort_ws(T, k, E)] (or None where that is 0)."""
-    it, ldi, T, k, E = _check_ids(ids, offsets, slot)
+    it, ldi, T, k, E = _check_ids(ids, offsets, slot, ws)
     _here(ids, offsets, slot, ws)
     _call("fp8bs_moe_sort", _ptr(ids), it, ldi, T, k, first, E, M, _ptr(offsets), _ptr(slot), _ptr(ws), _workspace(ws),
           _stream(stream))
@@ -774,7 +787,7 @@ def fp8bs_moe_gather(src, x, s_in, slot, q, s, y, stream=None):
 def fp8bs_moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, stream=None):
     """fp8bs_moe_sort of ids and fp8bs_moe_gather of x in one call."""
     T, C = _check_source(src, x, s_in)
-    it, ldi, n, k, E = _check_ids(ids, offsets, slot)
+    it, ldi, n, k, E = _check_ids(ids, offsets, slot, ws)
     if n != T:
         raise ValueError(f"ids: {n} tokens, x has {T}")
     M = _check_rows(q, s, y, C)

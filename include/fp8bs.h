@@ -538,6 +538,8 @@ typedef enum { FP8BS_INDEX_I32 = 0, FP8BS_INDEX_I64 = 1 } fp8bs_index_type;
  *            (slot -1, offsets cut to M).  T k rows hold every case.
  *   ws       device memory of fp8bs_moe_sort_ws(T, k, E) bytes, 4-byte aligned
  *            (may be NULL where that is 0)
+ * offsets, slot and ws must overlap neither ids nor each other: workgroups read all of the
+ * ids while others write their slots.
  * T >= 0 (0: offsets of zeros), 0 < k <= 64, 0 < E <= 1024, T k <= 2^30,
  * else FP8BS_ERR_UNSUPPORTED_SHAPE; first >= 0, M >= 0.
  */
@@ -582,7 +584,7 @@ fp8bs_status fp8bs_moe_dispatch(fp8bs_requant_src src, const void *x, int64_t ld
  *                                      their weight is
  *   w     f32 [T][ldw] or NULL         NULL: 1 (the gradient of fp8bs_moe_gather)
  *   add   bf16 [T][ldadd] or NULL      may be out itself (with its row stride)
- *   out   bf16 [T][ldo]                must not overlap y
+ *   out   bf16 [T][ldo]                must not overlap the other inputs
  * T >= 0 (0 is a no-op), 0 < k <= 64, N > 0 and N % 128 == 0, T and M < 2^31.
  */
 fp8bs_status fp8bs_moe_combine(const void *y, fp8bs_out_dtype yt, int64_t ldy, int64_t M, const int32_t *slot,

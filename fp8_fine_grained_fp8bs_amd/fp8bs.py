@@ -727,14 +727,12 @@ def fp8bs_moe_sort_ws(T, k, E):
     return _sort_ws_bytes(T, k, E)
 
 
-def _overlap(rows, flat):
-    """Whether a contiguous tensor (or None) lies on values of a 2-D tensor with contiguous rows."""
-    if flat is None or flat.numel() == 0 or rows.numel() == 0:
+def _overlap(at, rows, width, step, begin, nbytes):
+    """Whether nbytes from address begin lie on rows of width bytes, step bytes apart, from address at."""
+    if begin >= at + (rows - 1) * step + width or begin + nbytes <= at or width == 0 or nbytes == 0:
         return False
-    item, at, begin = rows.element_size(), rows.data_ptr(), flat.data_ptr()
-    T, width, step = rows.shape[0], rows.shape[1] * item, max(rows.stride(0), 1) * item
-    first = max(0, (begin - at - width) // step + 1)     # of the rows that end behind flat's start
-    return first < T and at + first * step < begin + flat.numel() * flat.element_size()
+    first = max(0, (begin - at - width) // step + 1) if rows > 1 else 0   # of the rows that end behind begin
+    return first < rows and at + first * step < begin + nbytes
 
 
 def _check_ids(ids, offsets, slot, ws):
@@ -747,10 +745,12 @@ def _check_ids(ids, offsets, slot, ws):
         raise ValueError(f"ids: rows must be contiguous, got strides {(row, one)}")
     _check(offsets, "offsets", ((">=", 2),), ("int32",), contiguous=True)
     _check(slot, "slot", (T, k), ("int32",), contiguous=True)
-    for name, t in (("offsets", offsets), ("slot", slot), ("ws", ws)):
-        if _overlap(ids, t):
+    E, wide, at = offsets.shape[0] - 1, _dtype_names[ids.dtype] == "int64", ids.data_ptr()
+    item = 8 if wide else 4
+    for name, t, nbytes in (("offsets", offsets, 4 * E + 4), ("slot", slot, 4 * T * k), ("ws", ws, _workspace(ws))):
+        if nbytes and _overlap(at, T, k * item, max(row, 1) * item, t.data_ptr(), nbytes):
             raise ValueError(f"{name}: must not overlap ids")
-    return (INDEX_I64 if _dtype_names[ids.dtype] == "int64" else INDEX_I32), _row_ld(ids, k), T, k, offsets.shape[0] - 1
+    return (INDEX_I64 if wide else INDEX_I32), _row_ld(ids, k), T, k, E
 
 
 def fp8bs_moe_sort(ids, first, M, offsets, slot, ws, stream=None):

@@ -666,6 +666,13 @@ def _check_rows(q, s, y, C, rows=None):
     return rows
 
 
+def _row_count(q, s, y, C):
+    """Rows of a dispatch's or a gather's outputs, of which there has to be one."""
+    if q is None and y is None:
+        raise ValueError("no output")
+    return _check_rows(q, s, y, C)
+
+
 def fp8bs_rmsnorm_quant_1x128(x, r, gamma, eps, h, q, s, y, rstd, stream=None):
     """x (and r) bf16 [T][C], gamma bf16 or f32 [C] -> h = x + r bf16 [T][C] (with
     r), its norm as q u8 [T][C] with s f32 [T][C/128] and/or y bf16 [T][C], and
@@ -777,7 +784,7 @@ def fp8bs_moe_gather(src, x, s_in, slot, q, s, y, stream=None):
     rows slot i32 [T][k] of q u8 [M][C] with s f32 [M][C/128] and/or y bf16 [M][C]."""
     T, C = _check_source(src, x, s_in)
     _check(slot, "slot", (T, None), ("int32",), contiguous=True)
-    M = _check_rows(q, s, y, C)
+    M = _row_count(q, s, y, C)
     _here(x, s_in, slot, q, s, y)
     _call("fp8bs_moe_gather", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C,
           _ptr(slot), slot.shape[1], _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)), _ptr(y),
@@ -790,7 +797,7 @@ def fp8bs_moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, str
     it, ldi, n, k, E = _check_ids(ids, offsets, slot, ws)
     if n != T:
         raise ValueError(f"ids: {n} tokens, x has {T}")
-    M = _check_rows(q, s, y, C)
+    M = _row_count(q, s, y, C)
     _here(x, s_in, ids, offsets, slot, q, s, y, ws)
     _call("fp8bs_moe_dispatch", int(src), _ptr(x), _row_ld(x, C), _ptr(s_in), _row_ld(s_in, _groups(C)), T, C, _ptr(ids),
           it, ldi, k, first, E, _ptr(offsets), _ptr(slot), _ptr(q), _row_ld(q, C), _ptr(s), _row_ld(s, _groups(C)),

@@ -742,7 +742,18 @@ def _overlap(at, rows, width, step, begin, nbytes):
     return first < rows and at + first * step < begin + nbytes
 
 
-def _check_ids(ids, offsets, slot, ws):
+def _check_apart(ids, offsets, slot, ws):
+    """Refuse a caller's outputs and working memory that lie on the ids [T][k] of a sort."""
+    if ids.dim() != 2:
+        return      # refused with the ids
+    (T, k), item, at = ids.shape, ids.element_size(), ids.data_ptr()
+    for name, t in (("offsets", offsets), ("slot", slot), ("ws", ws)):
+        if t is not None and _overlap(at, T, k * item, max(ids.stride(0), 1) * item, t.data_ptr(),
+                                      t.numel() * t.element_size()):
+            raise ValueError(f"{name}: must not overlap ids")
+
+
+def _check_ids(ids, offsets, slot):
     """(index type, row stride, T, k, E) of a sort."""
     if _dtype_names[ids.dtype] not in ("int32", "int64") or ids.dim() != 2:
         raise ValueError(f"ids: expected int32 or int64 [T][k], got {ids.dtype} {tuple(ids.shape)}")
@@ -752,19 +763,19 @@ def _check_ids(ids, offsets, slot, ws):
         raise ValueError(f"ids: rows must be contiguous, got strides {(row, one)}")
     _check(offsets, "offsets", ((">=", 2),), ("int32",), contiguous=True)
     _check(slot, "slot", (T, k), ("int32",), contiguous=True)
-    E, wide, at = offsets.shape[0] - 1, _dtype_names[ids.dtype] == "int64", ids.data_ptr()
-    item = 8 if wide else 4
-    for name, t, nbytes in (("offsets", offsets, 4 * E + 4), ("slot", slot, 4 * T * k), ("ws", ws, _workspace(ws))):
-        if nbytes and _overlap(at, T, k * item, max(row, 1) * item, t.data_ptr(), nbytes):
-            raise ValueError(f"{name}: must not overlap ids")
-    return (INDEX_I64 if wide else INDEX_I32), _row_ld(ids, k), T, k, E
+    return (INDEX_I64 if _dtype_names[ids.dtype] == "int64" else INDEX_I32), _row_ld(ids, k), T, k, offsets.shape[0] - 1
 
 
 def fp8bs_moe_sort(ids, first, M, offsets, slot, ws, stream=None):
     """ids i32 or i64 [T][k] -> offsets i32 [E+1] and slot i32 [T][k] of the
     assignments to experts first .. first + E - 1; ws uint8
     [>= fp8bs_moe_sort_ws(T, k, E)] (or None where that is 0)."""
-    it, ldi, T, k, E = _check_ids(ids, offsets, slot, ws)
+    _check_apart(ids, offsets, slot, ws)
+    _moe_sort(ids, first, M, offsets, slot, ws, stream)
+
+
+def _moe_sort(ids, first, M, offsets, slot, ws, stream):
+    it, ldi, T, k, E = _check_ids(ids, offsets, slot)
     _here(ids, offsets, slot, ws)
     _call("fp8bs_moe_sort", _ptr(ids), it, ldi, T, k, first, E, M, _ptr(offsets), _ptr(slot), _ptr(ws), _workspace(ws),
           _stream(stream))
@@ -793,8 +804,13 @@ def fp8bs_moe_gather(src, x, s_in, slot, q, s, y, stream=None):
 
 def fp8bs_moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, stream=None):
     """fp8bs_moe_sort of ids and fp8bs_moe_gather of x in one call."""
+    _check_apart(ids, offsets, slot, ws)
+    _moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, stream)
+
+
+def _moe_dispatch(src, x, s_in, ids, first, offsets, slot, q, s, y, ws, stream):
     T, C = _check_source(src, x, s_in)
-    it, ldi, n, k, E = _check_ids(ids, offsets, slot, ws)
+    it, ldi, n, k, E = _check_ids(ids, offsets, slot)
     if n != T:
         raise ValueError(f"ids: {n} tokens, x has {T}")
     M = _row_count(q, s, y, C)
@@ -1177,8 +1193,8 @@ def moe_sort(ids, E, first=0, rows=None, stream=None):
     T, k = ids.shape
     offsets = torch.empty((E + 1,), dtype=torch.int32, device=ids.device)
     slot = torch.empty((T, k), dtype=torch.int32, device=ids.device)
-    fp8bs_moe_sort(ids, first, T * k if rows is None else rows, offsets, slot,
-                   _ws(_sort_ws_bytes(T, k, E), ids.device, stream), stream)
+    _moe_sort(ids, first, T * k if rows is None else rows, offsets, slot,
+              _ws(_sort_ws_bytes(T, k, E), ids.device, stream), stream)
     return offsets, slot
 
 
@@ -1216,8 +1232,8 @@ def moe_dispatch(x, ids, E, first=0, s_in=None, rows=None, codes=True, with_y=Fa
     q, s, y = _row_outputs(out, T * k if rows is None else rows, C, codes, with_y, x.device)
     offsets = torch.empty((E + 1,), dtype=torch.int32, device=x.device)
     slot = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    fp8bs_moe_dispatch(SRC_BF16 if s_in is None else SRC_FP8_1x128, x, s_in, ids, first, offsets, slot, q, s, y,
-                       _ws(_sort_ws_bytes(T, k, E), x.device, stream), stream)
+    _moe_dispatch(SRC_BF16 if s_in is None else SRC_FP8_1x128, x, s_in, ids, first, offsets, slot, q, s, y,
+                  _ws(_sort_ws_bytes(T, k, E), x.device, stream), stream)
     return q, s, y, offsets, slot
 
 

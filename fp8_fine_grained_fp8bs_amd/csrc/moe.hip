@@ -10,8 +10,10 @@
 // quantized once and written to k rows.  All of it moves memory: two or three
 // operations a byte.  Measured, per call in a stream of calls:
 //   8192 tokens of 7168, a tenth of them padding, 8 of 256 experts each, to the 32 held
-//     here: 28.7 us, of which 9.5 the sort's two kernels and 19 the rows, some 105
-//     MB at 5.5 TB/s; 16 tokens to 8 of 64 experts 6.2 us, one launch
+//     here: 28.7 to 34.6 us, as many as the ids send here; 9.5 of it the sort's two kernels,
+//     the rest the rows (19 of 28.7, some 105 MB at 5.5 TB/s); 4096 tokens of 7168 to 8 of
+//     64, all held, 71.7 us (301 MB, 4.2 TB/s), from codes 69.0 (273 MB, 4.0);
+//     16 tokens to 8 of 64 experts 6.2 us, one launch
 //   4099 x 8 rows of 7168 back: 588 MB, 98.3 us, 6.0 TB/s (as many bytes in order, 8
 //     reads to a write, move at 6.2)
 //   gradient of 8191 x 2 rows of 7168: 474 MB, 89.9 us, 5.3 TB/s: its reads alone take

@@ -147,8 +147,9 @@ __global__ __launch_bounds__(256) void swiglu_quant_kernel(const uint16_t* __res
 // as codes with 1x128 scales (the input gradient's operand) and in BF16 (the
 // weight gradient's source), and optionally h again.  A DPP row takes one tile
 // of dh, g and u, 8 values a lane, and gives one tile of dg and one of du.
-// HBM-bound: 16384 x 2048 with codes, BF16 gradients and h, 472 MB, 68.9 us, 6.8
-// TB/s; 33 rows 6.0 us, 3.1 in the kernel.
+// HBM-bound: 16384 x 2048 with codes, BF16 gradients and h, 472 MB, 73.9 us in the
+// kernel, 6.4 TB/s; 69 a call in a stream of calls that write the same buffers, which
+// stay in the caches in part (no rate of HBM).  33 rows 6.0 us, 3.3 in the kernel.
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
   const int sub = threadIdx.x & 15;
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
@@ -192,8 +193,8 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(SwigluBwd p, int G) {
   if (p.d != nullptr) {
     uint16_t* out = p.d + t * p.ldd + c;
     // past the caches: what reads them next, the weights' gradient, comes after the
-    // input gradient's product (69.0 us against 79.7 with plain stores; with that
-    // product and the re-quantization behind it 573 against 580)
+    // input gradient's product (calls in a stream 69.0 us against 79.7 with plain
+    // stores; with that product and the re-quantization behind it 573 against 580)
     __builtin_nontemporal_store(bf16x8_pack(g), reinterpret_cast<u32x4*>(out));
     __builtin_nontemporal_store(bf16x8_pack(u), reinterpret_cast<u32x4*>(out + p.I));
   }

@@ -1168,7 +1168,7 @@ def rmsnorm_quant_1x128(x, gamma, residual=None, eps=1e-6, codes=True, with_y=Fa
 def rmsnorm_bwd(dn, h, gamma, rstd, dres=None, with_dgamma=True, stream=None):
     """Gradient of the norm of h (the x + residual that rmsnorm_quant_1x128
     gave, or x): (dx, dgamma), dx that of x and of the residual, dgamma f32
-    or None.  dres: the gradient of h's other uses."""
+    or None.  dres: the gradient of h's other uses.  Not recorded by autograd."""
     if stream is None:
         way = _ways.get("fp8bs_rmsnorm_bwd") or _way("fp8bs_rmsnorm_bwd", "fp8bs_rmsnorm_bwd_ws")
         outputs = way(dn, h, gamma, rstd, dres, with_dgamma, None)
@@ -1210,8 +1210,8 @@ def _row_outputs(out, rows, C, codes, with_y, device):
 def moe_gather(x, slot, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
     """Tokens' rows (bf16, or codes x with scales s_in) to their places: (q, s, y)
     with codes and scales, and BF16 rows where asked for (None otherwise).  out:
-    such a triple to write into; rows that no slot names are not written.  Its
-    gradient is moe_combine without weights."""
+    such a triple to write into; rows that no slot names are not written.  Not
+    recorded by autograd; the gradient is moe_combine without weights."""
     T, C = x.shape
     q, s, y = _row_outputs(out, slot.numel() if rows is None else rows, C, codes, with_y, x.device)
     fp8bs_moe_gather(SRC_BF16 if s_in is None else SRC_FP8_1x128, x, s_in, slot, q, s, y, stream)
@@ -1219,7 +1219,8 @@ def moe_gather(x, slot, s_in=None, rows=None, codes=True, with_y=False, out=None
 
 
 def moe_dispatch(x, ids, E, first=0, s_in=None, rows=None, codes=True, with_y=False, out=None, stream=None):
-    """moe_sort and moe_gather in one call: (q, s, y, offsets, slot)."""
+    """moe_sort and moe_gather in one call: (q, s, y, offsets, slot).  Not recorded by
+    autograd; the gradient of x is moe_combine without weights."""
     if stream is None:
         way = _ways.get("fp8bs_moe_dispatch") or _way("fp8bs_moe_dispatch", "fp8bs_moe_sort_ws")
         outputs = way(x, s_in, ids, E, first, rows, codes, with_y, out, None)
@@ -1257,7 +1258,8 @@ def moe_combine(y, slot, w=None, add=None, stream=None):
 def moe_combine_bwd(dout, slot, w, y=None, rows=None, codes=True, with_dy=False, out=None, stream=None):
     """Gradient of moe_combine: (q, s, dy, dw), the rows' gradient as codes with
     scales and in BF16 where asked for, and the weights' (with y) or None.  out:
-    (q, s, dy) to write into; rows that no slot names are not written."""
+    (q, s, dy) to write into; rows that no slot names are not written.  Not recorded
+    by autograd."""
     if stream is None:
         way = _ways.get("fp8bs_moe_combine_bwd") or _way("fp8bs_moe_combine_bwd")
         outputs = way(dout, slot, w, y, rows, codes, with_dy, out, None)
@@ -1277,7 +1279,7 @@ def moe_combine_bwd(dout, slot, w, y=None, rows=None, codes=True, with_dy=False,
 def swiglu_bwd_quant_1x128(dh, g, u, codes=True, with_d=False, with_h=False, stream=None):
     """Gradient of h = silu(g) u: (q, s, d, h), the gradients of g and u side by
     side [T][2I] as codes with scales and in BF16, and h itself, where asked for
-    (None otherwise)."""
+    (None otherwise).  Not recorded by autograd."""
     if stream is None:
         way = _ways.get("fp8bs_swiglu_bwd_quant_1x128") or _way("fp8bs_swiglu_bwd_quant_1x128")
         outputs = way(dh, g, u, codes, with_d, with_h, None)

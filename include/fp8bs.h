@@ -490,7 +490,9 @@ int64_t fp8bs_attn_paged_ws(int64_t B, int64_t T, int64_t max_q, int64_t Hq, int
  * At least one of q and y; q, s, y and rstd must not overlap the inputs.
  * T >= 0 (0 is a no-op), C > 0, C % 128 == 0 and C <= 16384, else FP8BS_ERR_UNSUPPORTED_SHAPE; eps > 0 and finite.  gamma
  * 16-byte aligned.  Rows whose sum of squares passes FP32's range (values near
- * 10^19) are outside the contract.
+ * 10^19) are outside the contract, as are NaN and infinite values: the codes and
+ * scales of such rows are unspecified (they may be zeros, a NaN leaves no trace in
+ * them), while h, y and rstd carry a NaN on.
  */
 fp8bs_status fp8bs_rmsnorm_quant_1x128(const void *x, int64_t ldx, const void *r, int64_t ldr,
                                        const void *gamma, fp8bs_out_dtype gt, float eps, int64_t T, int64_t C,
@@ -557,7 +559,8 @@ int64_t fp8bs_moe_sort_ws(int64_t T, int64_t k, int64_t E);
  *          and/or y.  FP8BS_SRC_FP8_1x128: x u8 [T][ldx] codes with s_in f32
  *          [T][lds_in]; outputs q with s.  Others are refused.
  *   slot   i32 [T][k] of fp8bs_moe_sort, in device memory and not checked: rows
- *          outside 0 .. M-1 are never followed
+ *          outside 0 .. M-1 are never followed; what a row holds that it names
+ *          twice is unspecified
  *   q, s   u8 [M][ldq], f32 [M][lds]   y bf16 [M][ldy] or NULL
  * Outputs must not overlap inputs.  Rows that no slot names are left as they
  * were.  Its gradient is fp8bs_moe_combine without weights.  T >= 0 (0 is a no-op), 0 < k <= 64, C > 0 and
@@ -602,7 +605,7 @@ fp8bs_status fp8bs_moe_combine(const void *y, fp8bs_out_dtype yt, int64_t ldy, i
  *   dw    f32 [T][lddw] or NULL      FP32 sums in a fixed order; 0 without a row
  *   y     bf16 or f32 [M][ldy] by yt; ignored (may be NULL) without dw
  * At least one output, none overlapping an input.  Rows that no slot names are left as
- * they were.  Sizes as for fp8bs_moe_combine.
+ * they were; slot names a row at most once.  Sizes as for fp8bs_moe_combine.
  */
 fp8bs_status fp8bs_moe_combine_bwd(const void *dout, int64_t lddo, const void *y, fp8bs_out_dtype yt, int64_t ldy,
                                    const int32_t *slot, const float *w, int64_t ldw, int64_t T, int64_t k,
@@ -620,7 +623,8 @@ fp8bs_status fp8bs_moe_combine_bwd(const void *dout, int64_t lddo, const void *y
  *   d     bf16 [T][ldd] or NULL      the same 2 I columns in BF16
  *   h     bf16 [T][ldh] or NULL      silu(g) u in BF16, as fp8bs_swiglu_quant_1x128 gives it
  * At least one output, none overlapping an input.  T >= 0 (0 is a no-op), I > 0 and
- * I % 128 == 0.  NaN and infinite inputs are outside the contract.
+ * I % 128 == 0.  NaN and infinite inputs are outside the contract, and so are products
+ * dh u past FP32's range.
  */
 fp8bs_status fp8bs_swiglu_bwd_quant_1x128(const void *dh, int64_t lddh, const void *g, int64_t ldg, const void *u,
                                           int64_t ldu, int64_t T, int64_t I, uint8_t *q, int64_t ldq, float *s,
